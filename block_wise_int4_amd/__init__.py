@@ -5,6 +5,7 @@ include/mnb.h); `block_wise_int4_amd.mnb` is its Python binding.
 """
 
 from .mnb import (  # noqa: F401
+    KvCache,
     MNB_F16,
     MNB_F32,
     MnbError,
@@ -12,6 +13,7 @@ from .mnb import (  # noqa: F401
     Plan,
     lib,
     mnb_abi_version,
+    mnb_cross_attn,
     mnb_dequant,
     mnb_gemm,
     mnb_gemm_i8,
@@ -20,8 +22,11 @@ from .mnb import (  # noqa: F401
     mnb_gemm_split_k_workspace_bytes,
     mnb_gemm_grouped,
     mnb_gemv,
+    mnb_kv_append,
+    mnb_kv_tables,
     mnb_pack,
     mnb_packed_bytes,
+    mnb_paged_attn,
     mnb_plan_grouped,
     mnb_quantize_act_i8,
     mnb_quantize_rtn,

@@ -1,0 +1,172 @@
+// Block tables and slot maps of a step, and the append of its keys and
+// values to the paged cache.
+#include "mnb_attn.h"
+#include "mnb_device.h"
+
+namespace mnb {
+
+// ---------------------------------------------------------------------------
+// Tables. With have = ceil(cached / P) and need = the blocks a request takes
+// now, everything a request or a token needs is a prefix sum over the
+// requests before it: of need (its place in the free list) and of added (its
+// first row). Every workgroup scans all requests itself, kScan at a time
+// (8 bytes per request out of cache: cheaper than a second launch), then
+// resolves its own share of the tokens and of the new table entries by
+// binary search in the scanned sums. A token's block is worked out from the
+// request's sums, never read back from an entry this launch writes, so
+// nothing orders the workgroups.
+// ---------------------------------------------------------------------------
+constexpr int kTabThreads = 256;
+constexpr int kTabPer = 4;                         // requests per thread and pass
+constexpr int kScan = kTabThreads * kTabPer;       // requests per pass
+constexpr int kTabTokens = 1024;                   // tokens per workgroup
+
+// Largest i < n with first[i] <= x (first[0] <= x; ascending).
+__device__ __forceinline__ int last_not_above(const int64_t *first, int n, int64_t x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) {
+    __shared__ int64_t s_start[kScan];   // first new row of each request of the pass
+    __shared__ int64_t s_off[kScan];     // its place in the free list
+    __shared__ int32_t s_cached[kScan];
+    __shared__ int64_t s_wave[2][kTabThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t limit = (int64_t)a.width * a.page;
+    const int64_t t0 = (int64_t)blockIdx.x * kTabTokens;
+    const int64_t t1 = t0 + kTabTokens < a.tokens ? t0 + kTabTokens : a.tokens;
+    int64_t rows_before = 0, blocks_before = 0;    // over the passes so far
+    for (int base = 0; base < a.batch; base += kScan) {
+        const int n = a.batch - base < kScan ? a.batch - base : kScan;
+        int32_t cached[kTabPer];
+        int64_t added[kTabPer], need[kTabPer], len[kTabPer];
+        int64_t sum_rows = 0, sum_blocks = 0;
+#pragma unroll
+        for (int i = 0; i < kTabPer; ++i) {
+            const int b = tid * kTabPer + i;
+            cached[i] = 0;
+            added[i] = need[i] = len[i] = 0;
+            if (b < n) {
+                const int32_t c = a.cached[base + b], d = a.added[base + b];
+                cached[i] = c > 0 ? c : 0;
+                added[i] = d > 0 ? d : 0;
+                len[i] = cached[i] + added[i];
+                if (len[i] > limit) len[i] = limit;
+                need[i] = (len[i] + a.page - 1) / a.page - ((int64_t)cached[i] + a.page - 1) / a.page;
+                if (need[i] < 0) need[i] = 0;
+            }
+            sum_rows += added[i];
+            sum_blocks += need[i];
+        }
+        // exclusive prefix over the workgroup's threads
+        int64_t in_rows = sum_rows, in_blocks = sum_blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t r = __shfl_up(in_rows, d), k = __shfl_up(in_blocks, d);
+            if (lane >= d) {
+                in_rows += r;
+                in_blocks += k;
+            }
+        }
+        if (lane == 63) {
+            s_wave[0][wave] = in_rows;
+            s_wave[1][wave] = in_blocks;
+        }
+        __syncthreads();
+        int64_t rows = rows_before + in_rows - sum_rows, blocks = blocks_before + in_blocks - sum_blocks;
+        int64_t all_rows = rows_before, all_blocks = blocks_before;
+#pragma unroll
+        for (int w = 0; w < kTabThreads / 64; ++w) {
+            if (w < wave) {
+                rows += s_wave[0][w];
+                blocks += s_wave[1][w];
+            }
+            all_rows += s_wave[0][w];
+            all_blocks += s_wave[1][w];
+        }
+#pragma unroll
+        for (int i = 0; i < kTabPer; ++i) {
+            const int b = tid * kTabPer + i;
+            if (b < n) {
+                s_start[b] = rows;
+                s_off[b] = blocks;
+                s_cached[b] = cached[i];
+                if (blockIdx.x == 0) {
+                    a.lens[base + b] = (int32_t)len[i];
+                    a.starts[base + b] = (int32_t)(rows < a.tokens ? rows : a.tokens);
+                }
+                rows += added[i];
+                blocks += need[i];
+            }
+        }
+        __syncthreads();
+        // new table entries, dealt over all threads of the launch
+        for (int64_t e = blocks_before + (int64_t)blockIdx.x * kTabThreads + tid; e < all_blocks;
+             e += (int64_t)gridDim.x * kTabThreads) {
+            const int b = last_not_above(s_off, n, e);
+            const int64_t have = ((int64_t)s_cached[b] + a.page - 1) / a.page;
+            a.table[(int64_t)(base + b) * a.width + have + (e - s_off[b])] = e < a.n_free ? a.free_blocks[e] : -1;
+        }
+        // this workgroup's tokens that belong to requests of this pass
+        const int64_t u0 = t0 > rows_before ? t0 : rows_before, u1 = t1 < all_rows ? t1 : all_rows;
+        for (int64_t t = u0 + tid; t < u1; t += kTabThreads) {
+            const int b = last_not_above(s_start, n, t);
+            const int64_t c = s_cached[b], pos = c + (t - s_start[b]);
+            const int64_t have = (c + a.page - 1) / a.page, place = pos / a.page;
+            int64_t id = -1;
+            if (pos < limit) {
+                if (place < have) id = a.table[(int64_t)(base + b) * a.width + place];
+                else if (s_off[b] + place - have < a.n_free) id = a.free_blocks[s_off[b] + place - have];
+            }
+            a.slots[t] = id < 0 ? -1 : id * a.page + (pos - place * a.page);
+        }
+        rows_before = all_rows;
+        blocks_before = all_blocks;
+        __syncthreads();
+    }
+    for (int64_t t = (t0 > rows_before ? t0 : rows_before) + tid; t < t1; t += kTabThreads) a.slots[t] = -1;
+    if (blockIdx.x == 0 && tid == 0) {
+        a.starts[a.batch] = (int32_t)(rows_before < a.tokens ? rows_before : a.tokens);
+        a.taken[0] = (int32_t)blocks_before;
+    }
+}
+
+hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t st) {
+    const int64_t wgs = (a.tokens + kTabTokens - 1) / kTabTokens;
+    kv_tables_kernel<<<(unsigned)(wgs < 1 ? 1 : wgs), kTabThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Append: a copy of 16-byte pieces, token rows in, page rows out.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
+    const int row_pieces = a.row_bytes / 16, pieces = a.heads * row_pieces;
+    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const int64_t slot = a.slots[t];
+        if (slot < 0 || slot / a.page >= a.num_blocks) continue;
+        const int64_t at = slot / a.page * a.block_stride + slot % a.page * a.token_stride;
+        for (int p = threadIdx.x; p < 2 * pieces; p += 256) {
+            const bool second = p >= pieces;
+            const int i = second ? p - pieces : p, h = i / row_pieces;
+            const int64_t to = at + h * a.head_stride + (i - h * row_pieces) * 16;
+            const uint8_t *from = second ? a.v + t * a.v_stride : a.k + t * a.k_stride;
+            *reinterpret_cast<u32x4 *>((second ? a.v_cache : a.k_cache) + to) =
+                *reinterpret_cast<const u32x4 *>(from + (int64_t)i * 16);
+        }
+    }
+}
+
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t st) {
+    const int64_t wgs = a.tokens < 65536 ? a.tokens : 65536;
+    kv_append_kernel<<<(unsigned)wgs, 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace mnb

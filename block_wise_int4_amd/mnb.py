@@ -42,7 +42,20 @@ class mnb_problem(ctypes.Structure):
                 ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
+class mnb_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class mnb_attn_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGNATURES = {
     "mnb_abi_version": (_int, []),
     "mnb_status_string": (ctypes.c_char_p, [_int]),
@@ -67,6 +80,13 @@ _SIGNATURES = {
     "mnb_plan_grouped_i8": (_int, [ctypes.POINTER(mnb_problem), _int, _int, _int, _int, _vp, _sz]),
     "mnb_plan_launches": (_int, [_vp]),
     "mnb_gemm_grouped": (_int, [_vp, _vp, _vp]),
+    "mnb_kv_tables": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mnb_kv_append": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mnb_paged_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
+    "mnb_paged_attn": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _vp, _sz, _vp, _vp]),
+    "mnb_cross_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "mnb_cross_attn": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _vp, _sz, _vp,
+                              _vp]),
 }
 
 
@@ -513,3 +533,201 @@ def mnb_gemm_i8(x, pw, workspace=None, y=None):
         _dev(x, "x"), _dev(pw.packed, "packed"), _dev(y, "y"), ws_ptr, ws_bytes, M, pw.N, pw.K, pw.bits,
         pw.block_size, dtype_code(pw.dtype), _stream(x.device)))
     return y
+
+
+def _on(device, **tensors):
+    """Every given tensor (None is skipped) is on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _rows(t, name, dims, dtype):
+    """A strided tensor of `dims` dimensions whose last one is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _strides(t):
+    """Strides of all dimensions but the last (0 where only one index is in
+    range, whatever the tensor says there)."""
+    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+
+
+class KvCache:
+    """One layer's paged key-value cache: k and v [blocks, kv_heads, page_size,
+    head_dim], float16 or float32, of the same strides (a cache laid out
+    [blocks, page_size, kv_heads, head_dim] is passed transposed). Keeps the
+    tensors and their description for the library."""
+
+    def __init__(self, k, v):
+        dtype_code(k.dtype)
+        _rows(k, "k", 4, k.dtype)
+        _rows(v, "v", 4, k.dtype)
+        if k.device.type != "cuda":
+            raise ValueError("k must be on the GPU")
+        _on(k.device, v=v)
+        if k.shape != v.shape or _strides(k) != _strides(v):
+            raise ValueError("k and v must have the same shape and strides")
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.num_blocks, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self._desc = mnb_kv_cache(k.data_ptr(), v.data_ptr(), *k.shape, *_strides(k), dtype_code(k.dtype), 0)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def new(cls, num_blocks, kv_heads, page_size, head_dim, dtype, device="cuda"):
+        """A cache of its own memory (not cleared: slots that nothing was
+        appended to are never read as keys)."""
+        shape = (num_blocks, kv_heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+def mnb_kv_tables(cached, added, free_blocks, block_table, page_size, slots, lens=None, starts=None, taken=None):
+    """Block tables and slot maps of a step: request b has cached[b] tokens in
+    the cache and gets added[b] more (int32 [B]). Its new entries of
+    block_table (int32 [B, max_blocks], updated in place) come from the front
+    of free_blocks (int32), in the order of the requests; slots (int64 [T])
+    receives the new tokens' places in the cache, -1 where there is none.
+    Returns (lens [B], starts [B + 1], slots, taken [1])."""
+    device, B = block_table.device, cached.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    if lens is None:
+        lens = torch.empty(B, dtype=torch.int32, device=device)
+    if starts is None:
+        starts = torch.empty(B + 1, dtype=torch.int32, device=device)
+    if taken is None:
+        taken = torch.empty(1, dtype=torch.int32, device=device)
+    width = block_table.shape[1]
+    for t, name, count in ((cached, "cached", B), (added, "added", B), (block_table, "block_table", B * width),
+                           (lens, "lens", B), (starts, "starts", B + 1), (taken, "taken", 1),
+                           (free_blocks, "free_blocks", free_blocks.numel())):
+        _check_buf(t, name, torch.int32, count, device)
+    _check_buf(slots, "slots", torch.int64, slots.numel(), device)
+    _check("mnb_kv_tables", lib().mnb_kv_tables(
+        _dev(cached, "cached"), _dev(added, "added"), _dev(free_blocks, "free_blocks"), free_blocks.numel(), B,
+        page_size, width, slots.numel(), _dev(block_table, "block_table"), _dev(lens, "lens"),
+        _dev(starts, "starts"), _dev(slots, "slots"), _dev(taken, "taken"), _stream(device)))
+    return lens, starts, slots, taken
+
+
+def mnb_kv_append(k, v, slots, cache):
+    """Write the keys and values of T tokens (k, v [T, kv_heads, head_dim] or
+    [T, kv_heads * head_dim], any token stride) to the cache's slots (int64
+    [T]; slots outside the cache are skipped)."""
+    T, row = slots.numel(), (cache.kv_heads, cache.head_dim)
+    _check_buf(slots, "slots", torch.int64, T, cache.device)
+    _on(cache.device, k=k, v=v)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dim() == 2 and t.shape[1] == row[0] * row[1]:
+            _rows(t, name, 2, cache.dtype)
+        elif tuple(t.shape[1:]) == row and (row[0] == 1 or t.stride(1) == row[1]):
+            _rows(t, name, 3, cache.dtype)
+        else:
+            raise ValueError(f"{name} must be [T, {row[0]}, {row[1]}] with contiguous tokens")
+        if t.shape[0] != T:
+            raise ValueError(f"{name} has {t.shape[0]} tokens, slots {T}")
+    _check("mnb_kv_append", lib().mnb_kv_append(
+        k.data_ptr(), v.data_ptr(), _strides(k)[0], _strides(v)[0], _dev(slots, "slots"), T, cache._ref,
+        _stream(cache.device)))
+
+
+def mnb_paged_attn_workspace_bytes(B, heads, cache, max_len):
+    """Workspace bytes mnb_paged_attn needs for B requests of `heads` query heads."""
+    return lib().mnb_paged_attn_workspace_bytes(B, heads, cache.kv_heads, cache.head_dim, max_len,
+                                                dtype_code(cache.dtype))
+
+
+def paged_attn_workspace(q, cache, max_len):
+    """A workspace for mnb_paged_attn (None when the call splits nothing)."""
+    nbytes = mnb_paged_attn_workspace_bytes(q.shape[0], q.shape[1], cache, max_len)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+
+
+def _workspace(t, device):
+    if t is None:
+        return None, 0
+    _on(device, workspace=t)
+    return _dev(t, "workspace"), t.numel() * t.element_size()
+
+
+def mnb_paged_attn(q, cache, block_table, lens, max_len, scale=None, workspace=None, out=None):
+    """Attention of each request's one new token, q [B, heads, head_dim] (any
+    request stride), over its first lens[b] (int32 [B], at most max_len)
+    positions of a paged cache through block_table (int32 [B, max_blocks]).
+    scale: 1 / sqrt(head_dim) unless given. Returns out [B, heads, head_dim]."""
+    device = cache.device
+    _rows(q, "q", 3, cache.dtype)
+    B, heads, dim = q.shape
+    if dim != cache.head_dim or (heads > 1 and q.stride(1) != dim):
+        raise ValueError(f"q must be [B, heads, {cache.head_dim}] with contiguous requests")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _on(device, q=q)
+    width = block_table.shape[1]
+    _check_buf(block_table, "block_table", torch.int32, B * width, device)
+    _check_buf(lens, "lens", torch.int32, B, device)
+    if out is None:
+        out = torch.empty((B, heads, dim), dtype=q.dtype, device=device)
+    _check_buf(out, "out", q.dtype, B * heads * dim, device)
+    if workspace is None:
+        workspace = paged_attn_workspace(q, cache, max_len)
+    ws, ws_bytes = _workspace(workspace, device)
+    _check("mnb_paged_attn", lib().mnb_paged_attn(
+        q.data_ptr(), _strides(q)[0], cache._ref, _dev(block_table, "block_table"), _dev(lens, "lens"), B, heads, width,
+        max_len, dim ** -0.5 if scale is None else scale, ws, ws_bytes, _dev(out, "out"), _stream(device)))
+    return out
+
+
+def mnb_cross_attn_workspace_bytes(B, queries, keys, heads, kv_heads, head_dim, dtype):
+    return lib().mnb_cross_attn_workspace_bytes(B, queries, keys, heads, kv_heads, head_dim, dtype_code(dtype))
+
+
+def cross_attn_workspace(q, k):
+    """A workspace for mnb_cross_attn (None when the call splits nothing)."""
+    nbytes = mnb_cross_attn_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3],
+                                            q.dtype)
+    return torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+
+
+def _view(t):
+    return mnb_attn_view(t.data_ptr(), *_strides(t))
+
+
+def mnb_cross_attn(q, k, v, lens=None, scale=None, workspace=None, out=None):
+    """Attention of q [B, Tq, heads, head_dim] over an encoder's states k, v
+    [B, Tk, kv_heads, head_dim] (any strides whose rows of head_dim are
+    contiguous), of which the first lens[b] (int32 [B]; None: all) are valid.
+    scale: 1 / sqrt(head_dim) unless given. Returns out, shaped as q."""
+    dtype_code(q.dtype)
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError("q must be on the GPU")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _rows(t, name, 4, q.dtype)
+    B, Tq, heads, dim = q.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != dim:
+        raise ValueError("k and v must be [B, Tk, kv_heads, head_dim] with q's B and head_dim")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    _rows(out, "out", 4, q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _on(device, k=k, v=v, out=out)
+    if lens is not None:
+        _check_buf(lens, "lens", torch.int32, B, device)
+    if workspace is None:
+        workspace = cross_attn_workspace(q, k)
+    ws, ws_bytes = _workspace(workspace, device)
+    _check("mnb_cross_attn", lib().mnb_cross_attn(
+        ctypes.byref(_view(q)), ctypes.byref(_view(k)), ctypes.byref(_view(v)),
+        None if lens is None else _dev(lens, "lens"), B, Tq, k.shape[1], heads, k.shape[2], dim,
+        dim ** -0.5 if scale is None else scale, dtype_code(q.dtype), ws, ws_bytes, ctypes.byref(_view(out)),
+        _stream(device)))
+    return out

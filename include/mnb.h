@@ -379,6 +379,140 @@ int mnb_plan_launches(const void *plan_host);
  */
 int mnb_gemm_grouped(const void *plan_host, const void *plan_device, void *stream);
 
+/*
+ * The decoder's attention, between the q/k/v products and the o product.
+ *
+ * The exports keep each layer's keys and values from step to step ("Qwen3-
+ * ASR-0.6B ONNX for the browser", section "Graph contracts": [28, 1, 8, S,
+ * 128]), and a Whisper decoder also attends to its encoder's states. Here the
+ * cache of one layer is a pool of fixed-size pages that requests of different
+ * lengths share. A decoding step is: mnb_kv_tables (once per step: which
+ * pages, which slots), then per layer mnb_kv_append (the step's new keys and
+ * values) and mnb_paged_attn (each request's one new token against its
+ * pages), and mnb_cross_attn where there is an encoder.
+ *
+ * Shared rules, on top of the conventions above:
+ *  - dtype is MNB_F32 or MNB_F16 for keys, values, queries and outputs alike.
+ *    Scores, softmax statistics and the sums over keys are float32; each
+ *    output is rounded once to dtype.
+ *  - head_dim is 64 or 128 (MNB_ERR_SHAPE otherwise). Hq query heads read Hkv
+ *    key-value heads, Hq a multiple of Hkv: query head h reads head
+ *    h / (Hq / Hkv).
+ *  - A result is softmax(scale * q . k) over the valid keys, times their
+ *    values. A row whose weights sum to zero (no valid key, or every score
+ *    -infinity) is zeros. Keys and values in places that are not valid are
+ *    ignored whatever they hold, infinities and NaN included; in valid
+ *    places they act as the formula says.
+ *  - Strides are in elements and not negative; rows of head_dim elements are
+ *    contiguous. Row addresses must be 16-byte aligned: data pointers, and
+ *    strides in bytes, are multiples of 16 (MNB_ERR_ALIGN otherwise).
+ *    Index arrays: int32 4-byte, int64 8-byte aligned.
+ *  - Results do not depend on what else runs: the same arguments give the
+ *    same bits.
+ */
+#define MNB_MAX_PAGE 1024          /* tokens per page                        */
+#define MNB_MAX_REQUESTS 65536     /* requests per call                      */
+#define MNB_MAX_KEYS (1LL << 30)   /* keys per request                       */
+
+/* One layer's paged key-value cache. Token `t % page_size` of head h in block
+ * `id` starts at k (and v) + id * block_stride + h * head_stride +
+ * (t % page_size) * token_stride, so [block][head][token][dim] and
+ * [block][token][head][dim] are both strides of the same description. */
+typedef struct mnb_kv_cache {
+    void *k, *v;             /* device, dtype; the same strides for both   */
+    int64_t num_blocks;      /* ids 0 .. num_blocks - 1                    */
+    int64_t kv_heads;
+    int64_t page_size;       /* tokens per block: a multiple of 16, up to
+                                MNB_MAX_PAGE                               */
+    int64_t head_dim;
+    int64_t block_stride, head_stride, token_stride; /* elements           */
+    int32_t dtype;           /* mnb_dtype                                  */
+    int32_t reserved;        /* 0                                          */
+} mnb_kv_cache;
+
+/*
+ * Block tables and slot maps of a step, from the requests' lengths, on the
+ * GPU. For request b < B: cached[b] tokens are in the cache, added[b] enter
+ * it now (negative counts act as 0). With P = page_size:
+ *   have = ceil(cached / P),  len = min(cached + added, max_blocks * P),
+ *   need = max(0, ceil(len / P) - have),
+ * its new entries block_table[b][have + i] (i < need) receive the free
+ * blocks free_blocks[off + i], off = the sum of need over the requests before
+ * b, or -1 past n_free. Other entries are left as they are.
+ *   lens[b]   = len: what mnb_paged_attn takes after the append.
+ *   starts[b] = the sum of added over the requests before b, cut to T
+ *               (starts has B + 1 entries, the last is the total): the new
+ *               tokens of request b are rows starts[b] .. starts[b + 1] - 1.
+ *   slots[t]  = block * P + offset of new token t, where mnb_kv_append puts
+ *               it; -1 for a token past its table's width, in a block that is
+ *               -1, and for t past the total. T entries.
+ *   taken[0]  = the sum of need: the caller drops that many blocks from the
+ *               front of its free list. More than n_free: the pool ran out,
+ *               and the entries and slots it could not give are -1.
+ * One launch; the same inputs give the same outputs, also when the call is
+ * repeated on its own result. free_blocks may be NULL when n_free is 0, slots
+ * when T is 0, and the per-request arrays when B is 0.
+ * All device; MNB_ERR_SHAPE: B > MNB_MAX_REQUESTS, page_size not a multiple
+ * of 16 up to MNB_MAX_PAGE, B * max_blocks above 2^31 - 1, max_blocks *
+ * page_size above MNB_MAX_KEYS.
+ */
+int mnb_kv_tables(const int32_t *cached, const int32_t *added, const int32_t *free_blocks, int64_t n_free,
+                  int64_t B, int64_t page_size, int64_t max_blocks, int64_t T, int32_t *block_table,
+                  int32_t *lens, int32_t *starts, int64_t *slots, int32_t *taken, void *stream);
+
+/*
+ * Write T tokens' keys and values into the cache: k, v device [T][kv_heads]
+ * [head_dim] with rows (tokens) k_stride and v_stride elements apart, token t
+ * to slot slots[t] (device int64 [T]; block = slot / page_size). Slots
+ * outside the cache (-1 among them) are skipped. Two tokens with one slot
+ * leave either's values there. T = 0 enqueues nothing.
+ */
+int mnb_kv_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, const int64_t *slots,
+                  int64_t T, const mnb_kv_cache *cache, void *stream);
+
+/*
+ * Attention of each request's one new token over its paged cache: q [B][Hq]
+ * [head_dim] (requests q_stride elements apart), block_table int32 [B]
+ * [max_blocks], lens int32 [B], out [B][Hq][head_dim] contiguous. Valid keys
+ * of request b: positions below min(lens[b], max_len, max_blocks *
+ * page_size) whose table entry names a block of the cache. max_len is the
+ * caller's bound on lens: it sizes the launch and the workspace.
+ *
+ * Long caches are split over workgroups, whose partial results (float32) go
+ * through `workspace` and are joined in a fixed order by a second launch:
+ * device, 16-byte aligned, at least mnb_paged_attn_workspace_bytes(...) bytes
+ * (0 where nothing is split; then it may be NULL), any contents, not shared
+ * by calls that may overlap. MNB_ERR_INVALID if workspace_bytes is smaller,
+ * or scale is not finite. B = 0 enqueues nothing.
+ */
+size_t mnb_paged_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t max_len,
+                                      int dtype);
+int mnb_paged_attn(const void *q, int64_t q_stride, const mnb_kv_cache *cache, const int32_t *block_table,
+                   const int32_t *lens, int64_t B, int64_t Hq, int64_t max_blocks, int64_t max_len, float scale,
+                   void *workspace, size_t workspace_bytes, void *out, void *stream);
+
+/* A [batch][row][head][head_dim] tensor by its strides (elements). */
+typedef struct mnb_attn_view {
+    void *data;              /* device, dtype                              */
+    int64_t batch_stride, row_stride, head_stride;
+} mnb_attn_view;
+
+/*
+ * Cross attention: Tq query rows of each of B requests against the Tk rows
+ * of its encoder's states (no causal mask). q, out: [B][Tq][Hq][head_dim];
+ * k, v: [B][Tk][Hkv][head_dim], each by its strides (a batch stride of 0
+ * shares one encoder's states among the requests). lens: device int32 [B],
+ * how many rows of each request are valid (cut to 0 .. Tk), or NULL for all.
+ * Tq = 1 is the single-token form. workspace as in mnb_paged_attn, of
+ * mnb_cross_attn_workspace_bytes(...) bytes. B = 0 or Tq = 0 enqueues
+ * nothing; Tk = 0 gives zeros.
+ */
+size_t mnb_cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
+                                      int64_t head_dim, int dtype);
+int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_attn_view *v, const int32_t *lens,
+                   int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t head_dim, float scale,
+                   int dtype, void *workspace, size_t workspace_bytes, const mnb_attn_view *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

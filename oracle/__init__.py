@@ -43,6 +43,11 @@ notes. The functions and what pins each one (tests/test_oracle_pins.py):
                       blocks, round-trip bound
   matmul_nbits_i8     pinned: equality with matmul_nbits where the int8
                       activations are exact, Fraction-exact tiny shapes
+  kv_tables, attend,
+  paged_attention,
+  cross_attention     (attn_oracle, the decoder's attention) pinned in
+                      tests/test_attn_oracle.py: worked tables, closed forms
+                      of the softmax, equality of the paged and plain forms
 """
 
 from .mnb_oracle import (  # noqa: F401
@@ -66,4 +71,11 @@ from .mnb_oracle import (  # noqa: F401
     A8_QMAX,
     quantize_activations_i8,
     matmul_nbits_i8,
+)
+from .attn_oracle import (  # noqa: F401
+    attend,
+    cross_attention,
+    kv_tables,
+    paged_attention,
+    paged_rows,
 )
