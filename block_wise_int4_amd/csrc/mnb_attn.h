@@ -9,6 +9,7 @@ namespace mnb {
 // Keys a K or V tile shares a block-table entry over: pages hold a whole
 // number of these.
 constexpr int kPageGranule = 16;
+constexpr int64_t kMaxKeyStride = 1LL << 26;
 
 // A step's block tables and slot maps (mnb_kv_tables).
 struct KvTablesArgs {
@@ -35,7 +36,8 @@ hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t st);
 // Attention of `rows` query rows per (request, key-value head) over keys that
 // are paged (table not NULL: the batch strides of K and V step over blocks)
 // or one run per request. Row r is query token r / group, query head
-// kv_head * group + r % group. Strides in elements.
+// kv_head * group + r % group. Strides in elements; k_row and v_row at most
+// kMaxKeyStride (16 rows are addressed from one base with 32-bit offsets).
 struct AttnArgs {
     const void *q, *k, *v;
     void *out;

@@ -38,6 +38,7 @@ int check_cache(const mnb_kv_cache *c) {
         !page_ok(c->page_size) || (c->head_dim != 64 && c->head_dim != 128))
         return MNB_ERR_SHAPE;
     if (int st = check_strides(c->block_stride, c->head_stride, c->token_stride, c->dtype)) return st;
+    if (c->token_stride > kMaxKeyStride) return MNB_ERR_SHAPE;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return MNB_ERR_ALIGN;
     return c->reserved == 0 ? MNB_OK : MNB_ERR_INVALID;
 }
@@ -185,6 +186,7 @@ int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_att
     if (int st = check_heads(B, Tq, Tk, Hq, Hkv, head_dim, dtype)) return st;
     for (const mnb_attn_view *t : {q, k, v, out})
         if (int st = check_strides(t->batch_stride, t->row_stride, t->head_stride, dtype)) return st;
+    if (k->row_stride > kMaxKeyStride || v->row_stride > kMaxKeyStride) return MNB_ERR_SHAPE;
     if (!isfinite(scale)) return MNB_ERR_INVALID;
     if (B == 0 || Tq == 0) return MNB_OK;
     if (!q->data || !out->data || (Tk > 0 && (!k->data || !v->data))) return MNB_ERR_NULL;

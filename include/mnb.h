@@ -403,8 +403,8 @@ int mnb_gemm_grouped(const void *plan_host, const void *plan_device, void *strea
  *    -infinity) is zeros. Keys and values in places that are not valid are
  *    ignored whatever they hold, infinities and NaN included; in valid
  *    places they act as the formula says.
- *  - Strides are in elements and not negative; rows of head_dim elements are
- *    contiguous. Row addresses must be 16-byte aligned: data pointers, and
+ *  - Strides are in elements and not negative; from one key (or value) row to
+ *    the next at most 2^26. Rows of head_dim elements are contiguous. Row addresses must be 16-byte aligned: data pointers, and
  *    strides in bytes, are multiples of 16 (MNB_ERR_ALIGN otherwise).
  *    Index arrays: int32 4-byte, int64 8-byte aligned.
  *  - Results do not depend on what else runs: the same arguments give the
