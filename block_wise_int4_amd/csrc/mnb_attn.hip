@@ -2,11 +2,10 @@
 // per request): o = sum_t w_t V[t] / sum_t w_t, w_t = exp(s_t - m), s_t =
 // scale * q . K[t], with a reference m kept near the running maximum.
 //
-// Work: keys are cut into chunks; one workgroup takes up to 16 query rows of
-// one (request, key-value head) over one chunk, its waves every kWaves-th
-// tile of 16 or 32 keys. A wave streams its tiles from memory straight into
-// the registers that the matrix instructions read (no LDS, no barrier), the
-// next tile in flight while one is computed:
+// Work: a row is up to 16 query rows of one (request, key-value head); its
+// keys are cut into chunks, and a chunk's tiles of 16 or 32 keys are taken in
+// turn by the waves of one workgroup. A wave streams its tiles from memory
+// straight into the registers that the matrix instructions read (no LDS):
 //   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row), B = queries;
 //                 the result holds, per lane, four keys 4 (l / 16) + i of one
 //                 query l % 16, which is already the B operand's layout of
@@ -16,6 +15,11 @@
 //                 piece element e of lane row m is dimension m * (D / 16) + e:
 //                 float32 needs no shuffle at all, float16 one byte permute
 //                 per pair of keys.
+// The next tile's keys are requested as soon as the first product has read
+// this one's, its values after the second: one tile of registers, something
+// always in flight, three workgroups per CU. The code is kept small on
+// purpose: a wave of a short row executes most of it once, out of a cold
+// instruction cache.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
 #include "mnb_attn.h"
 #include "mnb_device.h"
@@ -25,7 +29,8 @@ namespace mnb {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kQ = 16;                      // query rows per workgroup
+constexpr int kOneUnits = 256;
+constexpr int kQ = 16;                      // query rows per row of tiles
 constexpr float kLowest = -3.402823466e38f; // the reference before any key
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -35,7 +40,7 @@ template <int Bytes> struct Piece;
 template <> struct Piece<16> { typedef u32x4 type; };
 template <> struct Piece<8> { typedef u32x2 type; };
 
-// Registers of one tile of 16 * NS keys of a float16 or float32 row of D.
+// Registers of one tile of keys of a float16 or float32 row of D.
 template <typename T, int D> struct TileShape {
     static constexpr int kRow = D * (int)sizeof(T);                 // bytes
     static constexpr int kSub = sizeof(T) == 4 && D == 128 ? 1 : 2; // 16-key parts (64 registers of K and V at D = 128)
@@ -44,13 +49,6 @@ template <typename T, int D> struct TileShape {
     static constexpr int kVBytes = kRow / 16 < 16 ? kRow / 16 : 16;
     static constexpr int kV = kRow / 16 / kVBytes;                  // pieces of a V row per lane
     static constexpr int kOut = D / 16;                             // 16-dimension parts of the output
-};
-
-template <typename T, int D> struct Tile {
-    using S = TileShape<T, D>;
-    u32x4 k[S::kSub][S::kK];
-    typename Piece<S::kVBytes>::type v[S::kSub][4][S::kV];
-    int valid[S::kSub];   // leading valid keys of each part
 };
 
 // Scores are kept as x = s * mul, weights are exp2 of differences: float16
@@ -68,101 +66,157 @@ template <typename T> __device__ __forceinline__ float weight(float x, float ref
 __device__ __forceinline__ f4 mma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma4(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-__device__ __forceinline__ int64_t keys_of(const AttnArgs &a, int64_t b) {
-    int64_t n = a.max_len;
+// A load that leaves no copy in the caches it passes (STREAM), for caches of
+// keys and values larger than those.
+template <bool STREAM, typename V> __device__ __forceinline__ V fetch(const uint8_t *p) {
+    const V *from = reinterpret_cast<const V *>(p);
+    if constexpr (STREAM) return __builtin_nontemporal_load(from);
+    else return *from;
+}
+
+__device__ __forceinline__ int keys_of(const AttnArgs &a, int64_t b) {
+    int n = a.max_len;
     if (a.lens && a.lens[b] < n) n = a.lens[b];
-    if (a.table && n > (int64_t)a.table_width * a.page) n = (int64_t)a.table_width * a.page;
     return n;
+}
+
+// Query token of a query row (a decoding step has one, and no division).
+__device__ __forceinline__ int token_of(const AttnArgs &a, int row) {
+    return a.rows == a.group ? 0 : (int)((uint32_t)row / (uint32_t)a.group);
+}
+
+// Four outputs from dimension d on of a query row.
+template <typename T>
+__device__ __forceinline__ void store_out(const AttnArgs &a, int64_t b, int h, int row, int d, f4 sum, float total) {
+    const int token = token_of(a, row);
+    T *out = static_cast<T *>(a.out) + b * a.o_batch + token * a.o_row +
+             (int64_t)(h * a.group + row - token * a.group) * a.o_head + d;
+    sum *= total == 0.0f ? 0.0f : 1.0f / total;
+    if constexpr (sizeof(T) == 2) {
+        const u32x2 w = {as_u32(h2{(_Float16)sum.x, (_Float16)sum.y}), as_u32(h2{(_Float16)sum.z, (_Float16)sum.w})};
+        *reinterpret_cast<u32x2 *>(out) = w;
+    } else {
+        *reinterpret_cast<f4 *>(out) = sum;
+    }
 }
 
 }  // namespace
 
-// Partial results of a split launch: per (request, head, row, chunk) D sums,
-// then per the same the reference and the weights' sum.
+// How a launch is cut. Pieces of rows of more than one chunk: per (request,
+// head, query row, chunk) D sums, and a reference and the weights' sum.
 struct AttnSplit {
-    int32_t chunk;      // keys per chunk (a multiple of kWaves tiles)
-    int32_t chunks;     // of max_len
-    int32_t q_tiles;    // of `rows`
+    int32_t chunk;        // keys per chunk
+    int32_t chunks;       // of max_len
+    int32_t q_tiles, held;   // of `rows`; min(rows, kQ)
     uint64_t page_magic;  // ceil(2^32 / (page / 16)): (part * magic) >> 32 = part / (page / 16) for part < 2^26
     float *sums, *stats;
 };
 
-template <typename T, int D, bool PAGED>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSplit sp) {
+// ONE: rows of at most a tile per wave, up to 16 waves; otherwise kWaves.
+template <typename T, int D, bool PAGED, bool STREAM, bool ONE>
+__global__ __launch_bounds__(ONE ? 1024 : 64 * kWaves, ONE || D * (int)sizeof(T) <= 128 ? 4 : 3)
+void attn_kernel(AttnArgs a, AttnSplit sp) {
+    constexpr int kMost = ONE ? 16 : kWaves;
     using S = TileShape<T, D>;
-    __shared__ float s_o[kWaves][kQ][D + 4];
-    __shared__ float s_m[kWaves][kQ], s_l[kWaves][kQ];
+    typedef typename Piece<S::kVBytes>::type VP;
+    extern __shared__ __attribute__((aligned(16))) float s_o[];   // [waves][held][D + 4]
+    __shared__ float s_m[kMost][kQ], s_l[kMost][kQ];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    uint32_t id = blockIdx.x;
-    const int chunk = id % sp.chunks;
-    id /= sp.chunks;
-    const int q_tile = id % sp.q_tiles;
-    id /= sp.q_tiles;
-    const int h = id % a.kv_heads;
-    const int64_t b = id / a.kv_heads;
-    const int n = (int)keys_of(a, b);
+    // the head varies fastest, the chunk slowest: blocks go to the XCDs in
+    // turn, and the late chunks that only long requests have spread over all
+    // of them
+    const int h = blockIdx.x;
+    const int64_t b = blockIdx.y;
+    int chunk = blockIdx.z, q_tile = 0;
+    if (sp.q_tiles > 1) {
+        chunk = blockIdx.z / sp.q_tiles;
+        q_tile = blockIdx.z - chunk * sp.q_tiles;
+    }
     const int begin = chunk * sp.chunk;
+    int key = begin + wave * S::kKeys;
+    const int32_t *table = PAGED ? a.table + b * a.table_width : nullptr;
+
+    // The table entries of the tile at key0 (past the table's end its last
+    // entry, which is not used).
+    int32_t ids[S::kSub];
+    auto look_up = [&](int key0) {
+        if constexpr (PAGED) {
+#pragma unroll
+            for (int s = 0; s < S::kSub; ++s) {
+                const uint32_t place = (uint32_t)((((uint32_t)key0 >> 4) + s) * sp.page_magic >> 32);
+                ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
+            }
+        }
+    };
+    look_up(key);
+    const int n = keys_of(a, b);
     if (begin >= n && chunk > 0) return;
-    const int end = n - begin < sp.chunk ? n : begin + sp.chunk;   // (n may be <= 0: nothing below runs)
+    const int end = n - begin < sp.chunk ? n : begin + sp.chunk;   // (n may be <= 0: no tile then)
     const int rows = a.rows - q_tile * kQ < kQ ? a.rows - q_tile * kQ : kQ;
 
     // queries: lane (query col, dimensions of its group g of each 64-byte run)
     u32x4 q[S::kK];
     {
-        const int r = q_tile * kQ + (col < rows ? col : 0);
-        const T *src = static_cast<const T *>(a.q) + b * a.q_batch + (int64_t)(r / a.group) * a.q_row +
-                       (int64_t)(h * a.group + r % a.group) * a.q_head;
+        const int r = q_tile * kQ + (col < rows ? col : 0), token = token_of(a, r);
+        const T *src = static_cast<const T *>(a.q) + b * a.q_batch + token * a.q_row +
+                       (int64_t)(h * a.group + r - token * a.group) * a.q_head;
         const uint8_t *p = reinterpret_cast<const uint8_t *>(src) + g * 16;
 #pragma unroll
         for (int j = 0; j < S::kK; ++j) q[j] = *reinterpret_cast<const u32x4 *>(p + j * 64);
     }
+
+    // One tile: keys, values, and where the next one is. Every address stays
+    // inside the cache: parts without a valid key read block 0 (or the
+    // request's first row), rows past the last valid key read that key's row.
+    u32x4 k[S::kSub][S::kK];
+    VP v[S::kSub][4][S::kV];
+    int valid[S::kSub];   // leading valid keys of each part
+    int64_t from_k[S::kSub], from_v[S::kSub];
     const uint8_t *kp = static_cast<const uint8_t *>(a.k) + h * a.k_head * (int64_t)sizeof(T);
     const uint8_t *vp = static_cast<const uint8_t *>(a.v) + h * a.v_head * (int64_t)sizeof(T);
-    const int64_t k_batch = a.k_batch * (int64_t)sizeof(T), v_batch = a.v_batch * (int64_t)sizeof(T);
     const uint32_t k_row = (uint32_t)a.k_row * sizeof(T), v_row = (uint32_t)a.v_row * sizeof(T);
-    const int32_t *table = PAGED ? a.table + b * a.table_width : nullptr;
-    const int per_page = PAGED ? a.page >> 4 : 1;
-
-    // Loads a tile's keys and values. Every address stays inside the cache:
-    // parts without a valid key read block 0 (or the request's first row),
-    // rows past the last valid key read that key's row.
-    auto load = [&](Tile<T, D> &t, int key0) {
+    auto locate = [&](int key0, int *valid) {
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
             const int first = key0 + 16 * s;
-            int valid = end - first;
-            valid = valid < 0 ? 0 : valid > 16 ? 16 : valid;
-            int64_t kb = 0, vb = 0;
+            int ok = end - first;
+            ok = ok < 0 ? 0 : ok > 16 ? 16 : ok;
+            int64_t row = first, of = b;
             if constexpr (PAGED) {
-                int id = 0, within = 0;
-                if (valid > 0) {
-                    const uint32_t part = (uint32_t)first >> 4;
-                    const uint32_t place = (uint32_t)((part * sp.page_magic) >> 32);
-                    within = (int)(part - place * per_page) << 4;
-                    id = table[place];
-                    if (id < 0 || id >= a.num_blocks) id = within = valid = 0;
-                }
-                kb = id * k_batch + (int64_t)within * k_row;
-                vb = id * v_batch + (int64_t)within * v_row;
-            } else {
-                const int from = valid > 0 ? first : 0;
-                kb = b * k_batch + (int64_t)from * k_row;
-                vb = b * v_batch + (int64_t)from * v_row;
+                of = ids[s];
+                if (of < 0 || of >= a.num_blocks) ok = 0;
+                const uint32_t part = (uint32_t)first >> 4;
+                row = (int)(part - (uint32_t)(part * sp.page_magic >> 32) * (a.page >> 4)) << 4;
             }
-            t.valid[s] = valid;
-            const int last = valid > 0 ? valid - 1 : 0;
-            const uint8_t *ks = kp + kb, *vs = vp + vb;
-            const uint32_t ko = (uint32_t)(col < last ? col : last) * k_row + g * 16;
+            if (ok == 0) {
+                row = 0;
+                of = PAGED ? 0 : b;
+            }
+            valid[s] = ok;
+            from_k[s] = (of * a.k_batch + row * a.k_row) * (int64_t)sizeof(T);
+            from_v[s] = (of * a.v_batch + row * a.v_row) * (int64_t)sizeof(T);
+        }
+    };
+    auto load_k = [&](const int *valid) {
 #pragma unroll
-            for (int j = 0; j < S::kK; ++j) t.k[s][j] = *reinterpret_cast<const u32x4 *>(ks + ko + j * 64);
+        for (int s = 0; s < S::kSub; ++s) {
+            const int last = valid[s] > 0 ? valid[s] - 1 : 0;
+            const uint32_t at = (uint32_t)(col < last ? col : last) * k_row + g * 16;
+#pragma unroll
+            for (int j = 0; j < S::kK; ++j) k[s][j] = fetch<STREAM, u32x4>(kp + from_k[s] + at + j * 64);
+        }
+    };
+    auto load_v = [&](const int *valid) {
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s) {
+            const int last = valid[s] > 0 ? valid[s] - 1 : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = 4 * g + i;
-                const uint32_t vo = (uint32_t)(key < last ? key : last) * v_row + col * S::kVBytes;
+                const int r = 4 * g + i;
+                const uint32_t at = (uint32_t)(r < last ? r : last) * v_row + col * S::kVBytes;
 #pragma unroll
-                for (int c = 0; c < S::kV; ++c)
-                    t.v[s][i][c] = *reinterpret_cast<const typename Piece<S::kVBytes>::type *>(vs + vo + c * 256);
+                for (int c = 0; c < S::kV; ++c) v[s][i][c] = fetch<STREAM, VP>(vp + from_v[s] + at + c * 256);
             }
         }
     };
@@ -176,7 +230,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
     // passes it by more than that
     const float slack = sizeof(T) == 4 ? 5.5f : 8.0f;
 
-    auto compute = [&](Tile<T, D> &t) {
+    const int step = kWaves * S::kKeys;
+    if (key < end) {
+        locate(key, valid);
+        load_k(valid);
+        load_v(valid);
+        if constexpr (!ONE) look_up(key + step);
+    }
+    for (; key < end; key += step) {
         float x[S::kSub][4];
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
@@ -184,9 +245,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
 #pragma unroll
             for (int j = 0; j < S::kK; ++j) {
                 if constexpr (sizeof(T) == 2) {
-                    c = mma16(__builtin_bit_cast(h8, t.k[s][j]), __builtin_bit_cast(h8, q[j]), c);
+                    c = mma16(__builtin_bit_cast(h8, k[s][j]), __builtin_bit_cast(h8, q[j]), c);
                 } else {
-                    const f4 kk = __builtin_bit_cast(f4, t.k[s][j]), qq = __builtin_bit_cast(f4, q[j]);
+                    const f4 kk = __builtin_bit_cast(f4, k[s][j]), qq = __builtin_bit_cast(f4, q[j]);
                     c = mma4(kk.x, qq.x, c);
                     c = mma4(kk.y, qq.y, c);
                     c = mma4(kk.z, qq.z, c);
@@ -195,16 +256,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[s][i] = c[i] * mul;
-            if (t.valid[s] < 16) {   // uniform: the end of a row, or a missing block
+        }
+        int valid_next[S::kSub];
+        if constexpr (!ONE) {
+            locate(key + step, valid_next);
+            load_k(valid_next);
+            look_up(key + 2 * step);
+        }
+        bool partial = false;
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s) partial |= valid[s] < 16;
+        if (partial) {   // uniform: the end of a row, or a missing block
+#pragma unroll
+            for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool on = 4 * g + i < t.valid[s];
+                    const bool on = 4 * g + i < valid[s];
                     x[s][i] = on ? x[s][i] : -__builtin_inff();
 #pragma unroll
-                    for (int c2 = 0; c2 < S::kV; ++c2)
-                        t.v[s][i][c2] = on ? t.v[s][i][c2] : typename Piece<S::kVBytes>::type(0u);
+                    for (int c = 0; c < S::kV; ++c) v[s][i][c] = on ? v[s][i][c] : VP(0u);
                 }
-            }
         }
         float top = x[0][0];
 #pragma unroll
@@ -221,13 +292,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
 #pragma unroll
             for (int i = 0; i < S::kOut; ++i) o[i] *= keep;
         }
-        float p[S::kSub][4];
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[s][i] = weight<T>(x[s][i], ref);
-                l += p[s][i];
+                x[s][i] = weight<T>(x[s][i], ref);
+                l += x[s][i];
             }
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -236,9 +306,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int c = 0; c < S::kV; ++c) {
-                        const f4 vv = __builtin_bit_cast(f4, t.v[s][i][c]);
+                        const f4 vv = __builtin_bit_cast(f4, v[s][i][c]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[4 * c + e] = mma4(vv[e], p[s][i], o[4 * c + e]);
+                        for (int e = 0; e < 4; ++e) o[4 * c + e] = mma4(vv[e], x[s][i], o[4 * c + e]);
                     }
         } else {
             // the weights as a float16 pair hi + lo (22 bits): the stream
@@ -248,145 +318,184 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(AttnArgs a, AttnSp
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const _Float16 w = (_Float16)p[s][i];
+                    const _Float16 w = (_Float16)x[s][i];
                     hi[4 * s + i] = w;
-                    lo[4 * s + i] = (_Float16)(p[s][i] - (float)w);
+                    lo[4 * s + i] = (_Float16)(x[s][i] - (float)w);
                 }
 #pragma unroll
             for (int e = 0; e < S::kOut; ++e) {
                 u32x4 w;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const auto &v0 = t.v[j >> 1][2 * (j & 1)][0], &v1 = t.v[j >> 1][2 * (j & 1) + 1][0];
+                    const VP &v0 = v[j >> 1][2 * (j & 1)][0], &v1 = v[j >> 1][2 * (j & 1) + 1][0];
                     w[j] = __builtin_amdgcn_perm(v1[e >> 1], v0[e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
                 }
                 o[e] = mma16(__builtin_bit_cast(h8, w), hi, o[e]);
                 o[e] = mma16(__builtin_bit_cast(h8, w), lo, o[e]);
             }
         }
-    };
+        if constexpr (ONE) break;
+        load_v(valid_next);
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s) valid[s] = valid_next[s];
+    }
 
-    const int step = kWaves * S::kKeys;
-    int key = begin + wave * S::kKeys;
-    if (key < end) {
-        Tile<T, D> t0, t1;
-        load(t0, key);
-        for (; key < end; key += 2 * step) {
-            load(t1, key + step);
-            compute(t0);
-            if (key + step >= end) break;
-            load(t0, key + 2 * step);
-            compute(t1);
+    // join the waves (those that have keys)
+    const int tiles = n <= S::kKeys ? 1 : (end - begin + S::kKeys - 1) / S::kKeys;
+    const int waves = tiles < (int)(blockDim.x >> 6) ? tiles : blockDim.x >> 6;
+    if (wave < waves) {
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (g == 0) {
+            s_m[wave][col] = ref;
+            s_l[wave][col] = l;
         }
-    }
-
-    // join the waves
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (g == 0) {
-        s_m[wave][col] = ref;
-        s_l[wave][col] = l;
-    }
-    if (col < rows) {
+        if (col < rows) {
+            // a lane's part e, row m = 4 g + i is dimension m * (D / 16) + e
+            // (float16), 64 * (e / 4) + 4 m + e % 4 (float32)
+            float *to = s_o + (wave * sp.held + col) * (D + 4);
 #pragma unroll
-        for (int e = 0; e < S::kOut; ++e)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // row 4 g + i of part e (float16: element e of a lane's piece;
-                // float32: element e % 4 of its piece e / 4)
-                const int m = 4 * g + i;
-                const int d = sizeof(T) == 2 ? m * S::kOut + e : 64 * (e >> 2) + 4 * m + (e & 3);
-                s_o[wave][col][d] = o[e][i];
-            }
+                for (int e = 0; e < S::kOut; e += 4)
+                    *reinterpret_cast<f4 *>(to + (sizeof(T) == 2 ? (4 * g + i) * S::kOut + e : 16 * e + 4 * (4 * g + i))) =
+                        f4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
+        }
     }
     __syncthreads();
     const bool whole = n <= sp.chunk;   // this chunk is the row's only one
-    const int64_t row0 = ((b * a.kv_heads + h) * a.rows + q_tile * kQ);
-    for (int e = threadIdx.x; e < rows * D; e += 64 * kWaves) {
-        const int r = e / D, d = e % D;
+    for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = s_m[0][r];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][r]);
-        float sum = 0.0f, total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 1; w < waves; ++w) m = fmaxf(m, s_m[w][r]);
+        f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        float total = 0.0f;
+        for (int w = 0; w < waves; ++w) {
             const float f = weight<T>(s_m[w][r], m);
-            sum += s_o[w][r][d] * f;
+            sum += *reinterpret_cast<const f4 *>(s_o + (w * sp.held + r) * (D + 4) + d) * f;
             total += s_l[w][r] * f;
         }
         if (whole) {
-            const int row = q_tile * kQ + r;
-            T *out = static_cast<T *>(a.out) + b * a.o_batch + (int64_t)(row / a.group) * a.o_row +
-                     (int64_t)(h * a.group + row % a.group) * a.o_head;
-            out[d] = Io<T>::from_f32(total == 0.0f ? 0.0f : sum / total);
+            store_out<T>(a, b, h, q_tile * kQ + r, d, sum, total);
         } else {
-            const int64_t at = (row0 + r) * sp.chunks + chunk;
-            sp.sums[at * D + d] = sum;
+            const int64_t piece = ((b * a.kv_heads + h) * a.rows + q_tile * kQ + r) * sp.chunks + chunk;
+            *reinterpret_cast<f4 *>(sp.sums + piece * D + d) = sum;
             if (d == 0) {
-                sp.stats[2 * at] = m;
-                sp.stats[2 * at + 1] = total;
+                sp.stats[2 * piece] = m;
+                sp.stats[2 * piece + 1] = total;
             }
         }
     }
 }
 
-// Joins the chunks of one query row, in their order.
+// Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
+// D / 4 lanes, which take every 2^shift-th chunk; then their sums are added.
+// (Small and without a division: the launch is as long as its latencies.)
+constexpr int kJoin = 256;
 template <typename T, int D>
-__global__ __launch_bounds__(D) void attn_join_kernel(AttnArgs a, AttnSplit sp) {
-    uint32_t id = blockIdx.x;
-    const int row = id % a.rows;
-    const int h = id / a.rows % a.kv_heads;
-    const int64_t b = id / a.rows / a.kv_heads;
-    const int n = (int)keys_of(a, b);
-    if (n <= sp.chunk) return;
-    const int chunks = (n + sp.chunk - 1) / sp.chunk;
-    const float *stats = sp.stats + 2 * (int64_t)id * sp.chunks;
-    const float *sums = sp.sums + (int64_t)id * sp.chunks * D;
-    float m = stats[0];
-    for (int c = 1; c < chunks; ++c) m = fmaxf(m, stats[2 * c]);
-    float sum = 0.0f, total = 0.0f;
-    for (int c = 0; c < chunks; ++c) {
-        const float f = weight<T>(stats[2 * c], m);
-        sum += sums[(int64_t)c * D + threadIdx.x] * f;
-        total += stats[2 * c + 1] * f;
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, AttnSplit sp, int shift) {
+    constexpr int kLanes = D / 4, kLaneBits = D == 128 ? 5 : 4;
+    __shared__ f4 s_sum[kJoin];
+    __shared__ float s_m[kJoin], s_l[kJoin];
+    const int tid = threadIdx.x, d = tid % kLanes * 4, groups = 1 << shift;
+    const int group = (tid >> kLaneBits) & (groups - 1);
+    const int row = blockIdx.z * (kJoin >> (kLaneBits + shift)) + (tid >> (kLaneBits + shift));
+    const int h = blockIdx.x;
+    const int64_t b = blockIdx.y;
+    const int n = keys_of(a, b);
+    const bool on = row < a.rows;
+    const int64_t first = ((b * a.kv_heads + h) * a.rows + (on ? row : 0)) * sp.chunks;
+    f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kLowest, l = 0.0f;
+    // (the first place of every group is read whatever the length, so that
+    // nothing waits for it; absent chunks are left out)
+    for (int c = group; c < sp.chunks; c += groups) {
+        const float *stats = sp.stats + 2 * (first + c);
+        float pm = stats[0], pl = stats[1];
+        f4 ps = *reinterpret_cast<const f4 *>(sp.sums + (first + c) * D + d);
+        if (c * sp.chunk >= n) break;
+        const float to = fmaxf(m, pm), keep = weight<T>(m, to), f = weight<T>(pm, to);
+        sum = sum * keep + ps * f;
+        l = l * keep + pl * f;
+        m = to;
     }
-    T *out = static_cast<T *>(a.out) + b * a.o_batch + (int64_t)(row / a.group) * a.o_row +
-             (int64_t)(h * a.group + row % a.group) * a.o_head;
-    out[threadIdx.x] = Io<T>::from_f32(total == 0.0f ? 0.0f : sum / total);
+    s_sum[tid] = sum;
+    s_m[tid] = m;
+    s_l[tid] = l;
+    __syncthreads();
+    if (group != 0 || !on || n <= sp.chunk) return;
+    for (int g = 1; g < groups; ++g) {
+        const int from = tid + (g << kLaneBits);
+        const float to = fmaxf(m, s_m[from]), keep = weight<T>(m, to), f = weight<T>(s_m[from], to);
+        sum = sum * keep + s_sum[from] * f;
+        l = l * keep + s_l[from] * f;
+        m = to;
+    }
+    store_out<T>(a, b, h, row, d, sum, l);
 }
 
 namespace {
 
-struct Split {
-    int64_t chunk, chunks, q_tiles;
+struct Plan {
+    int64_t chunk, chunks, q_tiles, held;
+    int waves;
+    bool one;
 };
 
-// Chunk length: long enough that a chunk's stream (hundreds of KB) outweighs
-// its start and its partial result, short enough that the chip has several
-// workgroups per place (512 resident) to even out ragged lengths.
-Split plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len) {
-    Split s;
-    s.q_tiles = (rows + kQ - 1) / kQ;
-    const int64_t units = batch * kv_heads * s.q_tiles;
+// How a call is cut into workgroups of `waves` waves over `chunk` keys.
+Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
+    Plan p;
+    p.q_tiles = (rows + kQ - 1) / kQ;
+    p.held = rows < kQ ? rows : kQ;
+    const int64_t units = batch * kv_heads * p.q_tiles;
+    const int64_t tile = dtype == 0 && head_dim == 128 ? 16 : 32;
+    // short rows: a tile per wave (64 KB of LDS hold the waves' sums)
+    const int64_t tiles = (max_len + tile - 1) / tile;
+    p.one = tiles <= 4 || (tiles <= 16 && units <= kOneUnits && tiles * p.held * (head_dim + 4) <= 16000);
+    if (p.one) {
+        p.waves = tiles > 0 ? (int)tiles : 1;
+        p.chunk = p.waves * tile;
+        p.chunks = 1;
+        return p;
+    }
+    p.waves = kWaves;
     const int64_t step = kWaves * 32;
     const int64_t keys = (max_len + step - 1) / step * step;
-    const int64_t want = 2048;    // workgroups
-    int64_t chunk = units > 0 ? keys / (want / units > 0 ? want / units : 1) : keys;
+    int64_t chunk = units * keys / 4096;
+    if (chunk < 512) chunk = 512;
+    if (units * ((keys + chunk - 1) / chunk) < 512) chunk = units * keys / 512;
+    if (chunk < step) chunk = step;
     chunk = (chunk + step - 1) / step * step;
-    if (chunk < 2 * step) chunk = 2 * step;
     if (chunk >= keys) chunk = keys > step ? keys : step;
-    s.chunk = chunk;
-    s.chunks = keys > 0 ? (keys + chunk - 1) / chunk : 1;
-    return s;
+    p.chunk = chunk;
+    p.chunks = keys > 0 ? (keys + chunk - 1) / chunk : 1;
+    return p;
+}
+
+template <typename T, int D, bool PAGED, bool STREAM>
+void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
+    const dim3 grid(a.kv_heads, a.batch, (unsigned)(p.q_tiles * p.chunks));
+    const unsigned threads = 64 * p.waves;
+    const size_t lds = (size_t)p.waves * sp.held * (D + 4) * sizeof(float);
+    if (p.one) attn_kernel<T, D, PAGED, false, true><<<grid, threads, lds, st>>>(a, sp);
+    else attn_kernel<T, D, PAGED, STREAM, false><<<grid, threads, lds, st>>>(a, sp);
 }
 
 template <typename T, int D>
-hipError_t launch(const AttnArgs &a, const AttnSplit &sp, hipStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)a.batch * a.kv_heads * sp.q_tiles * sp.chunks);
-    if (a.table) attn_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, sp);
-    else attn_kernel<T, D, false><<<grid, 64 * kWaves, 0, st>>>(a, sp);
-    if (sp.chunks > 1)
-        attn_join_kernel<T, D><<<(unsigned)((int64_t)a.batch * a.kv_heads * a.rows), D, 0, st>>>(a, sp);
+hipError_t launch(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
+    const double bytes = 2.0 * a.batch * a.kv_heads * a.max_len * D * sizeof(T);
+    const bool stream = sp.q_tiles == 1 && bytes > 32e6;
+    if (a.table && stream) launch_rows<T, D, true, true>(a, sp, p, st);
+    else if (a.table) launch_rows<T, D, true, false>(a, sp, p, st);
+    else launch_rows<T, D, false, false>(a, sp, p, st);
+    if (sp.chunks > 1) {
+        // a group of lanes per chunk of the row, as far as a workgroup goes
+        int shift = 0;
+        while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin) ++shift;
+        const int per = kJoin / (D / 4) >> shift;   // rows per workgroup
+        const dim3 grid(a.kv_heads, a.batch, (unsigned)((a.rows + per - 1) / per));
+        attn_join_kernel<T, D><<<grid, kJoin, 0, st>>>(a, sp, shift);
+    }
     return hipGetLastError();
 }
 
@@ -394,30 +503,36 @@ hipError_t launch(const AttnArgs &a, const AttnSplit &sp, hipStream_t st) {
 
 int64_t attn_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim,
                              int dtype) {
-    const Split s = plan(batch, kv_heads, rows, max_len);
-    return s.chunks > 1 ? batch * kv_heads * rows * s.chunks * (head_dim + 2) * 4 : 0;
+    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
+    return p.chunks > 1 ? batch * kv_heads * rows * p.chunks * (head_dim + 2) * 4 : 0;
 }
 
 bool attn_fits(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
-    const int64_t most = (1LL << 24) - 1;   // workgroups: a launch's threads are counted in 32 bits
-    const Split s = plan(batch, kv_heads, rows, max_len);
-    const int64_t pairs = batch * kv_heads;  // <= 2^31
-    if (pairs == 0 || rows == 0) return true;
-    if (pairs > most / s.q_tiles || pairs * s.q_tiles > most / s.chunks) return false;
-    return s.chunks == 1 || pairs <= most / rows;
+    // a launch's grid: threads of x in 32 bits, 65536 workgroups in y and z
+    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
+    if (batch == 0 || rows == 0) return true;
+    if (kv_heads > (1 << 22) - 1 || batch > 65536 || p.q_tiles > 65536 || p.q_tiles * p.chunks > 65536) return false;
+    return p.chunks == 1 || rows <= 65536;
 }
 
 hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
-    const Split s = plan(a.batch, a.kv_heads, a.rows, a.max_len);
+    const Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len, head_dim, dtype);
     AttnSplit sp{};
-    sp.chunk = (int32_t)s.chunk;
-    sp.chunks = (int32_t)s.chunks;
-    sp.q_tiles = (int32_t)s.q_tiles;
+    sp.chunk = (int32_t)p.chunk;
+    sp.chunks = (int32_t)p.chunks;
+    sp.q_tiles = (int32_t)p.q_tiles;
+    sp.held = (int32_t)p.held;
     sp.page_magic = a.table ? ((1ull << 32) + a.page / 16 - 1) / (a.page / 16) : 0;
-    sp.sums = static_cast<float *>(workspace);
-    sp.stats = sp.sums + (int64_t)a.batch * a.kv_heads * a.rows * s.chunks * head_dim;
-    if (dtype == 1) return head_dim == 128 ? launch<_Float16, 128>(a, sp, st) : launch<_Float16, 64>(a, sp, st);
-    return head_dim == 128 ? launch<float, 128>(a, sp, st) : launch<float, 64>(a, sp, st);
+    if (p.chunks > 1) {
+        sp.sums = static_cast<float *>(workspace);
+        sp.stats = sp.sums + (int64_t)a.batch * a.kv_heads * a.rows * p.chunks * head_dim;
+    }
+    AttnArgs c = a;
+    // (no key past the table's width is valid)
+    if (a.table && c.max_len > (int64_t)a.table_width * a.page) c.max_len = a.table_width * a.page;
+    if (dtype == 1)
+        return head_dim == 128 ? launch<_Float16, 128>(c, sp, p, st) : launch<_Float16, 64>(c, sp, p, st);
+    return head_dim == 128 ? launch<float, 128>(c, sp, p, st) : launch<float, 64>(c, sp, p, st);
 }
 
 }  // namespace mnb

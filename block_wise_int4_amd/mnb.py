@@ -10,6 +10,7 @@ to another implementation when it is missing.
 import ctypes
 import os
 import re
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -85,8 +86,8 @@ _SIGNATURES = {
     "mnb_paged_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
     "mnb_paged_attn": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _vp, _sz, _vp, _vp]),
     "mnb_cross_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
-    "mnb_cross_attn": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _vp, _sz, _vp,
-                              _vp]),
+    "mnb_cross_attn": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _f32,
+                              _int, _vp, _sz, _vp, _vp]),
 }
 
 
@@ -535,11 +536,29 @@ def mnb_gemm_i8(x, pw, workspace=None, y=None):
     return y
 
 
+def _stream_handle(index):
+    """torch's current HIP stream of a device, without building a Stream object
+    (the calls below are as short as 5 us on the GPU)."""
+    if index < 0:
+        raise ValueError("the tensors must be on the GPU")
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _on(device, **tensors):
     """Every given tensor (None is skipped) is on `device`."""
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _whole(t, name, dtype, numel, index, device):
+    """Address of a contiguous buffer on `device` (whose index is `index`) that
+    the kernels read or write whole."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.numel() != numel:
+        _check_buf(t, name, dtype, numel, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _rows(t, name, dims, dtype):
@@ -557,7 +576,7 @@ def _rows(t, name, dims, dtype):
 def _strides(t):
     """Strides of all dimensions but the last (0 where only one index is in
     range, whatever the tensor says there)."""
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+    return [stride if size > 1 else 0 for size, stride in zip(t.shape[:-1], t.stride())]
 
 
 class KvCache:
@@ -575,10 +594,11 @@ class KvCache:
         _on(k.device, v=v)
         if k.shape != v.shape or _strides(k) != _strides(v):
             raise ValueError("k and v must have the same shape and strides")
-        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
         self.num_blocks, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.token_shape = (self.kv_heads, self.head_dim)
         self._desc = mnb_kv_cache(k.data_ptr(), v.data_ptr(), *k.shape, *_strides(k), dtype_code(k.dtype), 0)
-        self._ref = ctypes.byref(self._desc)
+        self.ref = ctypes.byref(self._desc)
 
     @classmethod
     def new(cls, num_blocks, kv_heads, page_size, head_dim, dtype, device="cuda"):
@@ -595,47 +615,54 @@ def mnb_kv_tables(cached, added, free_blocks, block_table, page_size, slots, len
     of free_blocks (int32), in the order of the requests; slots (int64 [T])
     receives the new tokens' places in the cache, -1 where there is none.
     Returns (lens [B], starts [B + 1], slots, taken [1])."""
-    device, B = block_table.device, cached.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
+    device, index, B, width = block_table.device, block_table.get_device(), cached.numel(), block_table.shape[1]
+    n_free, T, i32 = free_blocks.numel(), slots.numel(), torch.int32
     if lens is None:
-        lens = torch.empty(B, dtype=torch.int32, device=device)
+        lens = torch.empty(B, dtype=i32, device=device)
     if starts is None:
-        starts = torch.empty(B + 1, dtype=torch.int32, device=device)
+        starts = torch.empty(B + 1, dtype=i32, device=device)
     if taken is None:
-        taken = torch.empty(1, dtype=torch.int32, device=device)
-    width = block_table.shape[1]
-    for t, name, count in ((cached, "cached", B), (added, "added", B), (block_table, "block_table", B * width),
-                           (lens, "lens", B), (starts, "starts", B + 1), (taken, "taken", 1),
-                           (free_blocks, "free_blocks", free_blocks.numel())):
-        _check_buf(t, name, torch.int32, count, device)
-    _check_buf(slots, "slots", torch.int64, slots.numel(), device)
-    _check("mnb_kv_tables", lib().mnb_kv_tables(
-        _dev(cached, "cached"), _dev(added, "added"), _dev(free_blocks, "free_blocks"), free_blocks.numel(), B,
-        page_size, width, slots.numel(), _dev(block_table, "block_table"), _dev(lens, "lens"),
-        _dev(starts, "starts"), _dev(slots, "slots"), _dev(taken, "taken"), _stream(device)))
+        taken = torch.empty(1, dtype=i32, device=device)
+    status = lib().mnb_kv_tables(
+        _whole(cached, "cached", i32, B, index, device), _whole(added, "added", i32, B, index, device),
+        _whole(free_blocks, "free_blocks", i32, n_free, index, device), n_free, B, page_size, width, T,
+        _whole(block_table, "block_table", i32, B * width, index, device), _whole(lens, "lens", i32, B, index, device),
+        _whole(starts, "starts", i32, B + 1, index, device), _whole(slots, "slots", torch.int64, T, index, device),
+        _whole(taken, "taken", i32, 1, index, device), _stream_handle(index))
+    if status:
+        _check("mnb_kv_tables", status)
     return lens, starts, slots, taken
+
+
+def _tokens(t, name, T, cache):
+    """Token stride of new keys or values [T, kv_heads, head_dim], or the same
+    with the two last dimensions as one."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not cache.dtype or t.get_device() != cache.index:
+        _check_buf(t, name, cache.dtype, t.numel(), cache.device)
+    if len(shape) == 3 and shape[1:] == cache.token_shape and stride[2] == 1:
+        whole = stride[1] == cache.head_dim or cache.kv_heads == 1
+    else:
+        whole = len(shape) == 2 and shape[1] == cache.kv_heads * cache.head_dim and stride[1] == 1
+    if not whole:
+        raise ValueError(f"{name} must be [T, {cache.kv_heads}, {cache.head_dim}] with contiguous tokens")
+    if shape[0] != T:
+        raise ValueError(f"{name} has {shape[0]} tokens, slots {T}")
+    return stride[0] if T > 1 else 0
 
 
 def mnb_kv_append(k, v, slots, cache):
     """Write the keys and values of T tokens (k, v [T, kv_heads, head_dim] or
     [T, kv_heads * head_dim], any token stride) to the cache's slots (int64
     [T]; slots outside the cache are skipped)."""
-    T, row = slots.numel(), (cache.kv_heads, cache.head_dim)
-    _check_buf(slots, "slots", torch.int64, T, cache.device)
-    _on(cache.device, k=k, v=v)
-    for t, name in ((k, "k"), (v, "v")):
-        if t.dim() == 2 and t.shape[1] == row[0] * row[1]:
-            _rows(t, name, 2, cache.dtype)
-        elif tuple(t.shape[1:]) == row and (row[0] == 1 or t.stride(1) == row[1]):
-            _rows(t, name, 3, cache.dtype)
-        else:
-            raise ValueError(f"{name} must be [T, {row[0]}, {row[1]}] with contiguous tokens")
-        if t.shape[0] != T:
-            raise ValueError(f"{name} has {t.shape[0]} tokens, slots {T}")
-    _check("mnb_kv_append", lib().mnb_kv_append(
-        k.data_ptr(), v.data_ptr(), _strides(k)[0], _strides(v)[0], _dev(slots, "slots"), T, cache._ref,
-        _stream(cache.device)))
+    T, device, index = slots.numel(), cache.device, cache.index
+    k_stride, v_stride = _tokens(k, "k", T, cache), _tokens(v, "v", T, cache)
+    status = lib().mnb_kv_append(k.data_ptr(), v.data_ptr(), k_stride, v_stride, _whole(slots, "slots", torch.int64, T, index, device),
+                                 T, cache.ref, _stream_handle(index))
+    if status:
+        _check("mnb_kv_append", status)
 
 
 def mnb_paged_attn_workspace_bytes(B, heads, cache, max_len):
@@ -645,16 +672,17 @@ def mnb_paged_attn_workspace_bytes(B, heads, cache, max_len):
 
 
 def paged_attn_workspace(q, cache, max_len):
-    """A workspace for mnb_paged_attn (None when the call splits nothing)."""
+    """A workspace for mnb_paged_attn on q's shape (empty when the call splits
+    nothing)."""
     nbytes = mnb_paged_attn_workspace_bytes(q.shape[0], q.shape[1], cache, max_len)
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
 
 
-def _workspace(t, device):
-    if t is None:
-        return None, 0
-    _on(device, workspace=t)
-    return _dev(t, "workspace"), t.numel() * t.element_size()
+def _workspace(t, index, device):
+    if t.get_device() != index or not t.is_contiguous():
+        _on(device, workspace=t)
+        _dev(t, "workspace")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def mnb_paged_attn(q, cache, block_table, lens, max_len, scale=None, workspace=None, out=None):
@@ -662,42 +690,55 @@ def mnb_paged_attn(q, cache, block_table, lens, max_len, scale=None, workspace=N
     request stride), over its first lens[b] (int32 [B], at most max_len)
     positions of a paged cache through block_table (int32 [B, max_blocks]).
     scale: 1 / sqrt(head_dim) unless given. Returns out [B, heads, head_dim]."""
-    device = cache.device
-    _rows(q, "q", 3, cache.dtype)
-    B, heads, dim = q.shape
-    if dim != cache.head_dim or (heads > 1 and q.stride(1) != dim):
+    device, index, dtype = cache.device, cache.index, cache.dtype
+    if not isinstance(q, torch.Tensor) or q.dtype is not dtype or q.get_device() != index:
+        _check_buf(q, "q", dtype, q.numel(), device)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.stride(2) != 1 or (
+            q.shape[1] > 1 and q.stride(1) != cache.head_dim):
         raise ValueError(f"q must be [B, heads, {cache.head_dim}] with contiguous requests")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
-    _on(device, q=q)
+    B, heads, dim = q.shape
     width = block_table.shape[1]
-    _check_buf(block_table, "block_table", torch.int32, B * width, device)
-    _check_buf(lens, "lens", torch.int32, B, device)
     if out is None:
-        out = torch.empty((B, heads, dim), dtype=q.dtype, device=device)
-    _check_buf(out, "out", q.dtype, B * heads * dim, device)
+        out = torch.empty((B, heads, dim), dtype=dtype, device=device)
     if workspace is None:
         workspace = paged_attn_workspace(q, cache, max_len)
-    ws, ws_bytes = _workspace(workspace, device)
-    _check("mnb_paged_attn", lib().mnb_paged_attn(
-        q.data_ptr(), _strides(q)[0], cache._ref, _dev(block_table, "block_table"), _dev(lens, "lens"), B, heads, width,
-        max_len, dim ** -0.5 if scale is None else scale, ws, ws_bytes, _dev(out, "out"), _stream(device)))
+    status = lib().mnb_paged_attn(
+        q.data_ptr(), q.stride(0) if B > 1 else 0, cache.ref,
+        _whole(block_table, "block_table", torch.int32, B * width, index, device),
+        _whole(lens, "lens", torch.int32, B, index, device), B, heads, width, max_len, dim ** -0.5 if scale is None else scale,
+        *_workspace(workspace, index, device), _whole(out, "out", dtype, B * heads * dim, index, device), _stream_handle(index))
+    if status:
+        _check("mnb_paged_attn", status)
     return out
 
 
 def mnb_cross_attn_workspace_bytes(B, queries, keys, heads, kv_heads, head_dim, dtype):
+    """Workspace bytes mnb_cross_attn needs."""
     return lib().mnb_cross_attn_workspace_bytes(B, queries, keys, heads, kv_heads, head_dim, dtype_code(dtype))
 
 
 def cross_attn_workspace(q, k):
-    """A workspace for mnb_cross_attn (None when the call splits nothing)."""
+    """A workspace for mnb_cross_attn on q's and k's shapes (empty when the
+    call splits nothing)."""
     nbytes = mnb_cross_attn_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3],
                                             q.dtype)
-    return torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=q.device)
 
 
-def _view(t):
-    return mnb_attn_view(t.data_ptr(), *_strides(t))
+_VIEW = struct.Struct("Pqqq")   # mnb_attn_view
+
+
+def _view(t, name, dtype, index, device):
+    """The mnb_attn_view of a [batch, rows, heads, head_dim] tensor (strides of
+    dimensions with one index are left out), as bytes."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _check_buf(t, name, dtype, t.numel(), device)
+    if t.dim() != 4 or t.stride(3) != 1:
+        _rows(t, name, 4, dtype)
+    (b, r, h, _), (sb, sr, sh, _) = t.shape, t.stride()
+    return _VIEW.pack(t.data_ptr(), sb if b > 1 else 0, sr if r > 1 else 0, sh if h > 1 else 0)
 
 
 def mnb_cross_attn(q, k, v, lens=None, scale=None, workspace=None, out=None):
@@ -705,29 +746,22 @@ def mnb_cross_attn(q, k, v, lens=None, scale=None, workspace=None, out=None):
     [B, Tk, kv_heads, head_dim] (any strides whose rows of head_dim are
     contiguous), of which the first lens[b] (int32 [B]; None: all) are valid.
     scale: 1 / sqrt(head_dim) unless given. Returns out, shaped as q."""
-    dtype_code(q.dtype)
-    device = q.device
-    if device.type != "cuda":
-        raise ValueError("q must be on the GPU")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _rows(t, name, 4, q.dtype)
+    code, dtype, device, index = dtype_code(q.dtype), q.dtype, q.device, q.get_device()
+    views = _view(q, "q", dtype, index, device), _view(k, "k", dtype, index, device), _view(v, "v", dtype, index, device)
     B, Tq, heads, dim = q.shape
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != dim:
         raise ValueError("k and v must be [B, Tk, kv_heads, head_dim] with q's B and head_dim")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=device)
-    _rows(out, "out", 4, q.dtype)
-    if out.shape != q.shape:
+        out = torch.empty(q.shape, dtype=dtype, device=device)
+    elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _on(device, k=k, v=v, out=out)
-    if lens is not None:
-        _check_buf(lens, "lens", torch.int32, B, device)
+    to = _view(out, "out", dtype, index, device)
     if workspace is None:
         workspace = cross_attn_workspace(q, k)
-    ws, ws_bytes = _workspace(workspace, device)
-    _check("mnb_cross_attn", lib().mnb_cross_attn(
-        ctypes.byref(_view(q)), ctypes.byref(_view(k)), ctypes.byref(_view(v)),
-        None if lens is None else _dev(lens, "lens"), B, Tq, k.shape[1], heads, k.shape[2], dim,
-        dim ** -0.5 if scale is None else scale, dtype_code(q.dtype), ws, ws_bytes, ctypes.byref(_view(out)),
-        _stream(device)))
+    status = lib().mnb_cross_attn(
+        *views, None if lens is None else _whole(lens, "lens", torch.int32, B, index, device), B, Tq,
+        k.shape[1], heads, k.shape[2], dim, dim ** -0.5 if scale is None else scale, code,
+        *_workspace(workspace, index, device), to, _stream_handle(index))
+    if status:
+        _check("mnb_cross_attn", status)
     return out
