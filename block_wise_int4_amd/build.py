@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmnb.so")
 SOURCES = ("mnb_api.hip", "mnb_aux.hip", "mnb_gemv.hip", "mnb_gemm.hip", "mnb_embed.hip", "mnb_int8.hip",
-           "mnb_attn_api.hip", "mnb_attn.hip", "mnb_kv.hip")
+           "mnb_attn_api.hip", "mnb_attn.hip", "mnb_cross.hip", "mnb_kv.hip")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -57,6 +57,14 @@ int64_t attn_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t rows, int6
                              int dtype);
 // False: more workgroups than a launch takes.
 bool attn_fits(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype);
+// (workspace NULL: one launch, nothing split)
 hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspace, hipStream_t st);
+
+// The same sums for float16 calls with many query rows over unpaged keys
+// (mnb_cross.hip), which needs no workspace: whether it is the faster one, by
+// sizes alone, and whether it can address these strides.
+bool cross_many(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype);
+bool cross_fits(const AttnArgs &a, int head_dim);
+hipError_t launch_cross(const AttnArgs &a, int head_dim, hipStream_t st);
 
 }  // namespace mnb

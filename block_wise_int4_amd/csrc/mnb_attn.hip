@@ -516,7 +516,11 @@ bool attn_fits(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, i
 }
 
 hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
-    const Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len, head_dim, dtype);
+    Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len, head_dim, dtype);
+    if (!workspace && p.chunks > 1) {
+        p.chunk = (a.max_len + 31) / 32 * 32;
+        p.chunks = 1;
+    }
     AttnSplit sp{};
     sp.chunk = (int32_t)p.chunk;
     sp.chunks = (int32_t)p.chunks;

@@ -63,6 +63,12 @@ int check_workspace(int64_t need, const void *workspace, size_t bytes) {
     return bytes < (size_t)need ? MNB_ERR_INVALID : MNB_OK;
 }
 
+// Workspace of a cross attention call: by sizes alone, whichever kernel its
+// strides allow.
+int64_t cross_workspace(int64_t B, int64_t Hkv, int64_t rows, int64_t Tk, int head_dim, int dtype) {
+    return cross_many(B, Hkv, rows, Tk, head_dim, dtype) ? 0 : attn_workspace_bytes(B, Hkv, rows, Tk, head_dim, dtype);
+}
+
 }  // namespace
 
 extern "C" {
@@ -176,7 +182,7 @@ int mnb_paged_attn(const void *q, int64_t q_stride, const mnb_kv_cache *cache, c
 size_t mnb_cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t head_dim,
                                       int dtype) {
     if (check_heads(B, Tq, Tk, Hq, Hkv, head_dim, dtype) != MNB_OK || B == 0 || Tq == 0) return 0;
-    return (size_t)attn_workspace_bytes(B, Hkv, Tq * (Hq / Hkv), Tk, (int)head_dim, dtype);
+    return (size_t)cross_workspace(B, Hkv, Tq * (Hq / Hkv), Tk, (int)head_dim, dtype);
 }
 
 int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_attn_view *v, const int32_t *lens,
@@ -194,7 +200,7 @@ int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_att
         !aligned(lens, 4))
         return MNB_ERR_ALIGN;
     const int64_t rows = Tq * (Hq / Hkv);
-    const int64_t need = attn_workspace_bytes(B, Hkv, rows, Tk, (int)head_dim, dtype);
+    const int64_t need = cross_workspace(B, Hkv, rows, Tk, (int)head_dim, dtype);
     if (int st = check_workspace(need, workspace, workspace_bytes)) return st;
     AttnArgs a{};
     a.q = q->data;
@@ -220,7 +226,10 @@ int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_att
     a.rows = (int32_t)rows;
     a.max_len = (int32_t)Tk;
     a.scale = scale;
-    return hip_status(launch_attn(a, (int)head_dim, dtype, workspace, static_cast<hipStream_t>(stream)));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (cross_many(B, Hkv, rows, Tk, (int)head_dim, dtype) && cross_fits(a, (int)head_dim))
+        return hip_status(launch_cross(a, (int)head_dim, st));
+    return hip_status(launch_attn(a, (int)head_dim, dtype, need ? workspace : nullptr, st));
 }
 
 }  // extern "C"

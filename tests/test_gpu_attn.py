@@ -529,3 +529,92 @@ def test_binding_refusals():
         small = torch.empty(need - 1, dtype=torch.uint8, device=DEV)
         with pytest.raises(mnb.MnbError, match="INVALID"):
             mnb.mnb_paged_attn(long_q, long_cache, long_table, long_ln, 9000, workspace=small)
+
+
+# ---------------------------------------------------------------------------
+# cross attention with many rows (float16: the kernel whose tiles go through
+# LDS), in both of its forms
+# ---------------------------------------------------------------------------
+
+MANY = [  # batch, queries, keys, heads, kv_heads, dim
+    (24, 130, 200, 4, 2, 64), (24, 130, 257, 4, 2, 64), (24, 100, 333, 6, 2, 128), (13, 70, 100, 3, 3, 128),
+    (64, 17, 31, 4, 4, 64), (64, 17, 65, 4, 4, 128), (40, 64, 32, 2, 1, 64), (40, 65, 33, 5, 5, 128),
+    (100, 9, 96, 8, 2, 64), (200, 20, 1, 1, 1, 64),
+]
+
+
+def _many_rows(queries):
+    return sorted({0, queries // 3, queries - 1})
+
+
+@pytest.mark.parametrize("batch,queries,keys,heads,kv_heads,dim", MANY)
+def test_cross_many(batch, queries, keys, heads, kv_heads, dim):
+    print(f"cross many {batch}x{queries}x{keys} heads={heads}/{kv_heads} dim={dim}", flush=True)
+    q, k, v = _cross_case(batch + keys, batch, queries, keys, heads, kv_heads, dim, "f16")
+    got = mnb.mnb_cross_attn(q, k, v)
+    pick = [0, batch // 2, batch - 1]
+    _check_cross(got[pick], q[pick], k[pick], v[pick], None, "f16", rows=_many_rows(queries))
+    # every length around the steps of 32 and 64 keys, garbage past it
+    lens = [[keys, 0, 1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 128, 129, -5, 10 ** 6][b % 16] for b in range(batch)]
+    for b, n in enumerate(lens):
+        k[b, max(0, n):], v[b, max(0, n):] = NAN, (INF if b % 2 else NAN)
+    got = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    empty = [b for b, n in enumerate(lens) if n <= 0]
+    assert not got[empty].any()
+    pick = list(range(min(16, batch)))
+    _check_cross(got[pick], q[pick], k[pick], v[pick], [lens[b] for b in pick], "f16", rows=_many_rows(queries))
+    again = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_cross_many_strides(dim):
+    batch, queries, keys, heads = 40, 70, 77, 4
+    q, k, v = _cross_case(15, batch, queries, keys, heads, heads, dim, "f16")
+    ref = mnb.mnb_cross_attn(q, k, v)
+    kk = k.transpose(1, 2).contiguous().transpose(1, 2)
+    fused = torch.full((batch, keys, 2, heads, dim), NAN, dtype=torch.float16, device=DEV)
+    fused[:, :, 1] = v
+    wide = torch.full((batch, queries, heads, 3 * dim), NAN, dtype=torch.float16, device=DEV)
+    wide[..., dim: 2 * dim] = q
+    out = torch.full((batch, heads, queries, 2 * dim), 7.0, dtype=torch.float16, device=DEV)
+    got = mnb.mnb_cross_attn(wide[..., dim: 2 * dim], kk, fused[:, :, 1], out=out[..., :dim].transpose(1, 2))
+    assert torch.equal(got, ref)
+    assert (out[..., dim:] == 7.0).all()
+    shared = mnb.mnb_cross_attn(q, k[:1].expand(batch, -1, -1, -1), v[:1].expand(batch, -1, -1, -1))
+    assert torch.equal(shared[0], ref[0])
+    _check_cross(shared[-1:], q[-1:], k[:1], v[:1], None, "f16", rows=[0, 69])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("keys", [90, 300])
+def test_cross_many_scales_infinities_and_nan(keys, dim):
+    batch, queries, heads = 40, 80, 4
+    q, k, v = _cross_case(16, batch, queries, keys, heads, heads, dim, "f16")
+    for scale in (0.0, -0.21, 0.9):
+        got = mnb.mnb_cross_attn(q, k, v, scale=scale)
+        _check_cross(got[:2], q[:2], k[:2], v[:2], None, "f16", scale, rows=[0, 63, 64, 79])
+    # scores that rise along the keys by far more than the reference's slack
+    q[0] = 0.5
+    k[0] = (torch.arange(keys, device=DEV) * (30.0 / keys) - 15).half()[:, None, None]
+    q[1:4] = 1.0
+    k[1], k[2, keys - 1], k[3, 3] = -INF, NAN, INF
+    got = mnb.mnb_cross_attn(q, k, v, scale=1.0)
+    _check_cross(got[:1], q[:1], k[:1], v[:1], None, "f16", 1.0, rows=[0, 79])
+    assert not got[1].any()
+    assert torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+    assert torch.isfinite(got[4:]).all()
+
+
+def test_cross_many_rows_too_far_apart_for_32_bits():
+    # keys 2^25 elements apart: the LDS kernel's 32-bit range does not reach
+    batch, queries, keys, dim = 2, 3000, 40, 64
+    buf = torch.zeros((keys - 1) * 2 ** 25 + 4 * dim, dtype=torch.float16, device=DEV)
+    k = buf.as_strided((batch, keys, 1, dim), (dim, 2 ** 25, dim, 1))
+    v = buf.as_strided((batch, keys, 1, dim), (dim, 2 ** 25, dim, 1), 2 * dim)
+    g = torch.Generator(DEV).manual_seed(3)
+    q = torch.randn((batch, queries, 1, dim), device=DEV, generator=g).half()
+    k.copy_(torch.randn(k.shape, device=DEV, generator=g))
+    v.copy_(torch.randn(v.shape, device=DEV, generator=g))
+    got = mnb.mnb_cross_attn(q, k, v)
+    _check_cross(got, q, k, v, None, "f16", rows=[0, 1500, 2999])
