@@ -6,9 +6,10 @@
 // keys are cut into chunks, and a chunk's tiles of 16 or 32 keys are taken in
 // turn by the waves of one workgroup. A wave streams its tiles from memory
 // straight into the registers that the matrix instructions read (no LDS):
-//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row), B = queries;
-//                 the result holds, per lane, four keys 4 (l / 16) + i of one
-//                 query l % 16, which is already the B operand's layout of
+//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row, after a swap
+//                 between lanes l and l ^ 8), B = queries; the result holds,
+//                 per lane, four keys 4 (l / 16) + i of one query l % 16,
+//                 which is already the B operand's layout of
 //   O^T = V^T P^T with the contraction index renumbered: A's rows are
 //                 dimensions. A lane loads whole pieces of V rows (l % 16 says
 //                 which piece: a row is one coalesced run over 16 lanes), and
@@ -28,8 +29,7 @@ namespace mnb {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kOneUnits = 256;
+constexpr int kWaves = 4;                   // of a workgroup over a chunk (eight measured the same)
 constexpr int kQ = 16;                      // query rows per row of tiles
 constexpr float kLowest = -3.402823466e38f; // the reference before any key
 constexpr float kLog2e = 1.4426950408889634f;
@@ -198,14 +198,37 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
             from_v[s] = (of * a.v_batch + row * a.v_row) * (int64_t)sizeof(T);
         }
     };
+    // Keys are loaded eight rows by 128 bytes at a time, whole cache lines (16
+    // rows by 64 bytes, the layout the product wants, let a CU take in 37 GB/s
+    // instead of 116): lane (col, g) takes 16 bytes of row col % 8, or of row
+    // col % 8 + 8 in the other load of a pair, and swaps with lane col ^ 8.
     auto load_k = [&](const int *valid) {
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
-            const int last = valid[s] > 0 ? valid[s] - 1 : 0;
-            const uint32_t at = (uint32_t)(col < last ? col : last) * k_row + g * 16;
+            const int last = valid[s] > 0 ? valid[s] - 1 : 0, r = col & 7;
+            const uint32_t in = (col >> 3) * 64 + g * 16;
+            const uint32_t low = (uint32_t)(r < last ? r : last) * k_row + in;
+            const uint32_t high = (uint32_t)(r + 8 < last ? r + 8 : last) * k_row + in;
 #pragma unroll
-            for (int j = 0; j < S::kK; ++j) k[s][j] = fetch<STREAM, u32x4>(kp + from_k[s] + at + j * 64);
+            for (int j = 0; j < S::kK; j += 2) {
+                k[s][j] = fetch<STREAM, u32x4>(kp + from_k[s] + low + j * 64);
+                k[s][j + 1] = fetch<STREAM, u32x4>(kp + from_k[s] + high + j * 64);
+            }
         }
+    };
+    auto swap_k = [&]() {
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+            for (int j = 0; j < S::kK; j += 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // lanes 8..15 of 16 take the low half of their row from
+                    // lane - 8, lanes 0..7 the high half of theirs from lane + 8
+                    const int low = (int)k[s][j][e], high = (int)k[s][j + 1][e];
+                    k[s][j][e] = (uint32_t)__builtin_amdgcn_update_dpp(low, high, 0x128, 0xF, 0xC, false);
+                    k[s][j + 1][e] = (uint32_t)__builtin_amdgcn_update_dpp(high, low, 0x128, 0xF, 0x3, false);
+                }
     };
     auto load_v = [&](const int *valid) {
 #pragma unroll
@@ -239,24 +262,30 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
     }
     for (; key < end; key += step) {
         float x[S::kSub][4];
+        swap_k();
+        // (two sums per part, so that no product waits for the one before)
+        f4 c[S::kSub][2];
 #pragma unroll
-        for (int s = 0; s < S::kSub; ++s) {
-            f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < S::kSub; ++s) c[s][0] = c[s][1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < S::kK; ++j) {
-                if constexpr (sizeof(T) == 2) {
-                    c = mma16(__builtin_bit_cast(h8, k[s][j]), __builtin_bit_cast(h8, q[j]), c);
-                } else {
-                    const f4 kk = __builtin_bit_cast(f4, k[s][j]), qq = __builtin_bit_cast(f4, q[j]);
-                    c = mma4(kk.x, qq.x, c);
-                    c = mma4(kk.y, qq.y, c);
-                    c = mma4(kk.z, qq.z, c);
-                    c = mma4(kk.w, qq.w, c);
-                }
+        for (int j = 0; j < S::kK; ++j) {
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int s = 0; s < S::kSub; ++s)
+                    c[s][j & 1] = mma16(__builtin_bit_cast(h8, k[s][j]), __builtin_bit_cast(h8, q[j]), c[s][j & 1]);
+            } else {
+                const f4 qq = __builtin_bit_cast(f4, q[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int s = 0; s < S::kSub; ++s)
+                        c[s][e & 1] = mma4(__builtin_bit_cast(f4, k[s][j])[e], qq[e], c[s][e & 1]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[s][i] = c[i] * mul;
         }
+#pragma unroll
+        for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[s][i] = (c[s][0][i] + c[s][1][i]) * mul;
         int valid_next[S::kSub];
         if constexpr (!ONE) {
             locate(key + step, valid_next);
@@ -442,16 +471,23 @@ struct Plan {
     bool one;
 };
 
-// How a call is cut into workgroups of `waves` waves over `chunk` keys.
+// How a call is cut into workgroups of `waves` waves over `chunk` keys. Times
+// below are of whole calls, 16 query heads of 128 over 8 in float16 or 12 of 64
+// over 12 in float32.
 Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.q_tiles = (rows + kQ - 1) / kQ;
     p.held = rows < kQ ? rows : kQ;
     const int64_t units = batch * kv_heads * p.q_tiles;
     const int64_t tile = dtype == 0 && head_dim == 128 ? 16 : 32;
-    // short rows: a tile per wave (64 KB of LDS hold the waves' sums)
+    // Short rows: a tile per wave, one launch, as long as one round of
+    // workgroups holds them (256 CUs; 64 KB of LDS hold the waves' sums): 8
+    // requests of up to 130 keys 6.2 us against 8.5 in two launches of four
+    // waves, one of 452 keys 8.4 against 10.2; but 480 units of up to 250 keys
+    // 14.0 against 12.1. Up to four tiles both forms are one launch of four
+    // waves.
     const int64_t tiles = (max_len + tile - 1) / tile;
-    p.one = tiles <= 4 || (tiles <= 16 && units <= kOneUnits && tiles * p.held * (head_dim + 4) <= 16000);
+    p.one = tiles <= 4 || (tiles <= 16 && units <= 256 && tiles * p.held * (head_dim + 4) <= 16000);
     if (p.one) {
         p.waves = tiles > 0 ? (int)tiles : 1;
         p.chunk = p.waves * tile;
@@ -461,8 +497,12 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int he
     p.waves = kWaves;
     const int64_t step = kWaves * 32;
     const int64_t keys = (max_len + step - 1) / step * step;
+    // About 4096 workgroups (the card holds 768: rows end at different keys, and
+    // small pieces even that out), of 384 keys or more (16 x 1503 keys in
+    // float32: 22.4 us, 24.4 with 512, 22.2 with 256; 32 x 62..2001 keys in
+    // float16: 28.4, 28.4, 30.1), and of fewer where the card would be empty.
     int64_t chunk = units * keys / 4096;
-    if (chunk < 512) chunk = 512;
+    if (chunk < 384) chunk = 384;
     if (units * ((keys + chunk - 1) / chunk) < 512) chunk = units * keys / 512;
     if (chunk < step) chunk = step;
     chunk = (chunk + step - 1) / step * step;
@@ -483,6 +523,8 @@ void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStrea
 
 template <typename T, int D>
 hipError_t launch(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
+    // Caches that the L2 (32 MB in all) cannot hold are read past it: 1.1 GB at
+    // 6.5 TB/s instead of 5.7; smaller ones may stay there for the next call.
     const double bytes = 2.0 * a.batch * a.kv_heads * a.max_len * D * sizeof(T);
     const bool stream = sp.q_tiles == 1 && bytes > 32e6;
     if (a.table && stream) launch_rows<T, D, true, true>(a, sp, p, st);
