@@ -18,6 +18,7 @@ struct KvTablesArgs {
     int32_t batch, page, width;
     int32_t *table, *lens, *starts, *taken;
     int64_t *slots;
+    uint64_t page_magic;   // (set by the launcher)
 };
 hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t st);
 

@@ -19,7 +19,14 @@ namespace mnb {
 constexpr int kTabThreads = 256;
 constexpr int kTabPer = 4;                         // requests per thread and pass
 constexpr int kScan = kTabThreads * kTabPer;       // requests per pass
-constexpr int kTabTokens = 1024;                   // tokens per workgroup
+constexpr int kTabTokens = 256;                    // tokens per workgroup: one search per thread
+
+// x / page for 0 <= x < 2^30, page = 16 m, magic = ceil(2^32 / m): the error of
+// the product is below x / 16 * m / 2^32 < 1 / m, so the floor is exact.
+__device__ __forceinline__ int32_t blocks_in(int32_t x, uint64_t magic) {
+    return (int32_t)(((uint32_t)x >> 4) * magic >> 32);
+}
+__device__ __forceinline__ int32_t blocks_for(int32_t x, uint64_t magic) { return x > 0 ? blocks_in(x - 1, magic) + 1 : 0; }
 
 // Largest i < n with first[i] <= x (first[0] <= x; ascending).
 __device__ __forceinline__ int last_not_above(const int64_t *first, int n, int64_t x) {
@@ -38,14 +45,14 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
     __shared__ int32_t s_cached[kScan];
     __shared__ int64_t s_wave[2][kTabThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t limit = (int64_t)a.width * a.page;
+    const int32_t limit = a.width * a.page;        // <= 2^30
     const int64_t t0 = (int64_t)blockIdx.x * kTabTokens;
     const int64_t t1 = t0 + kTabTokens < a.tokens ? t0 + kTabTokens : a.tokens;
     int64_t rows_before = 0, blocks_before = 0;    // over the passes so far
     for (int base = 0; base < a.batch; base += kScan) {
         const int n = a.batch - base < kScan ? a.batch - base : kScan;
         int32_t cached[kTabPer];
-        int64_t added[kTabPer], need[kTabPer], len[kTabPer];
+        int32_t added[kTabPer], need[kTabPer], len[kTabPer];
         int64_t sum_rows = 0, sum_blocks = 0;
 #pragma unroll
         for (int i = 0; i < kTabPer; ++i) {
@@ -54,12 +61,11 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
             added[i] = need[i] = len[i] = 0;
             if (b < n) {
                 const int32_t c = a.cached[base + b], d = a.added[base + b];
-                cached[i] = c > 0 ? c : 0;
+                // (past the limit nothing has a place, wherever it starts)
+                cached[i] = c < 0 ? 0 : c < limit ? c : limit;
                 added[i] = d > 0 ? d : 0;
-                len[i] = cached[i] + added[i];
-                if (len[i] > limit) len[i] = limit;
-                need[i] = (len[i] + a.page - 1) / a.page - ((int64_t)cached[i] + a.page - 1) / a.page;
-                if (need[i] < 0) need[i] = 0;
+                len[i] = added[i] < limit - cached[i] ? cached[i] + added[i] : limit;
+                need[i] = blocks_for(len[i], a.page_magic) - blocks_for(cached[i], a.page_magic);
             }
             sum_rows += added[i];
             sum_blocks += need[i];
@@ -110,21 +116,26 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
         for (int64_t e = blocks_before + (int64_t)blockIdx.x * kTabThreads + tid; e < all_blocks;
              e += (int64_t)gridDim.x * kTabThreads) {
             const int b = last_not_above(s_off, n, e);
-            const int64_t have = ((int64_t)s_cached[b] + a.page - 1) / a.page;
+            const int64_t have = blocks_for(s_cached[b], a.page_magic);
             a.table[(int64_t)(base + b) * a.width + have + (e - s_off[b])] = e < a.n_free ? a.free_blocks[e] : -1;
         }
         // this workgroup's tokens that belong to requests of this pass
         const int64_t u0 = t0 > rows_before ? t0 : rows_before, u1 = t1 < all_rows ? t1 : all_rows;
         for (int64_t t = u0 + tid; t < u1; t += kTabThreads) {
             const int b = last_not_above(s_start, n, t);
-            const int64_t c = s_cached[b], pos = c + (t - s_start[b]);
-            const int64_t have = (c + a.page - 1) / a.page, place = pos / a.page;
-            int64_t id = -1;
-            if (pos < limit) {
+            const int32_t c = s_cached[b];
+            const int64_t past = t - s_start[b];
+            int64_t slot = -1;
+            if (past < limit - c) {
+                const int32_t pos = c + (int32_t)past;
+                const int32_t have = blocks_for(c, a.page_magic), place = blocks_in(pos, a.page_magic);
+                const int64_t fresh = s_off[b] + place - have;   // in the free list
+                int64_t id = -1;
                 if (place < have) id = a.table[(int64_t)(base + b) * a.width + place];
-                else if (s_off[b] + place - have < a.n_free) id = a.free_blocks[s_off[b] + place - have];
+                else if (fresh < a.n_free) id = a.free_blocks[fresh];
+                if (id >= 0) slot = id * a.page + (pos - place * a.page);
             }
-            a.slots[t] = id < 0 ? -1 : id * a.page + (pos - place * a.page);
+            a.slots[t] = slot;
         }
         rows_before = all_rows;
         blocks_before = all_blocks;
@@ -139,7 +150,9 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
 
 hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t st) {
     const int64_t wgs = (a.tokens + kTabTokens - 1) / kTabTokens;
-    kv_tables_kernel<<<(unsigned)(wgs < 1 ? 1 : wgs), kTabThreads, 0, st>>>(a);
+    KvTablesArgs c = a;
+    c.page_magic = ((1ull << 32) + a.page / 16 - 1) / (a.page / 16);
+    kv_tables_kernel<<<(unsigned)(wgs < 1 ? 1 : wgs), kTabThreads, 0, st>>>(c);
     return hipGetLastError();
 }
 
