@@ -6,10 +6,10 @@
 // keys are cut into chunks, and a chunk's tiles of 16 or 32 keys are taken in
 // turn by the waves of one workgroup. A wave streams its tiles from memory
 // straight into the registers that the matrix instructions read (no LDS):
-//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row, after a swap
-//                 between lanes l and l ^ 8), B = queries; the result holds,
-//                 per lane, four keys 4 (l / 16) + i of one query l % 16,
-//                 which is already the B operand's layout of
+//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row, after a
+//                 four-by-four turn between registers and lanes), B = queries;
+//                 the result holds, per lane, four keys 4 (l / 16) + i of one
+//                 query l % 16, which is already the B operand's layout of
 //   O^T = V^T P^T with the contraction index renumbered: A's rows are
 //                 dimensions. A lane loads whole pieces of V rows (l % 16 says
 //                 which piece: a row is one coalesced run over 16 lanes), and
@@ -18,10 +18,13 @@
 //                 per pair of keys.
 // The next tile's keys are requested as soon as the first product has read
 // this one's, its values after the second: one tile of registers, something
-// always in flight, three workgroups per CU. The code is kept small on
-// purpose: a wave of a short row executes most of it once, out of a cold
-// instruction cache.
+// always in flight, three workgroups per CU.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
+//
+// Bound: memory where the card is full (32 requests of 500..16384 keys, 1.1 GB:
+// 178 us, 6.2 TB/s; a bare copy's read side reaches 6.8), and latency below
+// some 30 MB: a launch, the chain length - table entry - tile, and the second
+// launch are 10 us by themselves.
 #include "mnb_attn.h"
 #include "mnb_device.h"
 
@@ -66,12 +69,12 @@ template <typename T> __device__ __forceinline__ float weight(float x, float ref
 __device__ __forceinline__ f4 mma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma4(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-// A load that leaves no copy in the caches it passes (STREAM), for caches of
-// keys and values larger than those.
-template <bool STREAM, typename V> __device__ __forceinline__ V fetch(const uint8_t *p) {
-    const V *from = reinterpret_cast<const V *>(p);
-    if constexpr (STREAM) return __builtin_nontemporal_load(from);
-    else return *from;
+// A load by buffer (bytes past its range read as zeros, from nowhere); STREAM
+// leaves no copy in the caches it passes, for caches of keys and values larger
+// than those.
+template <bool STREAM, typename V> __device__ __forceinline__ V fetch(__amdgpu_buffer_rsrc_t from, uint32_t at) {
+    if constexpr (sizeof(V) == 16) return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, STREAM ? 2 : 0));
+    else return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, STREAM ? 2 : 0));
 }
 
 __device__ __forceinline__ int keys_of(const AttnArgs &a, int64_t b) {
@@ -80,10 +83,33 @@ __device__ __forceinline__ int keys_of(const AttnArgs &a, int64_t b) {
     return n;
 }
 
+// Blocks before a part of 16 keys.
+__device__ __forceinline__ uint32_t blocks_before(uint32_t part, uint32_t magic) {
+    const uint32_t place = __umulhi(part, magic);
+    return magic ? place : part;
+}
+
 // Query token of a query row (a decoding step has one, and no division).
 __device__ __forceinline__ int token_of(const AttnArgs &a, int row) {
     return a.rows == a.group ? 0 : (int)((uint32_t)row / (uint32_t)a.group);
 }
+
+// A value of another lane of the four (a quad permutation).
+template <int Ctrl> __device__ __forceinline__ uint32_t from_lane(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, Ctrl, 0xF, 0xF, true);
+}
+
+// Lanes 32..63 of the first against lanes 0..31 of the second.
+__device__ __forceinline__ void swap_halves(u32x4 &a, u32x4 &b) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto w = __builtin_amdgcn_permlane32_swap(a[e], b[e], false, false);
+        a[e] = w[0];
+        b[e] = w[1];
+    }
+}
+
+__device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
 
 // Four outputs from dimension d on of a query row.
 template <typename T>
@@ -108,19 +134,16 @@ struct AttnSplit {
     int32_t chunk;        // keys per chunk
     int32_t chunks;       // of max_len
     int32_t q_tiles, held;   // of `rows`; min(rows, kQ)
-    uint64_t page_magic;  // ceil(2^32 / (page / 16)): (part * magic) >> 32 = part / (page / 16) for part < 2^26
+    uint32_t page_magic;  // ceil(2^32 / (page / 16)), 0 for pages of 16: part * magic >> 32 = part / (page / 16) for part < 2^26
     float *sums, *stats;
 };
 
-// ONE: rows of at most a tile per wave, up to 16 waves; otherwise kWaves.
-template <typename T, int D, bool PAGED, bool STREAM, bool ONE>
-__global__ __launch_bounds__(ONE ? 1024 : 64 * kWaves, ONE || D * (int)sizeof(T) <= 128 ? 4 : 3)
-void attn_kernel(AttnArgs a, AttnSplit sp) {
-    constexpr int kMost = ONE ? 16 : kWaves;
+template <typename T, int D, bool PAGED, bool STREAM>
+__device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSplit &sp) {
     using S = TileShape<T, D>;
     typedef typename Piece<S::kVBytes>::type VP;
     extern __shared__ __attribute__((aligned(16))) float s_o[];   // [waves][held][D + 4]
-    __shared__ float s_m[kMost][kQ], s_l[kMost][kQ];
+    __shared__ float s_m[kWaves][kQ], s_l[kWaves][kQ];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     // the head varies fastest, the chunk slowest: blocks go to the XCDs in
@@ -135,7 +158,9 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
     }
     const int begin = chunk * sp.chunk;
     int key = begin + wave * S::kKeys;
-    const int32_t *table = PAGED ? a.table + b * a.table_width : nullptr;
+    // (no kernel writes the table while this one reads it: scalar loads)
+    typedef __attribute__((address_space(4))) const int32_t table_entry;
+    table_entry *table = PAGED ? (table_entry *)(a.table + b * a.table_width) : nullptr;
 
     // The table entries of the tile at key0 (past the table's end its last
     // entry, which is not used).
@@ -144,7 +169,7 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
         if constexpr (PAGED) {
 #pragma unroll
             for (int s = 0; s < S::kSub; ++s) {
-                const uint32_t place = (uint32_t)((((uint32_t)key0 >> 4) + s) * sp.page_magic >> 32);
+                const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + s, sp.page_magic);
                 ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
             }
         }
@@ -155,20 +180,21 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;   // (n may be <= 0: no tile then)
     const int rows = a.rows - q_tile * kQ < kQ ? a.rows - q_tile * kQ : kQ;
 
-    // queries: lane (query col, dimensions of its group g of each 64-byte run)
+    // queries: lane (query col, dimensions of its group g, as `turn` leaves the keys)
     u32x4 q[S::kK];
     {
         const int r = q_tile * kQ + (col < rows ? col : 0), token = token_of(a, r);
         const T *src = static_cast<const T *>(a.q) + b * a.q_batch + token * a.q_row +
                        (int64_t)(h * a.group + r - token * a.group) * a.q_head;
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(src) + g * 16;
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(src) + (S::kK == 2 ? (g & 1) * 64 + (g >> 1) * 16 : g * 64);
 #pragma unroll
-        for (int j = 0; j < S::kK; ++j) q[j] = *reinterpret_cast<const u32x4 *>(p + j * 64);
+        for (int j = 0; j < S::kK; ++j)
+            q[j] = *reinterpret_cast<const u32x4 *>(p + (S::kK == 2 ? j * 32 : j / 4 * 256 + j % 4 * 16));
     }
 
-    // One tile: keys, values, and where the next one is. Every address stays
-    // inside the cache: parts without a valid key read block 0 (or the
-    // request's first row), rows past the last valid key read that key's row.
+    // One tile: keys, values, and where the next one is. A part (16 keys) is
+    // read through a buffer that ends with its last valid key: what lies behind
+    // reads as zeros, and a part without keys reads nothing.
     u32x4 k[S::kSub][S::kK];
     VP v[S::kSub][4][S::kV];
     int valid[S::kSub];   // leading valid keys of each part
@@ -182,65 +208,79 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
             const int first = key0 + 16 * s;
             int ok = end - first;
             ok = ok < 0 ? 0 : ok > 16 ? 16 : ok;
-            int64_t row = first, of = b;
+            int64_t of = b;
+            uint32_t row = first;
             if constexpr (PAGED) {
                 of = ids[s];
-                if (of < 0 || of >= a.num_blocks) ok = 0;
+                ok = (uint64_t)of < (uint64_t)a.num_blocks ? ok : 0;
                 const uint32_t part = (uint32_t)first >> 4;
-                row = (int)(part - (uint32_t)(part * sp.page_magic >> 32) * (a.page >> 4)) << 4;
+                row = (part - blocks_before(part, sp.page_magic) * (uint32_t)(a.page >> 4)) << 4;
             }
-            if (ok == 0) {
-                row = 0;
-                of = PAGED ? 0 : b;
-            }
-            valid[s] = ok;
-            from_k[s] = (of * a.k_batch + row * a.k_row) * (int64_t)sizeof(T);
-            from_v[s] = (of * a.v_batch + row * a.v_row) * (int64_t)sizeof(T);
+            valid[s] = __builtin_amdgcn_readfirstlane(ok);
+            from_k[s] = of * a.k_batch * (int64_t)sizeof(T) + (int64_t)((uint64_t)row * k_row);
+            from_v[s] = of * a.v_batch * (int64_t)sizeof(T) + (int64_t)((uint64_t)row * v_row);
         }
     };
-    // Keys are loaded eight rows by 128 bytes at a time, whole cache lines (16
-    // rows by 64 bytes, the layout the product wants, let a CU take in 37 GB/s
-    // instead of 116): lane (col, g) takes 16 bytes of row col % 8, or of row
-    // col % 8 + 8 in the other load of a pair, and swaps with lane col ^ 8.
+    auto part_of = [&](const uint8_t *base, int64_t from, int ok, uint32_t row) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base + from), 0,
+                                                 ok > 0 ? (uint32_t)(ok - 1) * row + S::kRow : 0u, 0x00020000);
+    };
+    // Keys are loaded so that four lanes after another take 64 bytes of a row:
+    // the load unit serves 16 lanes in turn, one run of bytes a cycle, and a CU
+    // takes in 105 GB/s like this but 37 where every lane reads another row, as
+    // the product wants them. Load i of a lane (4 a + x, g) is piece x of row
+    // 4 a + i, and `turn` makes it piece i of row 4 a + x.
+    uint32_t k_at[4], v_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (rows of two 64-byte runs: a load has eight rows, 4 a + i and 4 a + i + 2)
+        k_at[i] = S::kK == 2 ? ((col & 12) + (i & 1) + (g & 2)) * k_row + (g & 1) * 64 + (col & 3) * 16
+                             : ((col & 12) + i) * k_row + g * 64 + (col & 3) * 16;
+        v_at[i] = (4 * g + i) * v_row + col * S::kVBytes;
+    }
     auto load_k = [&](const int *valid) {
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
-            const int last = valid[s] > 0 ? valid[s] - 1 : 0, r = col & 7;
-            const uint32_t in = (col >> 3) * 64 + g * 16;
-            const uint32_t low = (uint32_t)(r < last ? r : last) * k_row + in;
-            const uint32_t high = (uint32_t)(r + 8 < last ? r + 8 : last) * k_row + in;
+            const auto from = part_of(kp, from_k[s], valid[s], k_row);
 #pragma unroll
-            for (int j = 0; j < S::kK; j += 2) {
-                k[s][j] = fetch<STREAM, u32x4>(kp + from_k[s] + low + j * 64);
-                k[s][j + 1] = fetch<STREAM, u32x4>(kp + from_k[s] + high + j * 64);
-            }
+            for (int j = 0; j < S::kK; ++j) k[s][j] = fetch<STREAM, u32x4>(from, k_at[j % 4] + j / 4 * 256);
         }
     };
-    auto swap_k = [&]() {
+    const uint32_t odd = col & 1 ? ~0u : 0u, high = col & 2 ? ~0u : 0u;
+    auto turn4 = [&](u32x4 &r0, u32x4 &r1, u32x4 &r2, u32x4 &r3) {
 #pragma unroll
-        for (int s = 0; s < S::kSub; ++s)
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = pick(odd, from_lane<0xB1>(r1[e]), r0[e]), a1 = pick(odd, r1[e], from_lane<0xB1>(r0[e]));
+            const uint32_t a2 = pick(odd, from_lane<0xB1>(r3[e]), r2[e]), a3 = pick(odd, r3[e], from_lane<0xB1>(r2[e]));
+            r0[e] = pick(high, from_lane<0x4E>(a2), a0);
+            r1[e] = pick(high, from_lane<0x4E>(a3), a1);
+            r2[e] = pick(high, a2, from_lane<0x4E>(a0));
+            r3[e] = pick(high, a3, from_lane<0x4E>(a1));
+        }
+    };
+    auto turn = [&]() {
+        if constexpr (S::kK == 2) {
+            // lanes 0..31 turn the first part, lanes 32..63 the second
+            swap_halves(k[0][0], k[1][0]);
+            swap_halves(k[0][1], k[1][1]);
+            turn4(k[0][0], k[0][1], k[1][0], k[1][1]);
+            swap_halves(k[0][0], k[0][1]);   // now k[j][s] is piece j of part s
+            swap_halves(k[1][0], k[1][1]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < S::kK; j += 2)
+            for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // lanes 8..15 of 16 take the low half of their row from
-                    // lane - 8, lanes 0..7 the high half of theirs from lane + 8
-                    const int low = (int)k[s][j][e], high = (int)k[s][j + 1][e];
-                    k[s][j][e] = (uint32_t)__builtin_amdgcn_update_dpp(low, high, 0x128, 0xF, 0xC, false);
-                    k[s][j + 1][e] = (uint32_t)__builtin_amdgcn_update_dpp(high, low, 0x128, 0xF, 0x3, false);
-                }
+                for (int j = 0; j < S::kK; j += 4) turn4(k[s][j], k[s][j + 1], k[s][j + 2], k[s][j + 3]);
+        }
     };
     auto load_v = [&](const int *valid) {
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
-            const int last = valid[s] > 0 ? valid[s] - 1 : 0;
+            const auto from = part_of(vp, from_v[s], valid[s], v_row);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * g + i;
-                const uint32_t at = (uint32_t)(r < last ? r : last) * v_row + col * S::kVBytes;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < S::kV; ++c) v[s][i][c] = fetch<STREAM, VP>(vp + from_v[s] + at + c * 256);
-            }
+                for (int c = 0; c < S::kV; ++c) v[s][i][c] = fetch<STREAM, VP>(from, v_at[i] + c * 256);
         }
     };
 
@@ -258,40 +298,36 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
         locate(key, valid);
         load_k(valid);
         load_v(valid);
-        if constexpr (!ONE) look_up(key + step);
+        look_up(key + step);
     }
     for (; key < end; key += step) {
         float x[S::kSub][4];
-        swap_k();
-        // (two sums per part, so that no product waits for the one before)
-        f4 c[S::kSub][2];
+        turn();
+        f4 c[S::kSub];
 #pragma unroll
-        for (int s = 0; s < S::kSub; ++s) c[s][0] = c[s][1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < S::kSub; ++s) c[s] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < S::kK; ++j) {
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int s = 0; s < S::kSub; ++s)
-                    c[s][j & 1] = mma16(__builtin_bit_cast(h8, k[s][j]), __builtin_bit_cast(h8, q[j]), c[s][j & 1]);
+                    c[s] = mma16(__builtin_bit_cast(h8, S::kK == 2 ? k[j][s] : k[s][j]), __builtin_bit_cast(h8, q[j]), c[s]);
             } else {
                 const f4 qq = __builtin_bit_cast(f4, q[j]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int s = 0; s < S::kSub; ++s)
-                        c[s][e & 1] = mma4(__builtin_bit_cast(f4, k[s][j])[e], qq[e], c[s][e & 1]);
+                    for (int s = 0; s < S::kSub; ++s) c[s] = mma4(__builtin_bit_cast(f4, k[s][j])[e], qq[e], c[s]);
             }
         }
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[s][i] = (c[s][0][i] + c[s][1][i]) * mul;
+            for (int i = 0; i < 4; ++i) x[s][i] = c[s][i] * mul;
         int valid_next[S::kSub];
-        if constexpr (!ONE) {
-            locate(key + step, valid_next);
-            load_k(valid_next);
-            look_up(key + 2 * step);
-        }
+        locate(key + step, valid_next);
+        load_k(valid_next);
+        look_up(key + 2 * step);
         bool partial = false;
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) partial |= valid[s] < 16;
@@ -299,12 +335,8 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
 #pragma unroll
             for (int s = 0; s < S::kSub; ++s)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool on = 4 * g + i < valid[s];
-                    x[s][i] = on ? x[s][i] : -__builtin_inff();
-#pragma unroll
-                    for (int c = 0; c < S::kV; ++c) v[s][i][c] = on ? v[s][i][c] : VP(0u);
-                }
+                for (int i = 0; i < 4; ++i)
+                    x[s][i] = 4 * g + i < valid[s] ? x[s][i] : -__builtin_inff();
         }
         float top = x[0][0];
 #pragma unroll
@@ -349,7 +381,7 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
                 for (int i = 0; i < 4; ++i) {
                     const _Float16 w = (_Float16)x[s][i];
                     hi[4 * s + i] = w;
-                    lo[4 * s + i] = (_Float16)(x[s][i] - (float)w);
+                    lo[4 * s + i] = (_Float16)fmaf(-1.0f, (float)w, x[s][i]);
                 }
 #pragma unroll
             for (int e = 0; e < S::kOut; ++e) {
@@ -363,7 +395,6 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
                 o[e] = mma16(__builtin_bit_cast(h8, w), lo, o[e]);
             }
         }
-        if constexpr (ONE) break;
         load_v(valid_next);
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) valid[s] = valid_next[s];
@@ -371,7 +402,7 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
 
     // join the waves (those that have keys)
     const int tiles = n <= S::kKeys ? 1 : (end - begin + S::kKeys - 1) / S::kKeys;
-    const int waves = tiles < (int)(blockDim.x >> 6) ? tiles : blockDim.x >> 6;
+    const int waves = tiles < kWaves ? tiles : kWaves;
     if (wave < waves) {
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
@@ -393,7 +424,7 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
     }
     __syncthreads();
     const bool whole = n <= sp.chunk;   // this chunk is the row's only one
-    for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
+    for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * kWaves) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = s_m[0][r];
         for (int w = 1; w < waves; ++w) m = fmaxf(m, s_m[w][r]);
@@ -415,6 +446,11 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
             }
         }
     }
+}
+
+template <typename T, int D, bool PAGED, bool STREAM>
+__global__ __launch_bounds__(64 * kWaves, D * (int)sizeof(T) <= 128 ? 4 : 3) void attn_kernel(AttnArgs a, AttnSplit sp) {
+    attn_workgroup<T, D, PAGED, STREAM>(a, sp);
 }
 
 // Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
@@ -467,58 +503,44 @@ namespace {
 
 struct Plan {
     int64_t chunk, chunks, q_tiles, held;
-    int waves;
-    bool one;
 };
 
-// How a call is cut into workgroups of `waves` waves over `chunk` keys. Times
-// below are of whole calls, 16 query heads of 128 over 8 in float16 or 12 of 64
-// over 12 in float32.
-Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
+// How a call is cut into workgroups over `chunk` keys. (Device times below: 16
+// query heads of 128 over 8 in float16 unless they say otherwise.)
+// A row of up to kWhole keys is one workgroup, and the call one launch: 16 x 500
+// keys 11.0 us against 12.2 cut in four, 256 x 600 98.6 against 104.9 in two; a
+// longer one takes longer alone than the second launch costs (8 x 1500: 18.9
+// against 12.1 in four). Then kMany workgroups (the card holds 768 at a time:
+// requests end at different keys, and pieces even that out; 32 x 500..16384 180
+// us, 191 with 2048) of kLeast keys or more (32 x 62..2001 30.4 us, 29.7 with
+// 512, 30.3 with 256; 12 heads of 64 in float32, 16 x 5..1503 24.8, 25.9, 22.5;
+// 8 x 1500 12.1, 12.2, 13.6), and at least kFew of them, one per CU (8 x 1500
+// 13.7 us with 384).
+constexpr int64_t kWhole = 640, kMany = 4096, kLeast = 384, kFew = 256;
+Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len) {
     Plan p;
     p.q_tiles = (rows + kQ - 1) / kQ;
     p.held = rows < kQ ? rows : kQ;
-    const int64_t units = batch * kv_heads * p.q_tiles;
-    const int64_t tile = dtype == 0 && head_dim == 128 ? 16 : 32;
-    // Short rows: a tile per wave, one launch, as long as one round of
-    // workgroups holds them (256 CUs; 64 KB of LDS hold the waves' sums): 8
-    // requests of up to 130 keys 6.2 us against 8.5 in two launches of four
-    // waves, one of 452 keys 8.4 against 10.2; but 480 units of up to 250 keys
-    // 14.0 against 12.1. Up to four tiles both forms are one launch of four
-    // waves.
-    const int64_t tiles = (max_len + tile - 1) / tile;
-    p.one = tiles <= 4 || (tiles <= 16 && units <= 256 && tiles * p.held * (head_dim + 4) <= 16000);
-    if (p.one) {
-        p.waves = tiles > 0 ? (int)tiles : 1;
-        p.chunk = p.waves * tile;
-        p.chunks = 1;
-        return p;
-    }
-    p.waves = kWaves;
-    const int64_t step = kWaves * 32;
+    const int64_t units = batch * kv_heads * p.q_tiles, step = kWaves * 32;
     const int64_t keys = (max_len + step - 1) / step * step;
-    // About 4096 workgroups (the card holds 768: rows end at different keys, and
-    // small pieces even that out), of 384 keys or more (16 x 1503 keys in
-    // float32: 22.4 us, 24.4 with 512, 22.2 with 256; 32 x 62..2001 keys in
-    // float16: 28.4, 28.4, 30.1), and of fewer where the card would be empty.
-    int64_t chunk = units * keys / 4096;
-    if (chunk < 384) chunk = 384;
-    if (units * ((keys + chunk - 1) / chunk) < 512) chunk = units * keys / 512;
+    int64_t chunk = keys;
+    if (keys > kWhole) {
+        chunk = units * keys / kMany;
+        if (chunk < kLeast) chunk = kLeast;
+        if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = units * keys / kFew;
+    }
     if (chunk < step) chunk = step;
     chunk = (chunk + step - 1) / step * step;
-    if (chunk >= keys) chunk = keys > step ? keys : step;
-    p.chunk = chunk;
-    p.chunks = keys > 0 ? (keys + chunk - 1) / chunk : 1;
+    p.chunk = chunk < keys ? chunk : keys > step ? keys : step;
+    p.chunks = keys > 0 ? (keys + p.chunk - 1) / p.chunk : 1;
     return p;
 }
 
 template <typename T, int D, bool PAGED, bool STREAM>
 void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
     const dim3 grid(a.kv_heads, a.batch, (unsigned)(p.q_tiles * p.chunks));
-    const unsigned threads = 64 * p.waves;
-    const size_t lds = (size_t)p.waves * sp.held * (D + 4) * sizeof(float);
-    if (p.one) attn_kernel<T, D, PAGED, false, true><<<grid, threads, lds, st>>>(a, sp);
-    else attn_kernel<T, D, PAGED, STREAM, false><<<grid, threads, lds, st>>>(a, sp);
+    const size_t lds = (size_t)kWaves * sp.held * (D + 4) * sizeof(float);
+    attn_kernel<T, D, PAGED, STREAM><<<grid, 64 * kWaves, lds, st>>>(a, sp);
 }
 
 template <typename T, int D>
@@ -545,20 +567,20 @@ hipError_t launch(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStre
 
 int64_t attn_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim,
                              int dtype) {
-    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
+    const Plan p = plan(batch, kv_heads, rows, max_len);
     return p.chunks > 1 ? batch * kv_heads * rows * p.chunks * (head_dim + 2) * 4 : 0;
 }
 
 bool attn_fits(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     // a launch's grid: threads of x in 32 bits, 65536 workgroups in y and z
-    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
+    const Plan p = plan(batch, kv_heads, rows, max_len);
     if (batch == 0 || rows == 0) return true;
     if (kv_heads > (1 << 22) - 1 || batch > 65536 || p.q_tiles > 65536 || p.q_tiles * p.chunks > 65536) return false;
     return p.chunks == 1 || rows <= 65536;
 }
 
 hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
-    Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len, head_dim, dtype);
+    Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len);
     if (!workspace && p.chunks > 1) {
         p.chunk = (a.max_len + 31) / 32 * 32;
         p.chunks = 1;
@@ -568,7 +590,7 @@ hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspa
     sp.chunks = (int32_t)p.chunks;
     sp.q_tiles = (int32_t)p.q_tiles;
     sp.held = (int32_t)p.held;
-    sp.page_magic = a.table ? ((1ull << 32) + a.page / 16 - 1) / (a.page / 16) : 0;
+    sp.page_magic = a.table ? (uint32_t)(((1ull << 32) + a.page / 16 - 1) / (a.page / 16)) : 0;
     if (p.chunks > 1) {
         sp.sums = static_cast<float *>(workspace);
         sp.stats = sp.sums + (int64_t)a.batch * a.kv_heads * a.rows * p.chunks * head_dim;
