@@ -312,15 +312,17 @@ bool four_rows(int64_t wgs, int64_t keys, int head_dim) {
 
 // Against mnb_attn.hip's kernel, which reads all keys again for every 16 rows
 // but splits them over workgroups as finely as it takes: that one wins while
-// its rows of tiles are few. Measured over 1500 keys, D = 64, 12 heads, us:
-//   1 request of 62 rows (48 row tiles)     10.5 (that one)  13.9 (this one)
-//   1 of 224 (168)                          13.7             14.1
-//   1 of 448 (336)                          20.9             15.0
-//   4 of 62 (192)                           16.4             15.0
-//   8 of 448 (2688)                        101.6             31.7
+// its rows of tiles are few. Measured over 1500 keys, 12 heads of 64, us:
+//   1 request of 62 rows (48 row tiles)     10.2 (that one)  14.3 (this one)
+//   1 of 224 (168)                          14.3             15.1
+//   4 of 62 (192)                           14.3             15.1
+//   1 of 448 (336)                          21.0             15.1
+//   8 of 62 (384)                           21.2             15.6
+//   8 of 448 (2688)                         82.1             31.1
+// and 4 of 62 with 16 heads of 128 over 8 (256) 22.6 and 22.2.
 bool cross_many(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     const int64_t tiles = (rows + 15) / 16;
-    return dtype == 1 && rows > 16 && batch * kv_heads >= (192 + tiles - 1) / tiles;
+    return dtype == 1 && rows > 16 && batch * kv_heads >= (256 + tiles - 1) / tiles;
 }
 
 bool cross_fits(const AttnArgs &a, int head_dim) {
