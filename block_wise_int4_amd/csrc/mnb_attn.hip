@@ -525,9 +525,11 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len) {
     const int64_t keys = (max_len + step - 1) / step * step;
     int64_t chunk = keys;
     if (keys > kWhole) {
-        chunk = units * keys / kMany;
+        // (in float64: requests x heads x rows x keys may pass 64 bits)
+        const double all = (double)units * (double)keys;
+        chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
         if (chunk < kLeast) chunk = kLeast;
-        if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = units * keys / kFew;
+        if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = (int64_t)(all / kFew);
     }
     if (chunk < step) chunk = step;
     chunk = (chunk + step - 1) / step * step;
