@@ -14,6 +14,14 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 
 inline bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+struct Range {
+    uintptr_t from, to;
+};
+inline Range range(const void *p, int64_t bytes) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+    return {from, from + (uintptr_t)bytes};
+}
+
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MNB_OK : MNB_ERR_HIP; }
 
 inline int64_t dtype_bytes(int dtype) { return dtype == MNB_F16 ? 2 : 4; }
@@ -86,6 +94,14 @@ int mnb_kv_tables(const int32_t *cached, const int32_t *added, const int32_t *fr
     if (!aligned(cached, 4) || !aligned(added, 4) || !aligned(free_blocks, 4) || !aligned(block_table, 4) ||
         !aligned(lens, 4) || !aligned(starts, 4) || !aligned(slots, 8) || !aligned(taken, 4))
         return MNB_ERR_ALIGN;
+    // (workgroups read the lengths while others write: lens in the place of
+    // cached would race)
+    const Range of[] = {range(cached, 4 * B), range(added, 4 * B), range(free_blocks, 4 * n_free),
+                        range(block_table, 4 * B * max_blocks), range(lens, 4 * B), range(starts, 4 * (B + 1)),
+                        range(slots, 8 * T), range(taken, 4)};
+    for (int o = 3; o < 8; ++o)
+        for (int i = 0; i < o; ++i)
+            if (of[i].from < of[o].to && of[o].from < of[i].to) return MNB_ERR_INVALID;
     KvTablesArgs a{};
     a.cached = cached;
     a.added = added;

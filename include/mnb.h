@@ -404,8 +404,9 @@ int mnb_gemm_grouped(const void *plan_host, const void *plan_device, void *strea
  *    ignored whatever they hold, infinities and NaN included; in valid
  *    places they act as the formula says.
  *  - Strides are in elements and not negative; from one key (or value) row to
- *    the next at most 2^26. Rows of head_dim elements are contiguous. Row addresses must be 16-byte aligned: data pointers, and
- *    strides in bytes, are multiples of 16 (MNB_ERR_ALIGN otherwise).
+ *    the next at most 2^26. Rows of head_dim elements are contiguous. Row
+ *    addresses must be 16-byte aligned: data pointers, and strides in bytes,
+ *    are multiples of 16 (MNB_ERR_ALIGN otherwise).
  *    Index arrays: int32 4-byte, int64 8-byte aligned.
  *  - Results do not depend on what else runs: the same arguments give the
  *    same bits.
@@ -454,7 +455,8 @@ typedef struct mnb_kv_cache {
  * when T is 0, and the per-request arrays when B is 0.
  * All device; MNB_ERR_SHAPE: B > MNB_MAX_REQUESTS, page_size not a multiple
  * of 16 up to MNB_MAX_PAGE, B * max_blocks above 2^31 - 1, max_blocks *
- * page_size above MNB_MAX_KEYS.
+ * page_size above MNB_MAX_KEYS. MNB_ERR_INVALID: an output overlaps an input
+ * or another output (lens given in the place of cached among them).
  */
 int mnb_kv_tables(const int32_t *cached, const int32_t *added, const int32_t *free_blocks, int64_t n_free,
                   int64_t B, int64_t page_size, int64_t max_blocks, int64_t T, int32_t *block_table,

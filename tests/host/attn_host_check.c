@@ -104,6 +104,13 @@ static void check_refusals(void) {
                                          dev(6), NULL, NULL);
             CHECK(st == MNB_ERR_NULL);
         }
+    /* an output in the place of an input, or of another output */
+    CHECK(mnb_kv_tables(dev(1), dev(2), dev(3), 4, 8, 16, 8, 4, dev(4), dev(1), dev(6), dev(7), dev(8), NULL) ==
+          MNB_ERR_INVALID);
+    CHECK(mnb_kv_tables(dev(1), dev(2), dev(3), 4, 8, 16, 8, 4, dev(4), (int32_t *)dev(2) + 7, dev(6), dev(7), dev(8),
+                        NULL) == MNB_ERR_INVALID);
+    CHECK(mnb_kv_tables(dev(1), dev(2), dev(3), 4, 8, 16, 8, 4, dev(4), dev(5), dev(6), dev(7), (int32_t *)dev(6) + 8,
+                        NULL) == MNB_ERR_INVALID);
     CHECK(mnb_kv_tables(dev(1), dev(2), dev(3), 4, 65536, 16, INT64_MAX, 4, dev(4), dev(5), dev(6), dev(7), dev(8),
                         NULL) == MNB_ERR_SHAPE);
 }
