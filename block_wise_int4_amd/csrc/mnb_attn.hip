@@ -4,10 +4,10 @@
 //
 // Work: a row is up to 16 query rows of one (request, key-value head); its
 // keys are cut into chunks, and a chunk's tiles of 16 or 32 keys are taken in
-// turn by the waves of one workgroup. A wave streams its tiles from memory
-// straight into the registers that the matrix instructions read (no LDS):
-//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row, after a
-//                 four-by-four turn between registers and lanes), B = queries;
+// turn by the waves of one workgroup. A wave streams its tiles: keys whole rows
+// at a time through a place of its own in LDS, which turns them into the layout
+// of the first product, values straight into registers:
+//   S^T = K Q^T   A = keys (lane: key l % 16, 16 bytes of its row), B = queries;
 //                 the result holds, per lane, four keys 4 (l / 16) + i of one
 //                 query l % 16, which is already the B operand's layout of
 //   O^T = V^T P^T with the contraction index renumbered: A's rows are
@@ -17,14 +17,16 @@
 //                 float32 needs no shuffle at all, float16 one byte permute
 //                 per pair of keys.
 // The next tile's keys are requested as soon as the first product has read
-// this one's, its values after the second: one tile of registers, something
-// always in flight, three workgroups per CU.
+// this one's, its values after the second: something is always in flight,
+// three workgroups per CU. Turning the keys in registers instead (four by four
+// between lanes, 160 of 339 vector instructions a tile) took 8.9 us for 8 x 452
+// keys where this takes 8.1, and 22.7 against 20.2 for 62 float32 query rows
+// over 1500 keys.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
 //
 // Bound: memory where the card is full (32 requests of 500..16384 keys, 1.1 GB:
-// 178 us, 6.2 TB/s; a bare copy's read side reaches 6.8), and latency below
-// some 30 MB: a launch, the chain length - table entry - tile, and the second
-// launch are 10 us by themselves.
+// 178 us, 6.2 TB/s; a bare read reaches 6.8), and latency below some 30 MB: a
+// launch and the chain length - table entry - tile are 6 us by themselves.
 #include "mnb_attn.h"
 #include "mnb_device.h"
 
@@ -32,12 +34,13 @@ namespace mnb {
 
 namespace {
 
-constexpr int kWaves = 4;                   // of a workgroup over a chunk (eight measured the same)
+constexpr int kWaves = 4;   // of a workgroup (8 or 12: no faster where it is alone on its CU, 5% slower where not)
 constexpr int kQ = 16;                      // query rows per row of tiles
 constexpr float kLowest = -3.402823466e38f; // the reference before any key
 constexpr float kLog2e = 1.4426950408889634f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void;
 
 template <int Bytes> struct Piece;
 template <> struct Piece<16> { typedef u32x4 type; };
@@ -48,6 +51,7 @@ template <typename T, int D> struct TileShape {
     static constexpr int kRow = D * (int)sizeof(T);                 // bytes
     static constexpr int kSub = sizeof(T) == 4 && D == 128 ? 1 : 2; // 16-key parts (64 registers of K and V at D = 128)
     static constexpr int kKeys = 16 * kSub;
+    static constexpr int kTileBytes = kKeys * kRow;                 // of keys in LDS
     static constexpr int kK = kRow / 64;                            // 16-byte pieces of a K row per lane
     static constexpr int kVBytes = kRow / 16 < 16 ? kRow / 16 : 16;
     static constexpr int kV = kRow / 16 / kVBytes;                  // pieces of a V row per lane
@@ -93,23 +97,6 @@ __device__ __forceinline__ uint32_t blocks_before(uint32_t part, uint32_t magic)
 __device__ __forceinline__ int token_of(const AttnArgs &a, int row) {
     return a.rows == a.group ? 0 : (int)((uint32_t)row / (uint32_t)a.group);
 }
-
-// A value of another lane of the four (a quad permutation).
-template <int Ctrl> __device__ __forceinline__ uint32_t from_lane(uint32_t x) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, Ctrl, 0xF, 0xF, true);
-}
-
-// Lanes 32..63 of the first against lanes 0..31 of the second.
-__device__ __forceinline__ void swap_halves(u32x4 &a, u32x4 &b) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const auto w = __builtin_amdgcn_permlane32_swap(a[e], b[e], false, false);
-        a[e] = w[0];
-        b[e] = w[1];
-    }
-}
-
-__device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
 
 // Four outputs from dimension d on of a query row.
 template <typename T>
@@ -180,22 +167,20 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;   // (n may be <= 0: no tile then)
     const int rows = a.rows - q_tile * kQ < kQ ? a.rows - q_tile * kQ : kQ;
 
-    // queries: lane (query col, dimensions of its group g, as `turn` leaves the keys)
+    // queries: lane (query col, piece g of each 64-byte run)
     u32x4 q[S::kK];
     {
         const int r = q_tile * kQ + (col < rows ? col : 0), token = token_of(a, r);
         const T *src = static_cast<const T *>(a.q) + b * a.q_batch + token * a.q_row +
                        (int64_t)(h * a.group + r - token * a.group) * a.q_head;
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(src) + (S::kK == 2 ? (g & 1) * 64 + (g >> 1) * 16 : g * 64);
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(src) + g * 16;
 #pragma unroll
-        for (int j = 0; j < S::kK; ++j)
-            q[j] = *reinterpret_cast<const u32x4 *>(p + (S::kK == 2 ? j * 32 : j / 4 * 256 + j % 4 * 16));
+        for (int j = 0; j < S::kK; ++j) q[j] = *reinterpret_cast<const u32x4 *>(p + j * 64);
     }
 
     // One tile: keys, values, and where the next one is. A part (16 keys) is
     // read through a buffer that ends with its last valid key: what lies behind
     // reads as zeros, and a part without keys reads nothing.
-    u32x4 k[S::kSub][S::kK];
     VP v[S::kSub][4][S::kV];
     int valid[S::kSub];   // leading valid keys of each part
     int64_t from_k[S::kSub], from_v[S::kSub];
@@ -225,53 +210,34 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base + from), 0,
                                                  ok > 0 ? (uint32_t)(ok - 1) * row + S::kRow : 0u, 0x00020000);
     };
-    // Keys are loaded so that four lanes after another take 64 bytes of a row:
-    // the load unit serves 16 lanes in turn, one run of bytes a cycle, and a CU
-    // takes in 105 GB/s like this but 37 where every lane reads another row, as
-    // the product wants them. Load i of a lane (4 a + x, g) is piece x of row
-    // 4 a + i, and `turn` makes it piece i of row 4 a + x.
-    uint32_t k_at[4], v_at[4];
+    // Keys go through LDS, a tile of the wave's own: a load takes whole rows, 64
+    // lanes on 1 KB after another, and a read gives lane (key col, g) piece
+    // 4 j + g of its row. Pieces are permuted by the row, so that eight lanes of
+    // a read touch all banks. (The load unit serves 16 lanes in turn, four
+    // neighbours on one run of 64 bytes a cycle: a CU takes in 105 GB/s like
+    // this but 37 where every lane loads from another row.)
+    constexpr int kPieces = S::kRow / 16, kRows = 64 / kPieces;   // of a row; of a load
+    uint8_t *s_k = reinterpret_cast<uint8_t *>(s_o) + wave * S::kTileBytes;
+    uint32_t k_at[S::kK], v_at[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // (rows of two 64-byte runs: a load has eight rows, 4 a + i and 4 a + i + 2)
-        k_at[i] = S::kK == 2 ? ((col & 12) + (i & 1) + (g & 2)) * k_row + (g & 1) * 64 + (col & 3) * 16
-                             : ((col & 12) + i) * k_row + g * 64 + (col & 3) * 16;
-        v_at[i] = (4 * g + i) * v_row + col * S::kVBytes;
+    for (int j = 0; j < S::kK; ++j) {
+        const int r = j * kRows + lane / kPieces;
+        k_at[j] = (uint32_t)r * k_row + ((lane % kPieces) ^ (r & 7)) * 16;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v_at[i] = (4 * g + i) * v_row + col * S::kVBytes;
     auto load_k = [&](const int *valid) {
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) {
             const auto from = part_of(kp, from_k[s], valid[s], k_row);
 #pragma unroll
-            for (int j = 0; j < S::kK; ++j) k[s][j] = fetch<STREAM, u32x4>(from, k_at[j % 4] + j / 4 * 256);
+            for (int j = 0; j < S::kK; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)(s_k + (s * S::kK + j) * 1024), 16, k_at[j], 0, 0,
+                                                         STREAM ? 2 : 0);
         }
     };
-    const uint32_t odd = col & 1 ? ~0u : 0u, high = col & 2 ? ~0u : 0u;
-    auto turn4 = [&](u32x4 &r0, u32x4 &r1, u32x4 &r2, u32x4 &r3) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t a0 = pick(odd, from_lane<0xB1>(r1[e]), r0[e]), a1 = pick(odd, r1[e], from_lane<0xB1>(r0[e]));
-            const uint32_t a2 = pick(odd, from_lane<0xB1>(r3[e]), r2[e]), a3 = pick(odd, r3[e], from_lane<0xB1>(r2[e]));
-            r0[e] = pick(high, from_lane<0x4E>(a2), a0);
-            r1[e] = pick(high, from_lane<0x4E>(a3), a1);
-            r2[e] = pick(high, a2, from_lane<0x4E>(a0));
-            r3[e] = pick(high, a3, from_lane<0x4E>(a1));
-        }
-    };
-    auto turn = [&]() {
-        if constexpr (S::kK == 2) {
-            // lanes 0..31 turn the first part, lanes 32..63 the second
-            swap_halves(k[0][0], k[1][0]);
-            swap_halves(k[0][1], k[1][1]);
-            turn4(k[0][0], k[0][1], k[1][0], k[1][1]);
-            swap_halves(k[0][0], k[0][1]);   // now k[j][s] is piece j of part s
-            swap_halves(k[1][0], k[1][1]);
-        } else {
-#pragma unroll
-            for (int s = 0; s < S::kSub; ++s)
-#pragma unroll
-                for (int j = 0; j < S::kK; j += 4) turn4(k[s][j], k[s][j + 1], k[s][j + 2], k[s][j + 3]);
-        }
+    auto read_k = [&](int s, int j) {
+        return *reinterpret_cast<const u32x4 *>(s_k + (16 * s + col) * S::kRow + ((4 * j + g) ^ (col & 7)) * 16);
     };
     auto load_v = [&](const int *valid) {
 #pragma unroll
@@ -297,12 +263,15 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     if (key < end) {
         locate(key, valid);
         load_k(valid);
+        asm volatile("" ::: "memory");   // (in this order: the wait below counts them)
         load_v(valid);
         look_up(key + step);
     }
     for (; key < end; key += step) {
         float x[S::kSub][4];
-        turn();
+        // this tile's keys are in LDS: all but the loads after theirs, those of
+        // its values, have come back (the compiler does not wait for loads to LDS)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kSub * 4 * S::kV) : "memory");
         f4 c[S::kSub];
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) c[s] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -311,13 +280,16 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int s = 0; s < S::kSub; ++s)
-                    c[s] = mma16(__builtin_bit_cast(h8, S::kK == 2 ? k[j][s] : k[s][j]), __builtin_bit_cast(h8, q[j]), c[s]);
+                    c[s] = mma16(__builtin_bit_cast(h8, read_k(s, j)), __builtin_bit_cast(h8, q[j]), c[s]);
             } else {
                 const f4 qq = __builtin_bit_cast(f4, q[j]);
+                f4 kk[S::kSub];
+#pragma unroll
+                for (int s = 0; s < S::kSub; ++s) kk[s] = __builtin_bit_cast(f4, read_k(s, j));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int s = 0; s < S::kSub; ++s) c[s] = mma4(__builtin_bit_cast(f4, k[s][j])[e], qq[e], c[s]);
+                    for (int s = 0; s < S::kSub; ++s) c[s] = mma4(kk[s][e], qq[e], c[s]);
             }
         }
 #pragma unroll
@@ -326,7 +298,9 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
             for (int i = 0; i < 4; ++i) x[s][i] = c[s][i] * mul;
         int valid_next[S::kSub];
         locate(key + step, valid_next);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the reads of this tile are over
         load_k(valid_next);
+        asm volatile("" ::: "memory");
         look_up(key + 2 * step);
         bool partial = false;
 #pragma unroll
@@ -399,6 +373,10 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
 #pragma unroll
         for (int s = 0; s < S::kSub; ++s) valid[s] = valid_next[s];
     }
+
+    // (the tile past the end, zeros, has arrived everywhere: its place is free)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
 
     // join the waves (those that have keys)
     const int tiles = n <= S::kKeys ? 1 : (end - begin + S::kKeys - 1) / S::kKeys;
@@ -507,24 +485,28 @@ struct Plan {
 
 // How a call is cut into workgroups over `chunk` keys. (Device times below: 16
 // query heads of 128 over 8 in float16 unless they say otherwise.)
-// A row of up to kWhole keys is one workgroup, and the call one launch: 16 x 500
-// keys 11.0 us against 12.2 cut in four, 256 x 600 98.6 against 104.9 in two; a
-// longer one takes longer alone than the second launch costs (8 x 1500: 18.9
-// against 12.1 in four). Then kMany workgroups (the card holds 768 at a time:
-// requests end at different keys, and pieces even that out; 32 x 500..16384 180
-// us, 191 with 2048) of kLeast keys or more (32 x 62..2001 30.4 us, 29.7 with
-// 512, 30.3 with 256; 12 heads of 64 in float32, 16 x 5..1503 24.8, 25.9, 22.5;
-// 8 x 1500 12.1, 12.2, 13.6), and at least kFew of them, one per CU (8 x 1500
-// 13.7 us with 384).
-constexpr int64_t kWhole = 640, kMany = 4096, kLeast = 384, kFew = 256;
-Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len) {
+// A row of up to kWholeBytes of keys and values is one workgroup, and the call
+// one launch: a CU alone takes in 384 KB in the time of the second launch (one
+// token over 1500 keys, 12 heads of 64: 9.6 us against 7.6 in two launches, but
+// 9.8 against 12.3 as a program calls it; 16 x 500 keys 10.4, 12.2 cut in four);
+// where rows fill the card, up to kFullBytes (128 x 1000: 82 us, 87 cut; 32 x
+// 62..2001 29.0, 29.8; 16 x 5..1503 in float32, 12 heads of 64, 21.8, 22.8). A
+// longer one takes longer alone (8 x 400..1500: 17.7 against 11.5).
+// Then kMany workgroups (the card holds 768 at a time: requests end at different
+// keys, and pieces even that out; 32 x 500..16384 177 us, 182 with 3072) of
+// kLeast keys or more (8 x 400..1500 11.5 us, 13.5 with 256; 100 x 100..4000 of
+// two heads 44.5, 46.7), and at least kFew of them, one per CU (8 x 400..1500
+// 13.6 us with 512, 1 x 8192 13.4 against 12.0).
+constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 384, kFew = 256;
+Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.q_tiles = (rows + kQ - 1) / kQ;
     p.held = rows < kQ ? rows : kQ;
     const int64_t units = batch * kv_heads * p.q_tiles, step = kWaves * 32;
     const int64_t keys = (max_len + step - 1) / step * step;
     int64_t chunk = keys;
-    if (keys > kWhole) {
+    const int64_t whole = (units < 192 ? kWholeBytes : kFullBytes) / (2 * head_dim * (dtype == 1 ? 2 : 4));
+    if (max_len > whole) {
         // (in float64: requests x heads x rows x keys may pass 64 bits)
         const double all = (double)units * (double)keys;
         chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
@@ -541,7 +523,8 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len) {
 template <typename T, int D, bool PAGED, bool STREAM>
 void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
     const dim3 grid(a.kv_heads, a.batch, (unsigned)(p.q_tiles * p.chunks));
-    const size_t lds = (size_t)kWaves * sp.held * (D + 4) * sizeof(float);
+    const size_t join = (size_t)kWaves * sp.held * (D + 4) * sizeof(float), keys = kWaves * TileShape<T, D>::kTileBytes;
+    const size_t lds = join > keys ? join : keys;
     attn_kernel<T, D, PAGED, STREAM><<<grid, 64 * kWaves, lds, st>>>(a, sp);
 }
 
@@ -569,20 +552,20 @@ hipError_t launch(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStre
 
 int64_t attn_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim,
                              int dtype) {
-    const Plan p = plan(batch, kv_heads, rows, max_len);
+    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
     return p.chunks > 1 ? batch * kv_heads * rows * p.chunks * (head_dim + 2) * 4 : 0;
 }
 
 bool attn_fits(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     // a launch's grid: threads of x in 32 bits, 65536 workgroups in y and z
-    const Plan p = plan(batch, kv_heads, rows, max_len);
+    const Plan p = plan(batch, kv_heads, rows, max_len, head_dim, dtype);
     if (batch == 0 || rows == 0) return true;
     if (kv_heads > (1 << 22) - 1 || batch > 65536 || p.q_tiles > 65536 || p.q_tiles * p.chunks > 65536) return false;
     return p.chunks == 1 || rows <= 65536;
 }
 
 hipError_t launch_attn(const AttnArgs &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
-    Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len);
+    Plan p = plan(a.batch, a.kv_heads, a.rows, a.max_len, head_dim, dtype);
     if (!workspace && p.chunks > 1) {
         p.chunk = (a.max_len + 31) / 32 * 32;
         p.chunks = 1;
