@@ -618,3 +618,19 @@ def test_cross_many_rows_too_far_apart_for_32_bits():
     v.copy_(torch.randn(v.shape, device=DEV, generator=g))
     got = mnb.mnb_cross_attn(q, k, v)
     _check_cross(got, q, k, v, None, "f16", rows=[0, 1500, 2999])
+
+
+# ---------------------------------------------------------------------------
+# rows that are cut, and the same rows whole where there are enough of them
+
+
+@pytest.mark.parametrize("dim,page,dt,longest", [(128, 16, "f16", 1100), (64, 32, "f32", 1100), (64, 16, "f16", 2100)])
+def test_paged_rows_cut_or_whole(dim, page, dt, longest):
+    for requests in (23, 24):       # 184 and 192 rows of keys
+        lens = [longest] + [(5 * b) % 37 for b in range(requests - 2)] + [longest - 1]
+        print(f"paged {dt} dim={dim} {requests} requests, longest {longest}", flush=True)
+        q, cache, table, ln = _paged_case(requests, lens, 8, 8, dim, page, dt)
+        cut = mnb.mnb_paged_attn_workspace_bytes(requests, 8, cache, longest) > 0
+        assert cut == (requests == 23)
+        got = mnb.mnb_paged_attn(q, cache, table, ln, longest)
+        _check_paged(got, q, cache, table, ln, longest, dt)
