@@ -311,6 +311,14 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x[s][i] = 4 * g + i < valid[s] ? x[s][i] : -__builtin_inff();
+            // (values past the last valid key are zeros already, unless rows overlap)
+            if (v_row < S::kRow)
+#pragma unroll
+                for (int s = 0; s < S::kSub; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < S::kV; ++c) v[s][i][c] = 4 * g + i < valid[s] ? v[s][i][c] : VP(0u);
         }
         float top = x[0][0];
 #pragma unroll

@@ -326,12 +326,13 @@ bool cross_many(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, 
 }
 
 bool cross_fits(const AttnArgs &a, int head_dim) {
-    // the buffers' 32-bit ranges; a scale that leaves masked scores infinite; a
-    // launch's grid
+    // the buffers' 32-bit ranges; rows that do not overlap, so that those ranges
+    // hide the ones that are not valid; a scale that leaves masked scores
+    // infinite; a launch's grid
     if (!(__builtin_fabsf(a.scale) >= 1e-30f)) return false;
     const int64_t most = 0x7FFFFFFFLL, rows = a.max_len + 8 * kCrossKeys;
     const int64_t stride = a.k_row > a.v_row ? a.k_row : a.v_row;
-    return rows * stride * 2 + head_dim * 2 <= most && a.kv_heads <= (1 << 22) && ((int64_t)a.rows + 63) / 64 <= 65536;
+    return a.v_row >= head_dim && rows * stride * 2 + head_dim * 2 <= most && a.kv_heads <= (1 << 22) && ((int64_t)a.rows + 63) / 64 <= 65536;
 }
 
 hipError_t launch_cross(const AttnArgs &a, int head_dim, hipStream_t st) {

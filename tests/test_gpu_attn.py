@@ -634,3 +634,21 @@ def test_paged_rows_cut_or_whole(dim, page, dt, longest):
         assert cut == (requests == 23)
         got = mnb.mnb_paged_attn(q, cache, table, ln, longest)
         _check_paged(got, q, cache, table, ln, longest, dt)
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_cross_rows_that_overlap_in_memory(dt, queries):
+    # rows 32 elements apart: the row after the last valid one shares half its
+    # elements, a NaN among them that only dimension 42 may see
+    batch, heads, rows, n = 8, 12, 20, 5
+    gen = torch.Generator().manual_seed(3)
+    values = torch.randn((batch, heads, 32 * (rows + 1)), generator=gen).to(TD[dt])
+    values[:, :, 32 * (n - 1) + 42] = NAN
+    values = values.to(DEV)
+    v = values.as_strided((batch, rows, heads, 64), (heads * 32 * (rows + 1), 32, 32 * (rows + 1), 1))
+    k = torch.randn((batch, rows, heads, 64), generator=gen).to(TD[dt]).to(DEV)
+    q = torch.randn((batch, queries, heads, 64), generator=gen).to(TD[dt]).to(DEV)
+    got = mnb.mnb_cross_attn(q, k, v, torch.full((batch,), n, dtype=torch.int32, device=DEV))
+    nan = torch.isnan(got)
+    assert nan[..., 42].all() and not nan[..., :42].any() and not nan[..., 43:].any()
