@@ -46,10 +46,10 @@ template <int Bytes> struct Piece;
 template <> struct Piece<16> { typedef u32x4 type; };
 template <> struct Piece<8> { typedef u32x2 type; };
 
-// Registers of one tile of keys of a float16 or float32 row of D.
+// One tile of keys and values of a float16 or float32 row of D.
 template <typename T, int D> struct TileShape {
     static constexpr int kRow = D * (int)sizeof(T);                 // bytes
-    static constexpr int kSub = sizeof(T) == 4 && D == 128 ? 1 : 2; // 16-key parts (64 registers of K and V at D = 128)
+    static constexpr int kSub = sizeof(T) == 4 && D == 128 ? 1 : 2; // 16-key parts (8 KB of keys, 32 registers of V)
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kTileBytes = kKeys * kRow;                 // of keys in LDS
     static constexpr int kK = kRow / 64;                            // 16-byte pieces of a K row per lane
@@ -70,15 +70,22 @@ template <typename T> __device__ __forceinline__ float weight(float x, float ref
     return __builtin_amdgcn_exp2f(sizeof(T) == 4 ? d * kLog2e : d);
 }
 
-__device__ __forceinline__ f4 mma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ f4 mma4(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f4 mma16(h8 a, h8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mma4(float a, float b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
 
 // A load by buffer (bytes past its range read as zeros, from nowhere); STREAM
 // leaves no copy in the caches it passes, for caches of keys and values larger
 // than those.
 template <bool STREAM, typename V> __device__ __forceinline__ V fetch(__amdgpu_buffer_rsrc_t from, uint32_t at) {
-    if constexpr (sizeof(V) == 16) return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, STREAM ? 2 : 0));
-    else return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, STREAM ? 2 : 0));
+    constexpr int how = STREAM ? 2 : 0;
+    if constexpr (sizeof(V) == 16)
+        return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, how));
+    else
+        return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, how));
 }
 
 __device__ __forceinline__ int keys_of(const AttnArgs &a, int64_t b) {
@@ -121,7 +128,8 @@ struct AttnSplit {
     int32_t chunk;        // keys per chunk
     int32_t chunks;       // of max_len
     int32_t q_tiles, held;   // of `rows`; min(rows, kQ)
-    uint32_t page_magic;  // ceil(2^32 / (page / 16)), 0 for pages of 16: part * magic >> 32 = part / (page / 16) for part < 2^26
+    uint32_t page_magic;  // ceil(2^32 / (page / 16)), 0 for pages of 16: part * magic >> 32 is
+                          // part / (page / 16) for part < 2^26
     float *sums, *stats;
 };
 
@@ -129,7 +137,8 @@ template <typename T, int D, bool PAGED, bool STREAM>
 __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSplit &sp) {
     using S = TileShape<T, D>;
     typedef typename Piece<S::kVBytes>::type VP;
-    extern __shared__ __attribute__((aligned(16))) float s_o[];   // [waves][held][D + 4]
+    // first the waves' tiles of keys, then their sums [kWaves][held][D + 4]
+    extern __shared__ __attribute__((aligned(16))) float s_o[];
     __shared__ float s_m[kWaves][kQ], s_l[kWaves][kQ];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
@@ -232,8 +241,8 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
             const auto from = part_of(kp, from_k[s], valid[s], k_row);
 #pragma unroll
             for (int j = 0; j < S::kK; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)(s_k + (s * S::kK + j) * 1024), 16, k_at[j], 0, 0,
-                                                         STREAM ? 2 : 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)(s_k + (s * S::kK + j) * 1024), 16, k_at[j],
+                                                         0, 0, STREAM ? 2 : 0);
         }
     };
     auto read_k = [&](int s, int j) {
@@ -403,9 +412,10 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < S::kOut; e += 4)
-                    *reinterpret_cast<f4 *>(to + (sizeof(T) == 2 ? (4 * g + i) * S::kOut + e : 16 * e + 4 * (4 * g + i))) =
-                        f4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
+                for (int e = 0; e < S::kOut; e += 4) {
+                    const int d = sizeof(T) == 2 ? (4 * g + i) * S::kOut + e : 16 * e + 4 * (4 * g + i);
+                    *reinterpret_cast<f4 *>(to + d) = f4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
+                }
         }
     }
     __syncthreads();
@@ -435,13 +445,17 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
 }
 
 template <typename T, int D, bool PAGED, bool STREAM>
-__global__ __launch_bounds__(64 * kWaves, D * (int)sizeof(T) <= 128 ? 4 : 3) void attn_kernel(AttnArgs a, AttnSplit sp) {
+__global__ __launch_bounds__(64 * kWaves, D * (int)sizeof(T) <= 128 ? 4 : 3)
+void attn_kernel(AttnArgs a, AttnSplit sp) {
     attn_workgroup<T, D, PAGED, STREAM>(a, sp);
 }
 
 // Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
 // D / 4 lanes, which take every 2^shift-th chunk; then their sums are added.
-// (Small and without a division: the launch is as long as its latencies.)
+// Bound: latency (2.4 us alone, 4.5 right behind the first launch), so small and
+// without a division. The first launch's last workgroups could join instead, but
+// their pieces' way past the XCDs' L2s took as long: 25.4 us against 24.8 for 16
+// float32 requests of up to 1503 keys.
 constexpr int kJoin = 256;
 template <typename T, int D>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, AttnSplit sp, int shift) {
