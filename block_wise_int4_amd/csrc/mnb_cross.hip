@@ -42,7 +42,9 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-__device__ __forceinline__ f16v mma32(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f16v mma32(h8 a, h8 b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
 
 // Where 16-byte piece c of LDS row `row` is: c ^ swizzle(row). Sixteen rows
 // (of one piece) and eight rows by two adjacent pairs of pieces (the two
@@ -297,13 +299,15 @@ template <int D, int R> void launch_rows(const AttnArgs &a, hipStream_t st) {
 
 // Which of the two forms: four waves of rows where workgroups of 128 rows fill
 // the chip (at D = 128, which the matrix unit bounds, a quarter of it will do)
-// or the keys are few; two groups otherwise. Measured over 1500 keys, us:
-//   384 workgroups of 128 rows, D = 64:   31.9 (four) 28.0 (two groups)
-//   768                                   54.6        58.1
-//   48                                    22.9        15.0
-//   512, D = 128                          64.6        80.8
-//   160, D = 128, 400 keys                14.7        16.7
-//   192, D = 64, 100 keys                  6.4         7.5
+// or the keys are few; two groups otherwise. Measured with 512 query rows over
+// 1500 keys, us:
+//    96 workgroups of 128 rows, D = 64:   24.1 (four) 16.3 (two groups)
+//   384                                   35.1        32.3
+//   768                                   56.5        63.1
+//    96, D = 128                          32.8        24.6
+//   192, D = 128                          35.1        36.6
+//   192, D = 64, 100 keys                  6.9         7.4
+//    96, D = 64, 100 keys                  6.3         5.6
 bool four_rows(int64_t wgs, int64_t keys, int head_dim) {
     return wgs >= (head_dim == 128 ? 128 : 512) || (wgs >= 128 && keys <= 256);
 }
@@ -311,18 +315,20 @@ bool four_rows(int64_t wgs, int64_t keys, int head_dim) {
 }  // namespace
 
 // Against mnb_attn.hip's kernel, which reads all keys again for every 16 rows
-// but splits them over workgroups as finely as it takes: that one wins while
-// its rows of tiles are few. Measured over 1500 keys, 12 heads of 64, us:
-//   1 request of 62 rows (48 row tiles)     10.2 (that one)  14.3 (this one)
-//   1 of 224 (168)                          14.3             15.1
-//   4 of 62 (192)                           14.3             15.1
-//   1 of 448 (336)                          21.0             15.1
-//   8 of 62 (384)                           21.2             15.6
-//   8 of 448 (2688)                         82.1             31.1
-// and 4 of 62 with 16 heads of 128 over 8 (256) 22.6 and 22.2.
+// but needs no step in common: that one wins while its rows of tiles are few.
+// Measured over 1500 keys, 12 heads of 64, us:
+//   4 requests of 62 rows (192 row tiles)   10.8 (that one)  15.1 (this one)
+//   1 of 340 (264)                          13.8             15.2
+//   8 of 62 (384)                           14.8             15.6
+//   4 of 200 (624)                          19.7             16.0
+//   2 of 448 (672)                          20.6             15.9
+//   8 of 448 (2688)                         66.3             30.5
+// over 400 keys, 12 of 62 (576) 10.6 and 8.7; with 16 heads of 128 over 8, 4 of
+// 62 (256) 14.3 and 22.0, 1 of 448 (448) 20.5 and 22.6, 2 of 448 (896) 36.5 and
+// 24.3.
 bool cross_many(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     const int64_t tiles = (rows + 15) / 16;
-    return dtype == 1 && rows > 16 && batch * kv_heads >= (256 + tiles - 1) / tiles;
+    return dtype == 1 && rows > 16 && batch * kv_heads >= (512 + tiles - 1) / tiles;
 }
 
 bool cross_fits(const AttnArgs &a, int head_dim) {
@@ -332,7 +338,8 @@ bool cross_fits(const AttnArgs &a, int head_dim) {
     if (!(__builtin_fabsf(a.scale) >= 1e-30f)) return false;
     const int64_t most = 0x7FFFFFFFLL, rows = a.max_len + 8 * kCrossKeys;
     const int64_t stride = a.k_row > a.v_row ? a.k_row : a.v_row;
-    return a.v_row >= head_dim && rows * stride * 2 + head_dim * 2 <= most && a.kv_heads <= (1 << 22) && ((int64_t)a.rows + 63) / 64 <= 65536;
+    return a.v_row >= head_dim && rows * stride * 2 + head_dim * 2 <= most && a.kv_heads <= (1 << 22) &&
+           ((int64_t)a.rows + 63) / 64 <= 65536;
 }
 
 hipError_t launch_cross(const AttnArgs &a, int head_dim, hipStream_t st) {

@@ -31,7 +31,9 @@ constexpr int kTabTokens = 256;                    // tokens per workgroup: one 
 __device__ __forceinline__ int32_t blocks_in(int32_t x, uint64_t magic) {
     return (int32_t)(((uint32_t)x >> 4) * magic >> 32);
 }
-__device__ __forceinline__ int32_t blocks_for(int32_t x, uint64_t magic) { return x > 0 ? blocks_in(x - 1, magic) + 1 : 0; }
+__device__ __forceinline__ int32_t blocks_for(int32_t x, uint64_t magic) {
+    return x > 0 ? blocks_in(x - 1, magic) + 1 : 0;
+}
 
 // Largest i < n with first[i] <= x (first[0] <= x; ascending).
 __device__ __forceinline__ int last_not_above(const int64_t *first, int n, int64_t x) {

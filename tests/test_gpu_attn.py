@@ -652,3 +652,32 @@ def test_cross_rows_that_overlap_in_memory(dt, queries):
     got = mnb.mnb_cross_attn(q, k, v, torch.full((batch,), n, dtype=torch.int32, device=DEV))
     nan = torch.isnan(got)
     assert nan[..., 42].all() and not nan[..., :42].any() and not nan[..., 43:].any()
+
+
+# ---------------------------------------------------------------------------
+# shapes of more row tiles, for the forms that only many of them take
+
+MORE = [(70, 70, 100, 3, 3, 128), (100, 64, 32, 2, 1, 64), (600, 20, 1, 1, 1, 64), (2, 1100, 300, 4, 4, 128),
+        (2, 1100, 129, 4, 4, 64), (64, 140, 70, 8, 8, 64)]
+
+
+@pytest.mark.parametrize("batch,queries,keys,heads,kv_heads,dim", MORE)
+def test_cross_more(batch, queries, keys, heads, kv_heads, dim):
+    test_cross_many(batch, queries, keys, heads, kv_heads, dim)
+
+
+def test_cross_more_rows_too_far_apart_for_32_bits():
+    batch, queries, keys, dim = 2, 5000, 40, 64
+    buf = torch.zeros((keys - 1) * 2 ** 25 + 4 * dim, dtype=torch.float16, device=DEV)
+    k = buf.as_strided((batch, keys, 1, dim), (dim, 2 ** 25, dim, 1))
+    v = buf.as_strided((batch, keys, 1, dim), (dim, 2 ** 25, dim, 1), 2 * dim)
+    g = torch.Generator(DEV).manual_seed(3)
+    q = torch.randn((batch, queries, 1, dim), device=DEV, generator=g).half()
+    k.copy_(torch.randn(k.shape, device=DEV, generator=g))
+    v.copy_(torch.randn(v.shape, device=DEV, generator=g))
+    got = mnb.mnb_cross_attn(q, k, v)
+    _check_cross(got, q, k, v, None, "f16", rows=[0, 2500, 4999])
+
+
+def test_cross_more_rows_that_overlap_in_memory():
+    test_cross_rows_that_overlap_in_memory("f16", 100)
