@@ -672,8 +672,8 @@ def mnb_paged_attn_workspace_bytes(B, heads, cache, max_len):
 
 
 def paged_attn_workspace(q, cache, max_len):
-    """A workspace for mnb_paged_attn on q's shape (empty when the call splits
-    nothing)."""
+    """A workspace for mnb_paged_attn on exactly q's shape and this max_len
+    (empty when the call splits nothing); others may need more."""
     nbytes = mnb_paged_attn_workspace_bytes(q.shape[0], q.shape[1], cache, max_len)
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
 
@@ -720,8 +720,8 @@ def mnb_cross_attn_workspace_bytes(B, queries, keys, heads, kv_heads, head_dim, 
 
 
 def cross_attn_workspace(q, k):
-    """A workspace for mnb_cross_attn on q's and k's shapes (empty when the
-    call splits nothing)."""
+    """A workspace for mnb_cross_attn on exactly q's and k's shapes (empty when
+    the call splits nothing)."""
     nbytes = mnb_cross_attn_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3],
                                             q.dtype)
     return torch.empty(nbytes, dtype=torch.uint8, device=q.device)

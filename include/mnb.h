@@ -484,8 +484,11 @@ int mnb_kv_append(const void *k, const void *v, int64_t k_stride, int64_t v_stri
  * through `workspace` and are joined in a fixed order by a second launch:
  * device, 16-byte aligned, at least mnb_paged_attn_workspace_bytes(...) bytes
  * (0 where nothing is split; then it may be NULL), any contents, not shared
- * by calls that may overlap. MNB_ERR_INVALID if workspace_bytes is smaller,
- * or scale is not finite. B = 0 enqueues nothing.
+ * by calls that may overlap. The size is that of a call of exactly this B and
+ * max_len: fewer requests or a smaller bound can need more, being split finer.
+ * A loop over changing lengths keeps max_len at its bound, or asks again (the
+ * function looks at nothing but its arguments). MNB_ERR_INVALID if
+ * workspace_bytes is smaller, or scale is not finite. B = 0 enqueues nothing.
  */
 size_t mnb_paged_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t max_len,
                                       int dtype);

@@ -93,11 +93,11 @@ class Decoder:
     def step(self, x):
         """One new token of each request, x [batch, width]."""
         slots = self.place([1] * self.batch)
-        max_len = max(self.host_lens)
         for layer in self.layers:
             layer.append(x, slots)
             q = mnb.mnb_gemm(x, layer.q).view(self.batch, HEADS, DIM)
-            a = mnb.mnb_paged_attn(q, layer.cache, self.table, self.lens, max_len, workspace=self.work)
+            a = mnb.mnb_paged_attn(q, layer.cache, self.table, self.lens, self.max_len,
+                                   workspace=self.work)
             x = x + mnb.mnb_gemm(a.view(self.batch, WIDTH), layer.o)
             q = mnb.mnb_gemm(x, layer.cross_q).view(self.batch, 1, HEADS, DIM)
             a = mnb.mnb_cross_attn(q, *layer.states, self.frames, workspace=self.cross_work)
