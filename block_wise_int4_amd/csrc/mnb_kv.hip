@@ -16,15 +16,16 @@ namespace mnb {
 // request's sums, never read back from an entry this launch writes, so
 // nothing orders the workgroups.
 // Bound: latency (a launch, two dependent loads, a scan, ten steps of a
-// search). On the device 8 decoding requests 4.3 us, 1000 5.4, 64 prompts of
-// 26240 tokens 4.8, where an empty launch is 2.4; with a token's four searches
-// one after another (1024 tokens a workgroup) and 64-bit divisions by the page
-// it was 4.8, 9.6 and 8.1.
+// search). On the device 8 decoding requests 4.3 us, 1000 5.5, 64 prompts of
+// 26240 tokens 4.9, where an empty launch is 2.4; with a token's four searches
+// one after another (1024 tokens for 256 threads) and 64-bit divisions by the
+// page it was 4.8, 9.6 and 8.1. Many requests cost their passes: 65536 105 us, 173
+// with 1024 a pass and none requested ahead.
 // ---------------------------------------------------------------------------
-constexpr int kTabThreads = 256;
+constexpr int kTabThreads = 512;
 constexpr int kTabPer = 4;                         // requests per thread and pass
 constexpr int kScan = kTabThreads * kTabPer;       // requests per pass
-constexpr int kTabTokens = 256;                    // tokens per workgroup: one search per thread
+constexpr int kTabTokens = 512;                    // tokens per workgroup: one search per thread
 
 // x / page for 0 <= x < 2^30, page = 16 m, magic = ceil(2^32 / m): the error of
 // the product is below x / 16 * m / 2^32 < 1 / m, so the floor is exact.
@@ -56,6 +57,16 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
     const int64_t t0 = (int64_t)blockIdx.x * kTabTokens;
     const int64_t t1 = t0 + kTabTokens < a.tokens ? t0 + kTabTokens : a.tokens;
     int64_t rows_before = 0, blocks_before = 0;    // over the passes so far
+    int32_t next_cached[kTabPer], next_added[kTabPer];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kTabPer; ++i) {
+            const int b = base + tid * kTabPer + i;
+            next_cached[i] = b < a.batch ? a.cached[b] : 0;
+            next_added[i] = b < a.batch ? a.added[b] : 0;
+        }
+    };
+    fetch(0);
     for (int base = 0; base < a.batch; base += kScan) {
         const int n = a.batch - base < kScan ? a.batch - base : kScan;
         int32_t cached[kTabPer];
@@ -67,7 +78,7 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
             cached[i] = 0;
             added[i] = need[i] = len[i] = 0;
             if (b < n) {
-                const int32_t c = a.cached[base + b], d = a.added[base + b];
+                const int32_t c = next_cached[i], d = next_added[i];
                 // (past the limit nothing has a place, wherever it starts)
                 cached[i] = c < 0 ? 0 : c < limit ? c : limit;
                 added[i] = d > 0 ? d : 0;
@@ -77,6 +88,7 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(KvTablesArgs a) 
             sum_rows += added[i];
             sum_blocks += need[i];
         }
+        fetch(base + kScan);
         // exclusive prefix over the workgroup's threads
         int64_t in_rows = sum_rows, in_blocks = sum_blocks;
 #pragma unroll
@@ -165,17 +177,32 @@ hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Append: a copy of 16-byte pieces, token rows in, page rows out. A workgroup
-// takes a token, and neighbouring tokens of a page meet in the L2. Bound: memory
-// (26240 tokens of 2 x 2 KB read and written: 44.8 us, 4.8 TB/s, what a large
-// copy reaches), and the launch for a decoding step (8 tokens: 2.5 us).
+// takes `per` tokens, as many as its threads have pieces for (or one), and
+// neighbouring tokens of a page meet in the L2. Bound: memory (26240 tokens of 2
+// x 2 KB read and written: 44.7 us, 4.8 TB/s, what a large copy reaches), and
+// the launch for a decoding step (8 tokens: 2.5 us). With one token a workgroup
+// 26240 of one head of 64 took 14.9 us instead of 5.0, 100000 of two heads of 128
+// 50 instead of 30.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
-    const int row_pieces = a.row_bytes / 16, pieces = a.heads * row_pieces;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+constexpr int kAppendThreads = 256;
+
+// (SHARED: per > 1; otherwise a token's place is worked out in scalar registers)
+template <bool SHARED> __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvAppendArgs a, int per) {
+    const int row_pieces = a.row_bytes / 16, pieces = a.heads * row_pieces, both = 2 * pieces;
+    const int which = SHARED ? threadIdx.x / both : 0, first = threadIdx.x - which * both;
+    if (SHARED && which >= per) return;
+    if (!SHARED) per = 1;
+    const uint32_t parts = a.page / 16;   // of 16 tokens
+    for (int64_t t = (int64_t)blockIdx.x * per + which; t < a.tokens; t += (int64_t)gridDim.x * per) {
         const int64_t slot = a.slots[t];
-        if (slot < 0 || slot / a.page >= a.num_blocks) continue;
-        const int64_t at = slot / a.page * a.block_stride + slot % a.page * a.token_stride;
-        for (int p = threadIdx.x; p < 2 * pieces; p += 256) {
+        if (slot < 0) continue;
+        const uint64_t part = (uint64_t)slot >> 4;
+        uint64_t block;
+        if constexpr (!SHARED) block = (uint64_t)slot / (uint32_t)a.page;
+        else block = part >> 32 ? part / parts : (uint32_t)part / parts;   // (a lane's own: 64 bits are slow)
+        if (block >= (uint64_t)a.num_blocks) continue;
+        const int64_t at = (int64_t)block * a.block_stride + (slot - (int64_t)block * a.page) * a.token_stride;
+        for (int p = first; p < both; p += kAppendThreads) {
             const bool second = p >= pieces;
             const int i = second ? p - pieces : p, h = i / row_pieces;
             const int64_t to = at + h * a.head_stride + (i - h * row_pieces) * 16;
@@ -187,8 +214,12 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
 }
 
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t st) {
-    const int64_t wgs = a.tokens < 65536 ? a.tokens : 65536;
-    kv_append_kernel<<<(unsigned)wgs, 256, 0, st>>>(a);
+    const int64_t both = 2 * ((int64_t)a.heads * (a.row_bytes / 16));
+    const int per = both < kAppendThreads ? (int)(kAppendThreads / both) : 1;
+    const int64_t wgs = (a.tokens + per - 1) / per;
+    const unsigned grid = (unsigned)(wgs < 65536 ? wgs : 65536);
+    if (per > 1) kv_append_kernel<true><<<grid, kAppendThreads, 0, st>>>(a, per);
+    else kv_append_kernel<false><<<grid, kAppendThreads, 0, st>>>(a, 1);
     return hipGetLastError();
 }
 

@@ -681,3 +681,41 @@ def test_cross_more_rows_too_far_apart_for_32_bits():
 
 def test_cross_more_rows_that_overlap_in_memory():
     test_cross_rows_that_overlap_in_memory("f16", 100)
+
+
+@pytest.mark.parametrize("batch", [2047, 2048, 2049, 4100])
+def test_tables_of_many_requests(batch):
+    page, width = 16, 3
+    rng = np.random.RandomState(batch)
+    cached, added = rng.randint(-1, page * width + 2, batch), rng.randint(-1, 4, batch)
+    free = rng.permutation(3 * batch)[:batch].astype(np.int32)      # too few for all
+    table = rng.randint(-1, 50, (batch, width)).astype(np.int32)
+    tokens = int(np.maximum(added, 0).sum()) + 3
+    want = oracle.kv_tables(cached.tolist(), added.tolist(), free.tolist(), table, page, tokens)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(DEV)
+    got_table, slots = dev(table), torch.full((tokens,), 9, dtype=torch.int64, device=DEV)
+    lens, starts, slots, taken = mnb.mnb_kv_tables(dev(cached), dev(added), dev(free), got_table, page, slots)
+    for got, ref in zip((got_table, lens, starts, slots), want):
+        assert np.array_equal(got.cpu().numpy(), ref)
+    assert int(taken) == want[4]
+
+
+@pytest.mark.parametrize("heads,dim,dt", [(1, 64, "f16"), (3, 64, "f16"), (1, 128, "f32"), (5, 64, "f32"), (16, 64, "f16"),
+                                          (17, 64, "f16")])
+@pytest.mark.parametrize("tokens", [1, 3, 77])
+def test_append_of_narrow_tokens(heads, dim, dt, tokens):
+    # several tokens a workgroup: two tokens' and one token's worth of threads,
+    # tokens that do not fill the last one, slots that are left out
+    page, blocks = 16, 7
+    gen = torch.Generator().manual_seed(tokens)
+    k, v = (torch.randn((tokens, heads, dim), generator=gen).to(TD[dt]).to(DEV) for _ in range(2))
+    cache = mnb.KvCache(*(torch.full((blocks, heads, page, dim), 5.0, dtype=TD[dt], device=DEV) for _ in range(2)))
+    slots = torch.randperm(blocks * page, generator=gen)[:tokens].long()
+    slots[tokens // 2] = [-1, blocks * page, 1 << 40][heads % 3]
+    mnb.mnb_kv_append(k, v, slots.to(DEV), cache)
+    for new, got in ((k, cache.k), (v, cache.v)):
+        want = torch.full((blocks, heads, page, dim), 5.0, dtype=TD[dt])
+        for t, slot in enumerate(slots.tolist()):
+            if 0 <= slot < blocks * page:
+                want[slot // page, :, slot % page] = new[t].cpu()
+        assert torch.equal(got.cpu(), want)
