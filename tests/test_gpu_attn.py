@@ -719,3 +719,26 @@ def test_append_of_narrow_tokens(heads, dim, dt, tokens):
             if 0 <= slot < blocks * page:
                 want[slot // page, :, slot % page] = new[t].cpu()
         assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("requests,longest", [(101, 2000), (37, 4000)])
+def test_paged_row_tiles_of_large_caches(requests, longest):
+    # two row tiles a head, ordered by their keys: 202 rows of keys whole, 74 cut
+    lens = [longest // 3, 0, 1, 700, 385] + [(7 * b) % 60 for b in range(requests - 5)]
+    print(f"paged f16 {requests} requests, bound {longest}", flush=True)
+    q, cache, table, ln = _paged_case(requests, lens, 40, 2, 128, 16, "f16")
+    assert (mnb.mnb_paged_attn_workspace_bytes(requests, 40, cache, longest) > 0) == (requests == 37)
+    got = mnb.mnb_paged_attn(q, cache, table, ln, longest)
+    _check_paged(got, q, cache, table, ln, longest, "f16")
+
+
+@pytest.mark.parametrize("dt,heads,queries", [("f32", 12, 40), ("f32", 3, 50)])
+def test_cross_row_tiles_of_large_states(dt, heads, queries):
+    # one encoder's states for all requests: their sizes alone order the tiles
+    batch, keys, dim = 67, 1500, 64
+    q, k, v = _cross_case(4, batch, queries, keys, heads, heads, dim, dt)
+    k, v = k[:1].expand(batch, -1, -1, -1), v[:1].expand(batch, -1, -1, -1)
+    lens = [(11 * b) % 71 for b in range(batch)]
+    got = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    pick = [0, 1, 33, 65, 66]
+    _check_cross(got[pick], q[pick], k[pick], v[pick], [lens[b] for b in pick], dt, rows=[0, 15, 16, queries - 1])
