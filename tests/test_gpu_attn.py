@@ -742,3 +742,17 @@ def test_cross_row_tiles_of_large_states(dt, heads, queries):
     got = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
     pick = [0, 1, 33, 65, 66]
     _check_cross(got[pick], q[pick], k[pick], v[pick], [lens[b] for b in pick], dt, rows=[0, 15, 16, queries - 1])
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_cross_one_token_of_large_states(dt, shared):
+    # states past 32 MB (read past the caches, unless the requests share them)
+    batch, heads, keys, dim = 30, 6, 1500, 64
+    q, k, v = _cross_case(6, batch, 1, keys, heads, heads, dim, dt)
+    if shared:
+        k, v = k[:1].expand(batch, -1, -1, -1), v[:1].expand(batch, -1, -1, -1)
+    lens = [(131 * b) % 1700 - 50 for b in range(batch)]
+    got = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    pick = [0, 1, 7, 14, 29]
+    _check_cross(got[pick], q[pick], k[pick], v[pick], [lens[b] for b in pick], dt, rows=[0])
