@@ -135,7 +135,9 @@ struct AttnSplit {
     float *sums, *stats;
 };
 
-template <typename T, int D, bool PAGED, bool STREAM>
+// FEW: one or two waves, rows of as many tiles at most (a kernel of its own: a
+// count of waves that is read costs the others 3%).
+template <typename T, int D, bool PAGED, bool STREAM, bool FEW>
 __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSplit &sp) {
     using S = TileShape<T, D>;
     typedef typename Piece<S::kVBytes>::type VP;
@@ -275,7 +277,7 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     // passes it by more than that
     const float slack = sizeof(T) == 4 ? 5.5f : 8.0f;
 
-    const int step = kWaves * S::kKeys;
+    const int step = kWaves * S::kKeys;   // (with fewer waves there is a tile for each, and no next one)
     if (key < end) {
         locate(key, valid);
         load_k(valid);
@@ -427,7 +429,7 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     }
     __syncthreads();
     const bool whole = n <= sp.chunk;   // this chunk is the row's only one
-    for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * kWaves) {
+    for (int e = threadIdx.x; e < rows * (D / 4); e += FEW ? blockDim.x : 64 * kWaves) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = s_m[0][r];
         for (int w = 1; w < waves; ++w) m = fmaxf(m, s_m[w][r]);
@@ -451,10 +453,10 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     }
 }
 
-template <typename T, int D, bool PAGED, bool STREAM>
+template <typename T, int D, bool PAGED, bool STREAM, bool FEW>
 __global__ __launch_bounds__(64 * kWaves, D * (int)sizeof(T) <= 128 ? 4 : 3)
 void attn_kernel(AttnArgs a, AttnSplit sp) {
-    attn_workgroup<T, D, PAGED, STREAM>(a, sp);
+    attn_workgroup<T, D, PAGED, STREAM, FEW>(a, sp);
 }
 
 // Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
@@ -562,9 +564,17 @@ void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStrea
     const unsigned groups = (unsigned)(((int64_t)a.batch * a.kv_heads + kXcds - 1) / kXcds);
     const dim3 grid = p.together ? dim3((unsigned)(kXcds * p.q_tiles), groups, (unsigned)p.chunks)
                                  : dim3(a.kv_heads, a.batch, (unsigned)(p.q_tiles * p.chunks));
-    const size_t join = (size_t)kWaves * sp.held * (D + 4) * sizeof(float), keys = kWaves * TileShape<T, D>::kTileBytes;
-    const size_t lds = join > keys ? join : keys;
-    attn_kernel<T, D, PAGED, STREAM><<<grid, 64 * kWaves, lds, st>>>(a, sp);
+    // Where the card is full (768 workgroups of four waves), one or two waves where
+    // there can be no more tiles: 2000 requests of 1..40 keys, 12 heads of 64, 44 us,
+    // 65 with four; with fewer workgroups four end sooner (16 rows of 64 requests
+    // over 30 keys 5.0 us, 5.7 with one).
+    const int tiles = (sp.chunk < a.max_len ? sp.chunk : a.max_len) / TileShape<T, D>::kKeys + 1;
+    const bool few = PAGED && tiles <= 2 && (int64_t)grid.x * grid.y * grid.z > 768;
+    const int waves = few ? tiles : kWaves;
+    const size_t join = (size_t)waves * sp.held * (D + 4) * sizeof(float);
+    const size_t keys = (size_t)waves * TileShape<T, D>::kTileBytes, lds = join > keys ? join : keys;
+    if (few) attn_kernel<T, D, PAGED, STREAM, PAGED><<<grid, 64 * waves, lds, st>>>(a, sp);
+    else attn_kernel<T, D, PAGED, STREAM, false><<<grid, 64 * waves, lds, st>>>(a, sp);
 }
 
 template <typename T, int D>

@@ -756,3 +756,14 @@ def test_cross_one_token_of_large_states(dt, shared):
     got = mnb.mnb_cross_attn(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
     pick = [0, 1, 7, 14, 29]
     _check_cross(got[pick], q[pick], k[pick], v[pick], [lens[b] for b in pick], dt, rows=[0])
+
+
+@pytest.mark.parametrize("dim,dt,longest", [(64, "f16", 31), (64, "f16", 32), (128, "f16", 64), (64, "f32", 40), (128, "f32", 47)])
+def test_paged_many_short_rows(dim, dt, longest):
+    # more workgroups than the card holds, of fewer waves than usual
+    requests, heads = 500, 4
+    lens = [(b * 7) % (longest + 1) for b in range(requests)]
+    q, cache, table, ln = _paged_case(longest, lens, heads, 2, dim, 16, dt)
+    got = mnb.mnb_paged_attn(q, cache, table, ln, longest)
+    pick = list(range(0, requests, 9))
+    _check_paged(got[pick], q[pick], cache, table[pick], ln[pick], longest, dt)
