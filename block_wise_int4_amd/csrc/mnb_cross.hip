@@ -54,6 +54,13 @@ template <int D> __device__ __forceinline__ int swizzle(int row) {
     else return (row & 7) << 1 | ((row >> 3) & 1);
 }
 
+// The workgroup meets: this wave's loads into LDS have arrived, and its reads of
+// LDS are over, so that the loads requested next, by any wave, may write where
+// they read. (The compiler counts neither for loads to LDS.)
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 }  // namespace
 
 // R: waves with rows of their own; 4 / R groups of them.
@@ -169,7 +176,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
                     const _Float16 *sv, _Float16 *sv_free) {
         // the next keys and these values have arrived, and the group is done
         // with the ones before
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        meet();
         request_k(sk_free);
         request_v(sv_free);
         if (tile >= tiles) return;   // (the odd group's last step)
@@ -224,7 +231,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     f16v s0, s1;
     if (tiles > 0) {
         request_k(s_k0[group]);
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        meet();
         request_k(s_k1[group]);
         request_v(s_v0[group]);
         s0 = scores(s_k0[group]);
@@ -240,7 +247,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     if constexpr (kGroups == 2) {
         // join the groups: the odd one hands its sums over in the key buffers, each
         // of which holds half of them
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        meet();
         constexpr int kHalf = D / 64;
         static_assert(sizeof(s_k0) == kHalf * 2 * 4096, "a key buffer holds half of two waves' sums");
         auto slot = [&](int i, int e) {
@@ -256,7 +263,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
             s_ml[0] = ref;
             s_ml[1] = l;
         }
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        meet();
         if (group == 1) return;
         {
             const float to = fmaxf(ref, s_ml[0]), keep = __builtin_amdgcn_exp2f(ref - to);
