@@ -112,7 +112,9 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int64_t b, int h, i
     const int token = token_of(a, row);
     T *out = static_cast<T *>(a.out) + b * a.o_batch + token * a.o_row +
              (int64_t)(h * a.group + row - token * a.group) * a.o_head + d;
-    sum *= total == 0.0f ? 0.0f : 1.0f / total;
+    // (zeros by choice, not by a product: the sum may be 0 * infinity)
+    if (total == 0.0f) sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    else sum *= 1.0f / total;
     if constexpr (sizeof(T) == 2) {
         const u32x2 w = {as_u32(h2{(_Float16)sum.x, (_Float16)sum.y}), as_u32(h2{(_Float16)sum.z, (_Float16)sum.w})};
         *reinterpret_cast<u32x2 *>(out) = w;

@@ -281,14 +281,17 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     }
     l += __shfl_xor(l, 32);
     if (!on) return;
-    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    // (zeros by choice, not by a product: the sums may be 0 * infinity)
+    const bool none = l == 0.0f;
+    const float by = 1.0f / l;
+    auto result = [&](float sum) { return (_Float16)(none ? 0.0f : sum * by); };
     _Float16 *out = static_cast<_Float16 *>(a.out) + b * a.o_batch + token * a.o_row + hq * a.o_head;
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-            const u32x2 w = {as_u32(h2{(_Float16)(o[dt][e] * by), (_Float16)(o[dt][e + 1] * by)}),
-                             as_u32(h2{(_Float16)(o[dt][e + 2] * by), (_Float16)(o[dt][e + 3] * by)})};
+            const u32x2 w = {as_u32(h2{result(o[dt][e]), result(o[dt][e + 1])}),
+                             as_u32(h2{result(o[dt][e + 2]), result(o[dt][e + 3])})};
             *reinterpret_cast<u32x2 *>(out + 32 * dt + 2 * e + 4 * half) = w;
         }
 }

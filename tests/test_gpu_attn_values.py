@@ -1,0 +1,84 @@
+"""GPU: attention at values where its arithmetic can go wrong, in every form of
+the kernels. Each case is one query row over one run of keys, the same for all
+requests, heads and query rows of a call whose sizes choose the form.
+
+Where an output is finite, it is held to the bound of test_gpu_attn (`_bound`),
+or to the one that the test derives.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import test_gpu_attn as base
+from block_wise_int4_amd import mnb
+
+pytestmark = pytest.mark.gpu
+
+DEV, TD, NAN, INF, DIM = base.DEV, base.TD, float("nan"), float("inf"), 64
+
+# form: (batch, query rows, heads, keys); the names are the kernels' forms
+FORMS = {
+    "paged": (3, 1, 2, 70),            # one token over pages, one workgroup a row
+    "paged-short": (500, 1, 2, 20),    # fewer waves a workgroup
+    "paged-cut": (1, 1, 2, 5000),      # chunks joined by a second launch
+    "token": (3, 1, 2, 70),            # one token over an encoder's states
+    "rows": (3, 20, 2, 70),            # two row tiles
+    "many-4": (130, 20, 2, 70),        # float16: four waves of rows
+    "many-2": (130, 20, 2, 300),       # float16: two groups of keys
+}
+F16_ONLY = ("many-4", "many-2")
+ALL = [(form, dt) for form in FORMS for dt in ("f16", "f32") if not (form in F16_ONLY and dt == "f32")]
+
+
+def _call(form, dt, q, k, v, n, scale):
+    """All output rows [rows, DIM] (float64) of query q [DIM] over the first n
+    of the rows k, v [keys, DIM], NaN and infinities in the places behind."""
+    batch, queries, heads, keys = FORMS[form]
+    q, k, v = (torch.as_tensor(t, dtype=torch.float64).to(TD[dt]).to(DEV) for t in (q, k, v))
+    k, v = k.clone(), v.clone()
+    k[n:], v[n:] = NAN, INF
+    lens = torch.full((batch,), n, dtype=torch.int32, device=DEV)
+    if form.startswith("paged"):
+        blocks = -(-keys // 16)
+        pages = [torch.full((blocks, heads, 16, DIM), NAN, dtype=TD[dt], device=DEV) for _ in range(2)]
+        for page, rows in zip(pages, (k, v)):
+            whole = torch.full((blocks * 16, DIM), NAN, dtype=TD[dt], device=DEV)
+            whole[:keys] = rows
+            page.copy_(whole.view(blocks, 1, 16, DIM).expand(-1, heads, -1, -1))
+        cache = mnb.KvCache(*pages)
+        table = torch.arange(blocks, dtype=torch.int32, device=DEV).repeat(batch, 1)
+        cut = mnb.mnb_paged_attn_workspace_bytes(batch, heads, cache, keys) > 0
+        assert cut == (form == "paged-cut")
+        got = mnb.mnb_paged_attn(q.expand(batch, heads, DIM).contiguous(), cache, table, lens, keys, scale=scale)
+    else:
+        whole = [t.expand(batch, heads, keys, DIM).transpose(1, 2).contiguous() for t in (k, v)]
+        got = mnb.mnb_cross_attn(q.expand(batch, queries, heads, DIM).contiguous(), *whole, lens, scale=scale)
+    got = got.reshape(-1, DIM)
+    torch.cuda.synchronize()
+    assert torch.equal(got.nan_to_num(7.0, 8.0, 9.0), got[:1].expand_as(got).nan_to_num(7.0, 8.0, 9.0)), "rows differ"
+    return got[0].cpu().double().numpy()
+
+
+def _rand(seed, keys, dt):
+    """q [DIM], k, v [keys, DIM] as float64, of values of the type."""
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(s, generator=g).to(TD[dt]).double().numpy() for s in ((DIM,), (keys, DIM), (keys, DIM))]
+
+
+def _say(form, dt, what):
+    print(f"{form} {dt} {what}", flush=True)
+
+
+# ---------------------------------------------------------------------------
+# rows whose weights sum to zero
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_rows_without_weight_are_zeros_whatever_their_values(form, dt):
+    _say(form, dt, "no weight")
+    keys = FORMS[form][3]
+    q, k, v = _rand(1, keys, dt)
+    q[:], k[:] = 1.0, -INF
+    v[1, 3], v[keys - 2, 5], v[0, 7], v[0, 8] = INF, NAN, -INF, NAN
+    assert not _call(form, dt, q, k, v, keys - 1, 1.0).any()
