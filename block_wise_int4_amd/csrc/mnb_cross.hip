@@ -152,12 +152,20 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
         }
         return s;
     };
-    // Makes the scores of keys that are not valid (zero rows, all but `left`)
-    // -infinity, by one more product: a column that is -infinity in their rows
-    // and 0 in the others, times ones. (mul is not zero: they stay so.)
-    auto mask = [&](f16v s, int left) {
-        const u32x4 ones = {half ? 0u : 0x3C00u, 0u, 0u, 0u}, off = {half || col < left ? 0u : 0xFC00u, 0u, 0u, 0u};
-        return mma32(__builtin_bit_cast(h8, off), __builtin_bit_cast(h8, ones), s);
+    // Makes the scores of keys that are not valid (all but the first `left`)
+    // -infinity, whatever they are: a zero row's score with an infinite query is
+    // NaN. A bit per element, spread over the word it masks: no scalar registers
+    // (comparisons take a pair each, 16 at once).
+    auto mask = [&](const f16v &s, int left) {
+        const int first = left - 4 * half, count = first < 0 ? 0 : first > 28 ? 28 : first;
+        const uint32_t bits = (1u << count) - 1u;
+        f16v r;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t keep = (uint32_t)((int32_t)(bits << (31 - (e % 4 + 8 * (e / 4)))) >> 31);
+            r[e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, (float)s[e]) & keep) | (0xFF800000u & ~keep));
+        }
+        return r;
     };
     auto largest = [&](const f16v &s) {
         float top = s[0];
@@ -342,8 +350,8 @@ bool cross_many(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, 
 }
 
 bool cross_fits(const AttnArgs &a, int head_dim) {
-    // the buffers' 32-bit ranges; rows that do not overlap, so that those ranges
-    // hide the ones that are not valid; a scale that leaves masked scores
+    // the buffers' 32-bit ranges; value rows that do not overlap, so that those
+    // ranges hide the ones that are not valid; a scale that leaves masked scores
     // infinite; a launch's grid
     if (!(__builtin_fabsf(a.scale) >= 1e-30f)) return false;
     const int64_t most = 0x7FFFFFFFLL, rows = a.max_len + 8 * kCrossKeys;

@@ -82,3 +82,38 @@ def test_rows_without_weight_are_zeros_whatever_their_values(form, dt):
     q[:], k[:] = 1.0, -INF
     v[1, 3], v[keys - 2, 5], v[0, 7], v[0, 8] = INF, NAN, -INF, NAN
     assert not _call(form, dt, q, k, v, keys - 1, 1.0).any()
+
+
+# ---------------------------------------------------------------------------
+# keys that are not valid, where the query is infinite
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_infinite_queries_do_not_reach_keys_that_are_not_valid(form, dt):
+    _say(form, dt, "infinite query")
+    keys = FORMS[form][3]
+    q, k, v = _rand(2, keys, dt)
+    q[5], k[:, 5] = -INF, np.abs(k[:, 5]) + 0.5       # every valid score is -infinity
+    for n in (1, keys - 33 if keys > 33 else 3, keys - 1):
+        assert not _call(form, dt, q, k, v, n, 0.125).any(), n
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("batch,keys", [(3, 20), (130, 20), (130, 300)])
+def test_key_rows_that_overlap_in_memory(batch, keys, dt):
+    # rows 32 elements apart: the row behind the last valid one starts with that
+    # one's second half, which the query's first half meets with another sign
+    queries, heads, n = 20, 2, 5
+    g = torch.Generator().manual_seed(3)
+    flat = torch.randn((32 * (keys + 1),), generator=g).to(TD[dt])
+    flat[32 * (n - 1) + 40] = -INF
+    q1 = torch.randn((DIM,), generator=g).to(TD[dt])
+    q1[40], q1[8] = 1.0, -1.0
+    v1 = torch.randn((keys, DIM), generator=g).to(TD[dt])
+    k1 = flat.as_strided((keys, DIM), (32, 1))
+    k = flat.to(DEV).as_strided((batch, keys, heads, DIM), (0, 32, 0, 1))
+    v = v1.to(DEV)[None, :, None].expand(batch, -1, heads, -1).contiguous()
+    q = q1.to(DEV).expand(batch, queries, heads, DIM).contiguous()
+    got = mnb.mnb_cross_attn(q, k, v, torch.full((batch,), n, dtype=torch.int32, device=DEV)).reshape(-1, DIM)
+    qn, kn, vn = (t.double().numpy() for t in (q1, k1[: n - 1], v1[: n - 1]))     # (the last one weighs nothing)
+    ref, tol = oracle.attend(qn, kn, vn, DIM ** -0.5), base._bound(qn, kn, vn, DIM ** -0.5, dt)
+    base._near(base._np(got), ref[None], tol[None], "overlapping keys")
