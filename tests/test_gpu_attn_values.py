@@ -117,3 +117,44 @@ def test_key_rows_that_overlap_in_memory(batch, keys, dt):
     qn, kn, vn = (t.double().numpy() for t in (q1, k1[: n - 1], v1[: n - 1]))     # (the last one weighs nothing)
     ref, tol = oracle.attend(qn, kn, vn, DIM ** -0.5), base._bound(qn, kn, vn, DIM ** -0.5, dt)
     base._near(base._np(got), ref[None], tol[None], "overlapping keys")
+
+
+# ---------------------------------------------------------------------------
+# infinite values in valid places
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_infinite_values_in_valid_places(form, dt):
+    _say(form, dt, "infinite values")
+    keys = FORMS[form][3]
+    for n in (1, 2, keys - 1):
+        q, k, v = _rand(4, keys, dt)
+        at = n - 1 if n > 1 else 0
+        v[at, 3], v[0, 7], v[at, 7], v[at // 2, 60] = INF, -INF, -INF, -INF
+        got = _call(form, dt, q, k, v, n, DIM ** -0.5)
+        ref = oracle.attend(q, k[:n], v[:n], DIM ** -0.5)
+        assert ref[3] == INF and ref[7] == ref[60] == -INF
+        assert got[3] == INF and got[7] == -INF and got[60] == -INF, (n, got[[3, 7, 60]])
+        rest = [d for d in range(DIM) if d not in (3, 7, 60)]
+        base._near(got[rest], ref[rest], base._bound(q, k[:n], v[:n][:, rest], DIM ** -0.5, dt), f"{n} keys")
+
+
+def _infinite_values_of_small_weight(form, dt):
+    _say(form, dt, "infinite values, small weight")
+    keys = FORMS[form][3]
+    n = keys - 1
+    q, k, v = _rand(5, keys, dt)
+    q[:], k[:] = 1.0, 0.0
+    k[n // 2] = 30.0 / DIM                       # 30 above the others: these weigh 1e-13, not nothing
+    v[1, 3], v[n - 1, 9] = INF, -INF
+    v[0, 20], v[n - 1, 20] = INF, -INF           # a sum of both
+    v[2, 21] = NAN
+    got = _call(form, dt, q, k, v, n, 1.0)
+    assert got[3] == INF and got[9] == -INF and np.isnan(got[[20, 21]]).all(), got[[3, 9, 20, 21]]
+    rest = [d for d in range(DIM) if d not in (3, 9, 20, 21)]
+    ref = oracle.attend(q, k[:n], v[:n][:, rest], 1.0)
+    base._near(got[rest], ref, base._bound(q, k[:n], v[:n][:, rest], 1.0, dt), "the other dimensions")
+
+
+@pytest.mark.parametrize("form,dt", [f for f in ALL if f[0] not in F16_ONLY])
+def test_infinite_values_of_small_weight_and_of_both_signs(form, dt):
+    _infinite_values_of_small_weight(form, dt)
