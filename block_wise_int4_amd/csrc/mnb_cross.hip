@@ -46,6 +46,10 @@ __device__ __forceinline__ f16v mma32(h8 a, h8 b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ f16v mma2(float a, float b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+
 // Where 16-byte piece c of LDS row `row` is: c ^ swizzle(row). Sixteen rows
 // (of one piece) and eight rows by two adjacent pairs of pieces (the two
 // kinds of read) each touch all banks evenly.
@@ -153,19 +157,13 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
         return s;
     };
     // Makes the scores of keys that are not valid (all but the first `left`)
-    // -infinity, whatever they are: a zero row's score with an infinite query is
-    // NaN. A bit per element, spread over the word it masks: no scalar registers
-    // (comparisons take a pair each, 16 at once).
-    auto mask = [&](const f16v &s, int left) {
-        const int first = left - 4 * half, count = first < 0 ? 0 : first > 28 ? 28 : first;
-        const uint32_t bits = (1u << count) - 1u;
-        f16v r;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t keep = (uint32_t)((int32_t)(bits << (31 - (e % 4 + 8 * (e / 4)))) >> 31);
-            r[e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, (float)s[e]) & keep) | (0xFF800000u & ~keep));
-        }
-        return r;
+    // -infinity, by one more product: a column that is -infinity in their rows and 0
+    // in the others, times ones. (A score that is no number stays so: an infinite
+    // query's with a zero row. The pass below that takes such keys again leaves
+    // them out by choice.)
+    auto mask = [&](f16v s, int left) {
+        const u32x4 ones = {half ? 0u : 0x3C00u, 0u, 0u, 0u}, off = {half || col < left ? 0u : 0xFC00u, 0u, 0u, 0u};
+        return mma32(__builtin_bit_cast(h8, off), __builtin_bit_cast(h8, ones), s);
     };
     auto largest = [&](const f16v &s) {
         float top = s[0];
@@ -177,17 +175,8 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     // tiles of 32 keys: this group's are group, group + 2, ...
     const int tiles = n > 0 ? (n + kCrossKeys - 1) / kCrossKeys : 0;
     float top = 0.0f;
-    // Tile `tile`, whose scores are s: its weights and their product with the
-    // values in sv, while the scores of the group's next one (keys in sk) are
-    // taken into s_next; the keys after those and the next values are requested.
-    auto step = [&](int tile, const f16v &s, f16v &s_next, const _Float16 *sk, _Float16 *sk_free,
-                    const _Float16 *sv, _Float16 *sv_free) {
-        // the next keys and these values have arrived, and the group is done
-        // with the ones before
-        meet();
-        request_k(sk_free);
-        request_v(sv_free);
-        if (tile >= tiles) return;   // (the odd group's last step)
+    // Moves the reference where the largest score passes it by more than the slack.
+    auto follow = [&]() {
         if (__any(top > ref + kSlack)) {
             float to = fmaxf(ref, top);
             to = fmaxf(to, __shfl_xor(to, 32));
@@ -199,6 +188,19 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] *= keep;
         }
+    };
+    // Tile `tile`, whose scores are s: its weights and their product with the
+    // values in sv, while the scores of the group's next one (keys in sk) are
+    // taken into s_next; the keys after those and the next values are requested.
+    auto step = [&](int tile, const f16v &s, f16v &s_next, const _Float16 *sk, _Float16 *sk_free,
+                    const _Float16 *sv, _Float16 *sv_free) {
+        // the next keys and these values have arrived, and the group is done
+        // with the ones before
+        meet();
+        request_k(sk_free);
+        request_v(sv_free);
+        if (tile >= tiles) return;   // (the odd group's last step)
+        follow();
         s_next = scores(sk);
         // weights, rounded to float16 for the second product; their sum is
         // taken from the rounded values, so that the rounding's mean cancels
@@ -251,6 +253,49 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
         step(tile + group, s0, s1, s_k1[group], s_k0[group], s_v0[group], s_v1[group]);
         if (tile + kGroups >= tiles) break;
         step(tile + kGroups + group, s1, s0, s_k0[group], s_k1[group], s_v1[group], s_v0[group]);
+    }
+    // A float16 weight may be zero where the weight is not, and gives NaN with an
+    // infinite value. Finite values leave finite sums, so a sum that is not finite
+    // says that the wave is to take its keys again, with the weights in float32:
+    // this time by itself, straight from memory.
+    float bad = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bad = __builtin_fmaf(o[i][e], 0.0f, bad);
+    if (__builtin_expect(__any(bad != 0.0f), 0)) {
+        ref = kRefLowest;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+        for (int tile = group; tile < tiles; tile += kGroups) {
+            const uint32_t first = tile * kCrossKeys;
+            f16v s;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                s = mma32(__builtin_bit_cast(h8, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     kr, (first + col) * k_row + (2 * j + half) * 16, 0, 0)),
+                          q[j], s);
+            const int left = n - (int)first - 4 * half;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = e % 4 + 8 * (e / 4) < left ? s[e] : -__builtin_inff();
+            top = largest(s);
+            follow();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], mul, -ref));
+                const uint32_t at = (first + e % 4 + 8 * (e / 4) + 4 * half) * v_row + col * 2;
+                l += w;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    o[i] = mma2((float)__builtin_bit_cast(_Float16, __builtin_amdgcn_raw_buffer_load_b16(vr, at + 64 * i, 0, 0)),
+                                w, o[i]);
+            }
+        }
     }
     if constexpr (kGroups == 2) {
         // join the groups: the odd one hands its sums over in the key buffers, each

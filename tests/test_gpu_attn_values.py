@@ -158,3 +158,11 @@ def _infinite_values_of_small_weight(form, dt):
 @pytest.mark.parametrize("form,dt", [f for f in ALL if f[0] not in F16_ONLY])
 def test_infinite_values_of_small_weight_and_of_both_signs(form, dt):
     _infinite_values_of_small_weight(form, dt)
+
+
+# ---------------------------------------------------------------------------
+# the same in the form for many rows
+
+@pytest.mark.parametrize("form", F16_ONLY)
+def test_infinite_values_of_small_weight_among_many_rows(form):
+    _infinite_values_of_small_weight(form, "f16")
