@@ -275,9 +275,14 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     f4 o[S::kOut];
     float ref, l;
     const float mul = score_mul<T>(a.scale);
-    // weights stay below exp2(8): the reference moves only when a score
-    // passes it by more than that
-    const float slack = sizeof(T) == 4 ? 5.5f : 8.0f;
+    // The reference of the weights follows the running maximum: it moves only when
+    // a score passes the maximum that set it by more than a factor of 2^8. In
+    // float16 it lies 2^7 below that maximum: weights reach 2^15, the type's range,
+    // and count down to 2^-32 of the maximum's. (At the maximum itself the end was
+    // 2^-25, and the many small weights of a long flat row below one leading key
+    // came out as nothing. Float32 sums of 32 keys at a time lose terms below some
+    // 2^-29 of themselves in any case.)
+    const float lift = sizeof(T) == 4 ? 0.0f : 7.0f, slack = sizeof(T) == 4 ? 5.5f : 8.0f + lift;
 
     const int step = kWaves * S::kKeys;   // (with fewer waves there is a tile for each, and no next one)
     // Takes this wave's tiles; exact (float16): with the second product in float32.
@@ -362,7 +367,7 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, x[s][i]);
             if (__any(top > ref + slack)) {
-                float to = fmaxf(ref, top);
+                float to = fmaxf(ref, top - lift);
                 to = fmaxf(to, __shfl_xor(to, 16));
                 to = fmaxf(to, __shfl_xor(to, 32));
                 const float keep = weight<T>(ref, to);
@@ -400,8 +405,10 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
                             o[e] = mma4((float)pair[e & 1], x[s][i], o[e]);
                         }
             } else {
-                // the weights as a float16 pair hi + lo (22 bits): the stream
-                // leaves the matrix units idle, so the second product is free
+                // the weights as a float16 pair hi + lo (22 bits for weights above
+                // 2^-10 of the largest, fewer below: hi and lo share the smallest
+                // step): the stream leaves the matrix units idle, so the second
+                // product is free
                 h8 hi, lo;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
@@ -432,7 +439,7 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     if constexpr (sizeof(T) == 2) {
         // A float16 weight, or a pair's second part, may be zero or negative where the
         // weight is not, and gives NaN with an infinite value. Finite values leave
-        // finite sums (below 2^8 * 2^16 * 2^30 keys), so a sum that is not finite
+        // finite sums (below 2^15 * 2^16 * 2^30 keys), so a sum that is not finite
         // says that the tiles are to be taken again with the weights in float32.
         // Nothing of it is in the first pass's loop.
         float none = 0.0f;

@@ -33,7 +33,10 @@ namespace {
 
 constexpr int kCrossKeys = 32;    // keys per step of a group
 constexpr float kRefLowest = -3.402823466e38f;
-constexpr float kSlack = 8.0f;    // weights stay below exp2(8)
+// The reference lies 2^7 below the running maximum and moves when a score passes
+// that maximum by more than 2^8: weights reach 2^15, float16's range, and count
+// down to 2^-32 of the maximum's.
+constexpr float kLift = 7.0f, kSlack = 8.0f + kLift;
 
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
@@ -178,7 +181,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     // Moves the reference where the largest score passes it by more than the slack.
     auto follow = [&]() {
         if (__any(top > ref + kSlack)) {
-            float to = fmaxf(ref, top);
+            float to = fmaxf(ref, top - kLift);
             to = fmaxf(to, __shfl_xor(to, 32));
             const float keep = __builtin_amdgcn_exp2f(ref - to);
             ref = to;

@@ -166,3 +166,27 @@ def test_infinite_values_of_small_weight_and_of_both_signs(form, dt):
 @pytest.mark.parametrize("form", F16_ONLY)
 def test_infinite_values_of_small_weight_among_many_rows(form):
     _infinite_values_of_small_weight(form, "f16")
+
+
+# ---------------------------------------------------------------------------
+# weights far below the largest
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_flat_tail_far_below_one_leading_key(form, dt):
+    # A key of value 0 and n - 1 keys of value `top` 17.7 below it: the output is
+    # the tail's share, whose weights (2^-25.5) may each be off by 2^-32 of the
+    # row's reference, and by 2 (DIM + 8) u S + 2^-21 relative (see _bound, S =
+    # 17.7); the sums are of equal terms, n u; then the output's own rounding.
+    _say(form, dt, "flat tail")
+    n = FORMS[form][3] - 1
+    q, k, v = np.ones(DIM), np.zeros((n + 1, DIM)), np.zeros((n + 1, DIM))
+    lead, top = 17.75, 32768.0
+    k[0] = lead / DIM                            # (exact in float16)
+    v[1:] = top
+    got = _call(form, dt, q, k, v, n, 1.0)
+    ref = oracle.attend(q, k[:n], v[:n], 1.0)
+    u = 2.0 ** -24
+    tol = ref * (2 * (DIM + 8) * u * lead + 2.0 ** -21 + 2 * (n + 64) * u) + 1e-30
+    if dt == "f16":
+        tol += n * 2.0 ** -32 * top + ref * 2.0 ** -11 + 2.0 ** -25
+    base._near(got, ref, tol, f"{n} keys")
