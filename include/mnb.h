@@ -394,7 +394,15 @@ int mnb_gemm_grouped(const void *plan_host, const void *plan_device, void *strea
  * Shared rules, on top of the conventions above:
  *  - dtype is MNB_F32 or MNB_F16 for keys, values, queries and outputs alike.
  *    Scores, softmax statistics and the sums over keys are float32; each
- *    output is rounded once to dtype.
+ *    output is rounded once to dtype. The softmax's weights are float32 in
+ *    float32 calls. In float16 calls the product with the values takes them
+ *    as a pair of float16 numbers (22 bits; an error of up to 2^-32 of the
+ *    row's largest weight where they are smaller than 2^-10 of it). Large
+ *    float16 calls of mnb_cross_attn take them as one float16 number (11
+ *    bits, in the denominator too): those with more than 16 query rows per
+ *    key-value head, rows = Tq * Hq / Hkv, and B * Hkv * ceil(rows / 16) >=
+ *    512, unless scale or strides are unusual (|scale| < 1e-30; keys or
+ *    values of one request that span 2 GiB, or value rows that overlap).
  *  - head_dim is 64 or 128 (MNB_ERR_SHAPE otherwise). Hq query heads read Hkv
  *    key-value heads, Hq a multiple of Hkv: query head h reads head
  *    h / (Hq / Hkv).
@@ -402,7 +410,8 @@ int mnb_gemm_grouped(const void *plan_host, const void *plan_device, void *strea
  *    values. A row whose weights sum to zero (no valid key, or every score
  *    -infinity) is zeros. Keys and values in places that are not valid are
  *    ignored whatever they hold, infinities and NaN included; in valid
- *    places they act as the formula says.
+ *    places they act as the formula says in float32 (an infinite value gives
+ *    infinity, but NaN where its weight is too small for a float32).
  *  - Strides are in elements and not negative; from one key (or value) row to
  *    the next at most 2^26. Rows of head_dim elements are contiguous. Row
  *    addresses must be 16-byte aligned: data pointers, and strides in bytes,

@@ -190,3 +190,35 @@ def test_flat_tail_far_below_one_leading_key(form, dt):
     if dt == "f16":
         tol += n * 2.0 ** -32 * top + ref * 2.0 ** -11 + 2.0 ** -25
     base._near(got, ref, tol, f"{n} keys")
+
+
+# ---------------------------------------------------------------------------
+# float16 weights of the form for few rows: a pair of float16 numbers
+
+@pytest.mark.parametrize("form", ["paged", "paged-short", "paged-cut", "token", "rows"])
+def test_few_rows_keep_more_than_float16_weights(form):
+    # Scores that are exact (small whole numbers, a scale of 1/8), values whose
+    # weighted sum cancels: what is left shows the weights' own errors. Those are
+    # 2^-22 relative for the pair, 2^-32 of the reference at least, |x| u twice
+    # for a score x = s log2(e) and its difference (|s| <= 4), 2^-21 for the
+    # exponential and the joins; sums of n terms n u, and 64 u for the joins.
+    # Weights of 11 bits would be off by some 2^-12.3 / sqrt(n) of `a`.
+    _say(form, "f16", "pairs")
+    n = FORMS[form][3] - 1
+    rng = np.random.default_rng(6)
+    q, k, v = np.zeros(DIM), np.zeros((n + 1, DIM)), rng.standard_normal((n + 1, DIM))
+    q[:32] = 1.0
+    k[:, :32] = rng.integers(-1, 2, (n + 1, 32))
+    k[:, 0] += rng.integers(-3, 4, n + 1)
+    score = (k @ q / 8)[:n]
+    assert np.abs(score).max() <= 4
+    p = np.exp(score - score.max())
+    v[:n] -= (p[:, None] * v[:n]).sum(axis=0) / p.sum()
+    v = v.astype(np.float16).astype(np.float64)
+    got = _call(form, "f16", q, k, v, n, 0.125)
+    ref = oracle.attend(q, k[:n], v[:n], 0.125)
+    a = (p[:, None] * np.abs(v[:n])).sum(axis=0) / p.sum()
+    u = 2.0 ** -24
+    tol = a * 2 * (2.0 ** -22 + 2 * 4 * 1.4427 * u * 2 + 2.0 ** -21 + (n + 64) * u)
+    tol += n / p.sum() * 2.0 ** -32 * np.abs(v).max() + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
+    base._near(got, ref, tol, f"{n} keys")
