@@ -260,8 +260,10 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
     // A float16 weight may be zero where the weight is not, and gives NaN with an
     // infinite value. Finite values leave finite sums, so a sum that is not finite
     // says that the wave is to take its keys again, with the weights in float32:
-    // this time by itself, straight from memory.
-    float bad = 0.0f;
+    // this time by itself, straight from memory. So does a reference so large that
+    // the rounding of s * mul in it, which the first pass's fused weights do not
+    // share, is no small factor (2^-4 at 2^20, 2^8 at 2^32: weights out of range).
+    float bad = ref > kRefLowest && __builtin_fabsf(ref) > 0x1p20f ? 1.0f : 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -290,7 +292,7 @@ template <int D, int R> __device__ __forceinline__ void cross_workgroup(const At
             follow();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], mul, -ref));
+                const float w = __builtin_amdgcn_exp2f(s[e] * mul - ref);
                 const uint32_t at = (first + e % 4 + 8 * (e / 4) + 4 * half) * v_row + col * 2;
                 l += w;
 #pragma unroll

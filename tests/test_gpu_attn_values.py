@@ -222,3 +222,25 @@ def test_few_rows_keep_more_than_float16_weights(form):
     tol = a * 2 * (2.0 ** -22 + 2 * 4 * 1.4427 * u * 2 + 2.0 ** -21 + (n + 64) * u)
     tol += n / p.sum() * 2.0 ** -32 * np.abs(v).max() + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
     base._near(got, ref, tol, f"{n} keys")
+
+
+# ---------------------------------------------------------------------------
+# scores of any size that finite float16 rows reach
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_scores_up_to_the_largest(form, dt):
+    # rows whose products are exact in float32, and so are ties; the keys of the
+    # largest score share the output, all others weigh nothing
+    _say(form, dt, "large scores")
+    keys = FORMS[form][3]
+    _, _, v = _rand(8, keys, dt)
+    for n in (1, keys - 1):
+        for size, scale in ((300.0, 0.125), (3000.0, 0.125), (30000.0, 0.125), (30000.0, 1.7)):
+            for sign in (1.0, -1.0):
+                q = np.full(DIM, sign * size)
+                k = np.repeat((np.arange(keys) % 7 + 1.0)[:, None] * size / 15, DIM, axis=1)
+                score = k[:n, 0] * sign
+                best = np.flatnonzero(score == score.max())
+                got = _call(form, dt, q, k, v, n, scale)
+                tol = base._bound(np.zeros(DIM), k[best], v[best], 1.0, dt)      # the mean of equal weights
+                base._near(got, v[best].mean(axis=0), tol, f"{n} keys, {sign * size}, scale {scale}")
