@@ -62,7 +62,7 @@ template <typename T, int D> struct TileShape {
 };
 
 // Scores are kept as x = s * mul, weights are exp2 of differences: float16
-// folds log2(e) into mul (a finite float16 score is far from overflow);
+// folds log2(e) into mul (its scale is at most 2^80, so no score overflows);
 // float32 does not, so that scores down to the type's lowest value stay
 // finite.
 template <typename T> __device__ __forceinline__ float score_mul(float scale) {

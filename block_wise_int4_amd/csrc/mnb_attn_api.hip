@@ -64,6 +64,14 @@ int check_heads(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int6
     return attn_fits(B, Hkv, rows, Tk, (int)head_dim, dtype) ? MNB_OK : MNB_ERR_SHAPE;
 }
 
+// The scale the kernels take. Float16 scores are multiplied by scale * log2(e) at
+// once, which must not overflow: products of float16 rows are whole multiples of
+// 2^-48 and below 2^40, so at 2^80 all scores are finite and different ones 2^32
+// apart, and a larger scale has the same softmax.
+float kernel_scale(float scale, int dtype) {
+    return dtype == MNB_F16 ? copysignf(fminf(fabsf(scale), 0x1p80f), scale) : scale;
+}
+
 int check_workspace(int64_t need, const void *workspace, size_t bytes) {
     if (need == 0) return MNB_OK;
     if (!workspace) return MNB_ERR_NULL;
@@ -191,7 +199,7 @@ int mnb_paged_attn(const void *q, int64_t q_stride, const mnb_kv_cache *cache, c
     a.page = (int32_t)cache->page_size;
     a.table_width = (int32_t)max_blocks;
     a.num_blocks = (int32_t)cache->num_blocks;
-    a.scale = scale;
+    a.scale = kernel_scale(scale, cache->dtype);
     return hip_status(launch_attn(a, head_dim, cache->dtype, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -241,7 +249,7 @@ int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_att
     a.group = (int32_t)(Hq / Hkv);
     a.rows = (int32_t)rows;
     a.max_len = (int32_t)Tk;
-    a.scale = scale;
+    a.scale = kernel_scale(scale, dtype);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (cross_many(B, Hkv, rows, Tk, (int)head_dim, dtype) && cross_fits(a, (int)head_dim))
         return hip_status(launch_cross(a, (int)head_dim, st));

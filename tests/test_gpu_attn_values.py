@@ -244,3 +244,27 @@ def test_scores_up_to_the_largest(form, dt):
                 got = _call(form, dt, q, k, v, n, scale)
                 tol = base._bound(np.zeros(DIM), k[best], v[best], 1.0, dt)      # the mean of equal weights
                 base._near(got, v[best].mean(axis=0), tol, f"{n} keys, {sign * size}, scale {scale}")
+
+
+# ---------------------------------------------------------------------------
+# scales at the ends of their range
+
+@pytest.mark.parametrize("form,dt", ALL)
+def test_scales_at_the_ends_of_their_range(form, dt):
+    _say(form, dt, "scales")
+    keys = FORMS[form][3]
+    n = keys - 1
+    q, k, v = _rand(7, keys, dt)
+    zero = np.zeros(DIM)
+    for scale in (3e38, -3e38, 1e-38, 0.0):
+        got = _call(form, dt, zero, k, v, n, scale)        # every score is 0: the mean
+        base._near(got, v[:n].mean(axis=0), base._bound(zero, k[:n], v[:n], 1.0, dt), f"scale {scale}")
+    if dt == "f16":
+        q[:], k[:] = 1.0, 0.0
+        k[:, 0] = np.arange(keys) % 7 * 0.25
+        k[n // 2, 0] = 2.0
+        for scale in (1e38, 3e38):                         # the largest score takes all
+            assert np.array_equal(_call(form, dt, q, k, v, n, scale), v[n // 2])
+            worst = np.flatnonzero(k[:n, 0] == 0.0)
+            got = _call(form, dt, q, k, v, n, -scale)
+            base._near(got, v[worst].mean(axis=0), base._bound(zero, k[worst], v[worst], 1.0, dt), f"scale -{scale}")
