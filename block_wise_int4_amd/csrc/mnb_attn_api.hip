@@ -22,6 +22,11 @@ inline Range range(const void *p, int64_t bytes) {
     return {from, from + (uintptr_t)bytes};
 }
 
+// (an empty range overlaps nothing, wherever it lies)
+inline bool overlap(const Range &a, const Range &b) {
+    return a.from < b.to && b.from < a.to && a.from < a.to && b.from < b.to;
+}
+
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MNB_OK : MNB_ERR_HIP; }
 
 inline int64_t dtype_bytes(int dtype) { return dtype == MNB_F16 ? 2 : 4; }
@@ -109,7 +114,7 @@ int mnb_kv_tables(const int32_t *cached, const int32_t *added, const int32_t *fr
                         range(slots, 8 * T), range(taken, 4)};
     for (int o = 3; o < 8; ++o)
         for (int i = 0; i < o; ++i)
-            if (of[i].from < of[o].to && of[o].from < of[i].to) return MNB_ERR_INVALID;
+            if (overlap(of[i], of[o])) return MNB_ERR_INVALID;
     KvTablesArgs a{};
     a.cached = cached;
     a.added = added;
