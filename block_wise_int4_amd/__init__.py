@@ -11,9 +11,11 @@ from .mnb import (  # noqa: F401
     MnbError,
     PackedWeight,
     Plan,
+    cross_attn_workspace,
     lib,
     mnb_abi_version,
     mnb_cross_attn,
+    mnb_cross_attn_workspace_bytes,
     mnb_dequant,
     mnb_gemm,
     mnb_gemm_i8,
@@ -27,9 +29,11 @@ from .mnb import (  # noqa: F401
     mnb_pack,
     mnb_packed_bytes,
     mnb_paged_attn,
+    mnb_paged_attn_workspace_bytes,
     mnb_plan_grouped,
     mnb_quantize_act_i8,
     mnb_quantize_rtn,
     mnb_status_string,
     mnb_unpack,
+    paged_attn_workspace,
 )

@@ -30,3 +30,11 @@ def test_tables_arrays_that_overlap_are_still_refused(L):  # noqa: F811
     args = dict(cached=A, added=B, free=C, table=D, lens=E, starts=at(A, 4096), slots=at(B, 4096), taken=at(C, 4096))
     assert tables(L, **{**args, "slots": at(D, 16), "T": 1}) == INVALID
     assert tables(L, **{**args, "free": at(D, 16), "n_free": 1}) == INVALID
+
+
+def test_package_exports_what_an_attention_step_calls():
+    import block_wise_int4_amd as package
+    for name in ("KvCache", "mnb_kv_tables", "mnb_kv_append", "mnb_paged_attn", "mnb_cross_attn",
+                 "mnb_paged_attn_workspace_bytes", "mnb_cross_attn_workspace_bytes", "paged_attn_workspace",
+                 "cross_attn_workspace"):
+        assert getattr(package, name) is getattr(package.mnb, name), name
