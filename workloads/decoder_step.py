@@ -74,6 +74,8 @@ class Decoder:
         """Room for added[b] new tokens of each request: the tables' new
         entries, the lengths, and the slot of each token. The host follows the
         lengths, so that it knows what was taken without waiting for it."""
+        if any(held + n > self.max_len for held, n in zip(self.host_lens, added)):
+            raise ValueError(f"a request holds at most {self.max_len} tokens")
         slots = torch.empty(sum(added), dtype=torch.int64, device=self.device)
         lens, *_ = mnb.mnb_kv_tables(self.lens, torch.tensor(added, dtype=torch.int32, device=self.device), self.free,
                                      self.table, self.page, slots)
@@ -85,7 +87,9 @@ class Decoder:
         return slots
 
     def prompt(self, x, added):
-        """Keys and values of prompts, x [sum(added), width]."""
+        """Keys and values of prompts, x [sum(added), width]. Attention among a
+        prompt's rows is not among the operators: every layer is given the
+        embeddings x, where a model would give it the layer before's output."""
         slots = self.place(added)
         for layer in self.layers:
             layer.append(x, slots)
