@@ -22,10 +22,12 @@
 // between lanes, 160 of 339 vector instructions a tile) took 8.9 us for 8 x 452
 // keys where this takes 8.1, and 22.7 against 20.2 for 62 float32 query rows
 // over 1500 keys.
-// The waves' sums are joined in LDS, and the chunks' by a second launch.
+// The waves' sums are joined in LDS, and the chunks' by a second launch. A wave of
+// a float16 call whose sums are not finite (infinite values) takes its tiles once
+// more with float32 weights.
 //
 // Bound: memory where the card is full (32 requests of 500..16384 keys, 1.1 GB:
-// 178 us, 6.2 TB/s; a bare read reaches 6.8), and latency below some 30 MB: a
+// 176 us, 6.3 TB/s; a bare read reaches 6.8), and latency below some 30 MB: a
 // launch and the chain length - table entry - tile are 6 us by themselves.
 #include "mnb_attn.h"
 #include "mnb_device.h"
@@ -235,9 +237,11 @@ __device__ __forceinline__ void attn_workgroup(const AttnArgs &a, const AttnSpli
     // Keys go through LDS, a tile of the wave's own: a load takes whole rows, 64
     // lanes on 1 KB after another, and a read gives lane (key col, g) piece
     // 4 j + g of its row. Pieces are permuted by the row, so that eight lanes of
-    // a read touch all banks. (The load unit serves 16 lanes in turn, four
-    // neighbours on one run of 64 bytes a cycle: a CU takes in 105 GB/s like
-    // this but 37 where every lane loads from another row.)
+    // a read touch all banks. (The counters still see conflicts in 42% of the LDS
+    // cycles where rows are 256 bytes, none at 128; waves wait for LDS in less
+    // than 1% of theirs. The load unit serves 16 lanes in turn, four
+    // neighbours on one run of 64 bytes a cycle: a CU takes in 105 GB/s like this
+    // but 37 where every lane loads from another row.)
     constexpr int kPieces = S::kRow / 16, kRows = 64 / kPieces;   // of a row; of a load
     uint8_t *s_k = reinterpret_cast<uint8_t *>(s_o) + wave * S::kTileBytes;
     uint32_t k_at[S::kK], v_at[4];
@@ -519,7 +523,8 @@ void attn_kernel(AttnArgs a, AttnSplit sp) {
 // Bound: latency (2.4 us alone, 4.5 right behind the first launch), so small and
 // without a division. The first launch's last workgroups could join instead, but
 // their pieces' way past the XCDs' L2s took as long: 25.4 us against 24.8 for 16
-// float32 requests of up to 1503 keys.
+// float32 requests of up to 1503 keys, when that case was cut (it is whole now),
+// and 62 against 12 where 32 workgroups join one row.
 constexpr int kJoin = 256;
 template <typename T, int D>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, AttnSplit sp, int shift) {
@@ -574,17 +579,27 @@ struct Plan {
 // query heads of 128 over 8 in float16 unless they say otherwise.)
 // A row of up to kWholeBytes of keys and values is one workgroup, and the call
 // one launch: a CU alone takes in 384 KB in the time of the second launch (one
-// token over 1500 keys, 12 heads of 64: 9.6 us against 7.6 in two launches, but
-// 9.8 against 12.3 as a program calls it; 16 x 500 keys 10.4, 12.2 cut in four);
-// where rows fill the card, up to kFullBytes (128 x 1000: 82 us, 87 cut; 32 x
-// 62..2001 29.0, 29.8; 16 x 5..1503 in float32, 12 heads of 64, 21.8, 22.8). A
-// longer one takes longer alone (8 x 400..1500: 17.7 against 11.5).
+// token over 1500 keys, 12 heads of 64: 8.7 us against 7.6 in two launches, but
+// 9.7 against 12.3 as a program calls it; 16 x 500 keys 10.4, 12.2 cut in four).
+// A longer one takes longer alone (8 x 400..1500: 17.7 against 11.5), until there
+// are rows enough to fill the card: from kFullUnits on, three workgroups to four
+// CUs, up to kFullBytes are whole. Rows of one length gain from some 120 on, rows
+// of all lengths from some 230 (whole and cut, us; eight rows a request):
+//            2000 keys each   5..2000 keys   1200 each
+//    64        23.1  17.9      21.4  15.2    15.4  12.1
+//   128        26.1  26.0      23.0  20.5    17.3  18.3
+//   192        31.8  35.5      24.6  23.1    20.6  24.9
+//   256        41.1  45.1      27.3  27.1    26.1  29.1
+//   512        79.3  85.7      46.1  47.0    49.5  53.7
+// (the same in float32 and over heads of 64; 320 equal rows, one and a quarter a
+// CU, are the exception: 60.1 and 56.1.)
 // Then kMany workgroups (the card holds 768 at a time: requests end at different
 // keys, and pieces even that out; 32 x 500..16384 177 us, 182 with 3072) of
 // kLeast keys or more (8 x 400..1500 11.5 us, 13.5 with 256; 100 x 100..4000 of
 // two heads 44.5, 46.7), and at least kFew of them, one per CU (8 x 400..1500
 // 13.6 us with 512, 1 x 8192 13.4 against 12.0).
-constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 384, kFew = 256;
+constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 384, kFew = 256,
+                  kFullUnits = 192;
 Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.q_tiles = (rows + kQ - 1) / kQ;
@@ -592,7 +607,7 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int he
     const int64_t units = batch * kv_heads * p.q_tiles, step = kWaves * 32;
     const int64_t keys = (max_len + step - 1) / step * step;
     int64_t chunk = keys;
-    const int64_t whole = (units < 192 ? kWholeBytes : kFullBytes) / (2 * head_dim * (dtype == 1 ? 2 : 4));
+    const int64_t whole = (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim * (dtype == 1 ? 2 : 4));
     if (max_len > whole) {
         // (in float64: requests x heads x rows x keys may pass 64 bits)
         const double all = (double)units * (double)keys;
@@ -634,10 +649,11 @@ void launch_rows(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStrea
 
 template <typename T, int D>
 hipError_t launch(const AttnArgs &a, const AttnSplit &sp, const Plan &p, hipStream_t st) {
-    // Caches that the L2 (32 MB in all) cannot hold are read past it: 1.1 GB at
-    // 6.5 TB/s instead of 5.7, one token of 256 requests over 1500 states (12 heads
-    // of 64) 188 us instead of 207; smaller ones may stay there for the next call,
-    // and states that the requests share for the next request.
+    // Caches that the L2 (32 MB in all) cannot hold are read past it: requests of
+    // 8192 keys each, 1.1 GB, at 6.5 TB/s instead of 5.7 (6.3 for 500..16384 keys),
+    // one token of 256 requests over 1500 states (12 heads of 64) 188 us instead of
+    // 207; smaller ones may stay there for the next call, and states that the
+    // requests share for the next request.
     const double bytes = 2.0 * a.batch * a.kv_heads * a.max_len * D * sizeof(T);
     const bool stream = sp.q_tiles == 1 && bytes > 32e6 && a.k_batch != 0;
     if (a.table && stream) launch_rows<T, D, true, true>(a, sp, p, st);

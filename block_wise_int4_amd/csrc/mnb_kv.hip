@@ -15,8 +15,8 @@ namespace mnb {
 // binary search in the scanned sums. A token's block is worked out from the
 // request's sums, never read back from an entry this launch writes, so
 // nothing orders the workgroups.
-// Bound: latency (a launch, two dependent loads, a scan, ten steps of a
-// search). On the device 8 decoding requests 4.3 us, 1000 5.5, 64 prompts of
+// Bound: latency (a launch, two dependent loads, a scan, up to eleven steps of
+// a search). On the device 8 decoding requests 4.3 us, 1000 5.5, 64 prompts of
 // 26240 tokens 4.9, where an empty launch is 2.4; with a token's four searches
 // one after another (1024 tokens for 256 threads) and 64-bit divisions by the
 // page it was 4.8, 9.6 and 8.1. Many requests cost their passes: 65536 105 us, 173

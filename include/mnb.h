@@ -476,7 +476,8 @@ int mnb_kv_tables(const int32_t *cached, const int32_t *added, const int32_t *fr
  * [head_dim] with rows (tokens) k_stride and v_stride elements apart, token t
  * to slot slots[t] (device int64 [T]; block = slot / page_size). Slots
  * outside the cache (-1 among them) are skipped. Two tokens with one slot
- * leave either's values there. T = 0 enqueues nothing.
+ * leave parts of either there, not the same ones each time. T = 0 enqueues
+ * nothing.
  */
 int mnb_kv_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, const int64_t *slots,
                   int64_t T, const mnb_kv_cache *cache, void *stream);
