@@ -268,3 +268,26 @@ def test_scales_at_the_ends_of_their_range(form, dt):
             worst = np.flatnonzero(k[:n, 0] == 0.0)
             got = _call(form, dt, q, k, v, n, -scale)
             base._near(got, v[worst].mean(axis=0), base._bound(zero, k[worst], v[worst], 1.0, dt), f"scale -{scale}")
+
+
+# ---------------------------------------------------------------------------
+# small weights in the denominator
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("batch,dim", [(3, 64), (130, 64), (130, 128), (1030, 64)])
+@pytest.mark.parametrize("keys", [200, 65000])
+def test_small_weights_count_in_both_sums(batch, dim, keys, dt):
+    # one leading key and a flat row of weights 2^-23 below it, all values 1: the
+    # output is 1 whatever the weights, if both sums have all of them. At 65000 keys
+    # the flat row is 0.8% of the sums; each is of some keys / 2 float32 additions at
+    # most of numbers below 2^-15 of it, off by less than 2^-11 of the whole (keys / 2
+    # roundings of 2^-24 and a common factor), and the output's rounding is 2^-11.
+    print(f"small weights {dt} batch={batch} dim={dim} keys={keys}", flush=True)
+    queries, heads = 20, 2
+    k = torch.zeros((1, keys, 1, dim), dtype=TD[dt], device=DEV)
+    k[0, 0, 0] = 23 * float(np.log(2)) / dim
+    v = torch.ones_like(k)
+    q = torch.ones((batch, queries, heads, dim), dtype=TD[dt], device=DEV)
+    k, v = (t.expand(batch, keys, heads, dim) for t in (k, v))
+    got = mnb.mnb_cross_attn(q, k, v, scale=1.0)
+    base._near(base._np(got), np.ones(got.shape), np.full(got.shape, keys / 2 * 2.0 ** -24 + 2.0 ** -11))
