@@ -8,6 +8,7 @@ to another implementation when it is missing.
 """
 
 import ctypes
+import math
 import os
 import re
 import struct
@@ -55,6 +56,15 @@ class mnb_attn_view(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class mnb_kv_cache_i8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("block_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _f32 = ctypes.c_float
 _SIGNATURES = {
@@ -88,6 +98,13 @@ _SIGNATURES = {
     "mnb_cross_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
     "mnb_cross_attn": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _f32,
                               _int, _vp, _sz, _vp, _vp]),
+    "mnb_rope": (_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _int,
+                        _f32, _int, _vp]),
+    "mnb_kv_append_i8": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mnb_kv_read_i8": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp]),
+    "mnb_paged_attn_i8_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "mnb_paged_attn_i8": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _vp, _sz,
+                                 _vp, _vp]),
 }
 
 
@@ -764,4 +781,222 @@ def mnb_cross_attn(q, k, v, lens=None, scale=None, workspace=None, out=None):
         *_workspace(workspace, index, device), to, _stream_handle(index))
     if status:
         _check("mnb_cross_attn", status)
+    return out
+
+
+def _launch(fn, index, *args):
+    """Calls entry point `fn` on torch's current stream of device `index`, with
+    that device current (the null stream is the current device's)."""
+    if index < 0:
+        raise ValueError("the tensors must be on the GPU")
+    call = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args, _stream_handle(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _stream_handle(index))
+    if status:
+        _check(fn, status)
+
+
+def _head_rows(t, name, heads, dim, dtype, index, device):
+    """Address and token stride of [T, heads, dim] rows whose heads are
+    contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _check_buf(t, name, dtype, t.numel() if isinstance(t, torch.Tensor) else 0, device)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name} must be [T, {heads}, {dim}] with contiguous heads")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else 0
+
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+def rope_frequencies(rot_dim, base=10000.0, linear=1.0, stretch=1.0, by_parts=None, device="cuda"):
+    """Frequencies for mnb_rope, float64 [rot_dim / 2] radians per position, and
+    the gain that belongs to them: f_i = base^(-2 i / rot_dim), scaled for
+    contexts longer than the model was trained on by at most one of
+
+      linear    positions squeezed by this factor: f_i / linear
+      stretch   a longer base, base * stretch^(rot_dim / (rot_dim - 2)): the
+                fastest pair keeps its frequency, the slowest is divided by
+                `stretch` ("NTK-aware" scaling)
+      by_parts  (factor, trained, slow, fast): pairs that turn more than `fast`
+                times within the `trained` positions keep their frequency,
+                those that turn less than `slow` times are divided by
+                `factor`, those between are mixed in proportion; the gain is
+                0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context
+                Window Extension of Large Language Models", 2023)
+
+    Returns (freqs, gain)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if (linear != 1.0) + (stretch != 1.0) + (by_parts is not None) > 1:
+        raise ValueError("one scaling at most: linear, stretch or by_parts")
+    if not (base > 0 and linear > 0 and stretch > 0):
+        raise ValueError("base, linear and stretch must be positive")
+    if stretch != 1.0:
+        if rot_dim < 4:
+            raise ValueError("stretch needs a rot_dim of 4 or more")
+        base = base * stretch ** (rot_dim / (rot_dim - 2))
+    freqs = [base ** (-2 * i / rot_dim) / linear for i in range(rot_dim // 2)]
+    gain = 1.0
+    if by_parts is not None:
+        factor, trained, slow, fast = by_parts
+        if not (factor >= 1 and trained > 0 and 0 <= slow < fast):
+            raise ValueError("by_parts: factor >= 1, trained > 0, 0 <= slow < fast")
+        for i, f in enumerate(freqs):
+            keep = min(1.0, max(0.0, (trained * f / (2 * math.pi) - slow) / (fast - slow)))
+            freqs[i] = f * keep + f / factor * (1.0 - keep)
+        gain = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(freqs, dtype=torch.float64, device=device), gain
+
+
+def mnb_rope(q, k, positions, freqs, interleaved=False, gain=1.0, q_out=None, k_out=None):
+    """Turns queries q [T, heads, dim] and keys k [T, kv_heads, dim] (either may
+    be None; any token stride) by their positions (int32 [T]): the first
+    2 * len(freqs) dimensions of every head, pairs (i, i + half) or, interleaved,
+    (2 i, 2 i + 1); freqs float64 radians per position (rope_frequencies).
+    q_out, k_out: new tensors unless given; q and k themselves turn in place.
+    Returns (q_out, k_out)."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k must be given")
+    if not isinstance(one, torch.Tensor) or one.dim() != 3:
+        raise ValueError("q and k must be [T, heads, dim]")
+    dtype, device, index = one.dtype, one.device, one.get_device()
+    code, (T, _, dim) = dtype_code(dtype), one.shape
+    args = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args += [None, 0, None, 0, 0]
+            continue
+        if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.shape[0] != T:
+            raise ValueError(f"{name} must be [{T}, heads, {dim}]")
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype, device=device)
+        elif not isinstance(out, torch.Tensor) or out.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape")
+        heads = x.shape[1]
+        args += [*_head_rows(x, name, heads, dim, dtype, index, device),
+                 *_head_rows(out, name + "_out", heads, dim, dtype, index, device), heads]
+        if name == "q":
+            q_out = out
+        else:
+            k_out = out
+    _launch("mnb_rope", index, *args, _whole(positions, "positions", torch.int32, T, index, device),
+            _whole(freqs, "freqs", torch.float64, freqs.numel(), index, device), T, dim, 2 * freqs.numel(),
+            ROPE_INTERLEAVED if interleaved else ROPE_HALF, gain, code)
+    return (None if q is None else q_out), (None if k is None else k_out)
+
+
+class KvCacheI8:
+    """One layer's paged key-value cache in 8 bits: codes k and v int8 [blocks,
+    kv_heads, page_size, head_dim] of the same strides, scales k_scale and
+    v_scale float32 [blocks, kv_heads, page_size] of the same strides, a page's
+    tokens contiguous. dtype: of the tokens written and read and of the queries,
+    float16 or float32. Keeps the tensors and their description."""
+
+    def __init__(self, k, v, k_scale, v_scale, dtype):
+        code = dtype_code(dtype)
+        for t, name in ((k, "k"), (v, "v")):
+            _rows(t, name, 4, torch.int8)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _rows(t, name, 3, torch.float32)
+        if k.device.type != "cuda":
+            raise ValueError("k must be on the GPU")
+        _on(k.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        if k.shape != v.shape or _strides(k) != _strides(v):
+            raise ValueError("k and v must have the same shape and strides")
+        if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or _strides(k_scale) != _strides(v_scale):
+            raise ValueError("k_scale and v_scale must be [blocks, kv_heads, page_size] of the same strides")
+        self.k, self.v, self.k_scale, self.v_scale, self.dtype = k, v, k_scale, v_scale, dtype
+        self.device, self.index = k.device, k.get_device()
+        self.num_blocks, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.token_shape = (self.kv_heads, self.head_dim)
+        self._desc = mnb_kv_cache_i8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *k.shape,
+                                     *_strides(k), *_strides(k_scale), code, 0)
+        self.ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def new(cls, num_blocks, kv_heads, page_size, head_dim, dtype, device="cuda"):
+        """A cache of its own memory (not cleared: slots that nothing was
+        appended to are never read as keys)."""
+        shape = (num_blocks, kv_heads, page_size, head_dim)
+        codes = [torch.empty(shape, dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales, dtype)
+
+
+def mnb_kv_append_i8(k, v, slots, cache):
+    """mnb_kv_append into a KvCacheI8: k and v (the cache's dtype, [T, kv_heads,
+    head_dim] or [T, kv_heads * head_dim], any token stride) are quantized, a
+    scale for every token and head, and written to slots (int64 [T]; slots
+    outside the cache are skipped)."""
+    T, device, index = slots.numel(), cache.device, cache.index
+    k_stride, v_stride = _tokens(k, "k", T, cache), _tokens(v, "v", T, cache)
+    _launch("mnb_kv_append_i8", index, k.data_ptr(), v.data_ptr(), k_stride, v_stride,
+            _whole(slots, "slots", torch.int64, T, index, device), T, cache.ref)
+
+
+def mnb_kv_read_i8(slots, cache, k=None, v=None):
+    """What the slots (int64 [T]) of a KvCacheI8 stand for, codes times scales
+    rounded once to its dtype: k, v [T, kv_heads, head_dim] (new tensors unless
+    given, any token stride), zeros for slots outside the cache."""
+    T, device, index = slots.numel(), cache.device, cache.index
+    if k is None:
+        k = torch.empty((T, *cache.token_shape), dtype=cache.dtype, device=device)
+    if v is None:
+        v = torch.empty((T, *cache.token_shape), dtype=cache.dtype, device=device)
+    k_stride, v_stride = _tokens(k, "k", T, cache), _tokens(v, "v", T, cache)
+    _launch("mnb_kv_read_i8", index, _whole(slots, "slots", torch.int64, T, index, device), T, cache.ref, k.data_ptr(),
+            v.data_ptr(), k_stride, v_stride)
+    return k, v
+
+
+def mnb_paged_attn_i8_workspace_bytes(B, heads, cache, max_len, max_new=1):
+    """Workspace bytes mnb_paged_attn_i8 needs for B requests of `heads` query
+    heads and at most max_new new tokens each."""
+    return lib().mnb_paged_attn_i8_workspace_bytes(B, heads, cache.kv_heads, cache.head_dim, max_len, max_new,
+                                                   dtype_code(cache.dtype))
+
+
+def paged_attn_i8_workspace(q, cache, block_table, max_len, max_new=1):
+    """A workspace for mnb_paged_attn_i8 with exactly q's heads, block_table's
+    requests and these bounds (empty when the call splits nothing); others may
+    need more."""
+    nbytes = mnb_paged_attn_i8_workspace_bytes(block_table.shape[0], q.shape[1], cache, max_len, max_new)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+
+
+def mnb_paged_attn_i8(q, cache, block_table, lens, max_len, starts=None, max_new=1, scale=None, workspace=None,
+                      out=None):
+    """Attention over a KvCacheI8, through block_table (int32 [B, max_blocks]).
+    One new token per request, q [B, heads, head_dim] over its first lens[b]
+    (int32 [B], at most max_len) positions; or, with starts (int32 [B + 1]),
+    several: rows starts[b] .. starts[b + 1] - 1 of q [T, heads, head_dim], at
+    most max_new, are the last of request b's lens[b] positions, and each sees
+    the positions up to its own. scale: 1 / sqrt(head_dim) unless given.
+    Returns out [T, heads, head_dim]; rows of no request stay as they were."""
+    device, index, dtype = cache.device, cache.index, cache.dtype
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError(f"q must be [T, heads, {cache.head_dim}] with contiguous heads")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    T, heads, dim = q.shape
+    B, width = block_table.shape
+    q_ptr, q_stride = _head_rows(q, "q", heads, cache.head_dim, dtype, index, device)
+    if starts is None and T != B:
+        raise ValueError(f"q has {T} tokens for {B} requests: starts says whose they are")
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=dtype, device=device)
+    if workspace is None:
+        workspace = paged_attn_i8_workspace(q, cache, block_table, max_len, max_new)
+    _launch("mnb_paged_attn_i8", index, q_ptr, q_stride, cache.ref,
+            _whole(block_table, "block_table", torch.int32, B * width, index, device),
+            _whole(lens, "lens", torch.int32, B, index, device),
+            None if starts is None else _whole(starts, "starts", torch.int32, B + 1, index, device), T, B, heads,
+            width, max_len, max_new, dim ** -0.5 if scale is None else scale, *_workspace(workspace, index, device),
+            _whole(out, "out", dtype, T * heads * dim, index, device))
     return out

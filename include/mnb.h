@@ -528,6 +528,126 @@ int mnb_cross_attn(const mnb_attn_view *q, const mnb_attn_view *k, const mnb_att
                    int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t head_dim, float scale,
                    int dtype, void *workspace, size_t workspace_bytes, const mnb_attn_view *out, void *stream);
 
+/*
+ * Rotary positions: queries and keys turned by their tokens' positions, between
+ * the q/k products and the append. For token t with position p = positions[t]
+ * and frequency f_i (i < rot_dim / 2), angle a = p * f_i:
+ *   y[i0] = gain * (x[i0] cos a - x[i1] sin a),
+ *   y[i1] = gain * (x[i0] sin a + x[i1] cos a),
+ * (i0, i1) = (i, i + rot_dim / 2) for MNB_ROPE_HALF, (2i, 2i + 1) for
+ * MNB_ROPE_INTERLEAVED; dimensions from rot_dim on are copied. The same for
+ * every head of q and of k. Angles are float64 products, reduced to a fraction
+ * of a turn in float64, so that far positions keep theirs; cosines, sines and
+ * the turning are float32, each output rounded once to dtype. Any int32
+ * position will do; a negative one turns back.
+ *
+ * freqs: device float64 [rot_dim / 2], radians per position: base^(-2i /
+ * rot_dim), or these scaled for longer contexts, which may also ask for a
+ * gain. positions: device int32 [T]. q, q_out: device [T][q_heads][head_dim],
+ * tokens q_stride and q_out_stride elements apart, heads contiguous; k, k_out
+ * the same (k_heads 0: no keys, k and k_out may be NULL; likewise q).
+ * head_dim * sizeof(dtype) a multiple of 16, head_dim <= 1024, rot_dim even,
+ * 2 .. head_dim (MNB_ERR_SHAPE). Rows 16-byte aligned: pointers, and strides
+ * in bytes (MNB_ERR_ALIGN); freqs 8, positions 4. An output may be its own
+ * input (the same address and stride); otherwise the rows of an output must
+ * not overlap those of an input or of the other output. MNB_ERR_INVALID: they
+ * do (rows of different strides whose address ranges meet count as
+ * overlapping; so do an output's own rows nearer than they are long), an
+ * unknown layout, a gain that is not finite. T = 0 enqueues nothing.
+ */
+#define MNB_ROPE_HALF 0
+#define MNB_ROPE_INTERLEAVED 1
+int mnb_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int64_t q_heads,
+             const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride, int64_t k_heads,
+             const int32_t *positions, const double *freqs, int64_t T, int64_t head_dim, int64_t rot_dim,
+             int layout, float gain, int dtype, void *stream);
+
+/*
+ * The key-value cache in 8 bits: half the memory of float16, and half the
+ * bytes of a decoding step's attention. Each row (one token's keys, or
+ * values, of one head: head_dim numbers) is stored as int8 codes c and one
+ * float32 scale s, and stands for c * s:
+ *   s = amax / 127, rounded to float32 (amax the row's largest |x|),
+ *   c = x / s rounded to the nearest whole number (the exact quotient, ties to
+ *       even), within -127 .. 127; 0 where s is 0.
+ * A scale of its own for every token and head: what is stored does not depend
+ * on how tokens are cut into calls, and no row is ever rounded twice. A row
+ * that holds an infinity or a NaN is stored as codes 0 with the scale NaN: it
+ * stands for NaN throughout.
+ *
+ * Pages, slots, tables and lengths are those of mnb_kv_cache (mnb_kv_tables
+ * serves both). The codes of token `t % page_size` of head h in block `id`
+ * start at k + id * block_stride + h * head_stride + (t % page_size) *
+ * token_stride; its scale is k_scale[id * scale_block_stride + h *
+ * scale_head_stride + t % page_size] (v the same). The limits and status codes
+ * are mnb_kv_cache's, with code strides multiples of 16 and scale strides
+ * multiples of 4 (MNB_ERR_ALIGN); all four pointers 16-byte aligned.
+ */
+typedef struct mnb_kv_cache_i8 {
+    int8_t *k, *v;             /* device codes; the same strides for both   */
+    float *k_scale, *v_scale;  /* device; the same strides for both         */
+    int64_t num_blocks, kv_heads, page_size, head_dim;   /* as mnb_kv_cache */
+    int64_t block_stride, head_stride, token_stride;     /* codes           */
+    int64_t scale_block_stride, scale_head_stride;       /* scales; a page's
+                                                            tokens of a head
+                                                            are contiguous  */
+    int32_t dtype;             /* of tokens, queries and outputs            */
+    int32_t reserved;          /* 0                                         */
+} mnb_kv_cache_i8;
+
+/*
+ * mnb_kv_append into the 8-bit cache: T tokens' keys and values, k, v device
+ * [T][kv_heads][head_dim] of the cache's dtype, rows k_stride and v_stride
+ * elements apart, quantized and written to slots[t] (device int64 [T]; slots
+ * outside the cache are skipped). Two tokens with one slot leave parts of
+ * either there. T = 0 enqueues nothing.
+ */
+int mnb_kv_append_i8(const void *k, const void *v, int64_t k_stride, int64_t v_stride, const int64_t *slots,
+                     int64_t T, const mnb_kv_cache_i8 *cache, void *stream);
+
+/*
+ * What the cache's slots stand for, as rows: k, v device [T][kv_heads]
+ * [head_dim] of the cache's dtype receive c * s, the exact product rounded
+ * once, of slots[t] (device int64 [T]); zeros for slots outside the cache
+ * (-1 among them). Rows k_stride and v_stride elements apart, not nearer than
+ * they are long, and k's and v's ranges must not meet unless the strides are
+ * equal and the rows disjoint (MNB_ERR_INVALID). T = 0 enqueues nothing.
+ */
+int mnb_kv_read_i8(const int64_t *slots, int64_t T, const mnb_kv_cache_i8 *cache, void *k, void *v,
+                   int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * Attention over the 8-bit cache, softmax(scale * q . k) over the keys that a
+ * query sees, times their values. One new token per request (starts NULL,
+ * T = B, max_new = 1): q [B][Hq][head_dim], request b sees its first lens[b]
+ * positions, as in mnb_paged_attn. Or several (starts int32 [B + 1], as
+ * mnb_kv_tables writes them): request b's new tokens are rows starts[b] ..
+ * starts[b + 1] - 1 of q [T][Hq][head_dim] (cut to 0 .. T), n of them, which
+ * are the last n of its lens[b] positions, already appended: row i sees the
+ * first lens[b] - n + i + 1. max_new is the caller's bound on n, as max_len is
+ * on lens: rows i >= max_new are not computed. Rows of q that belong to no
+ * request, and those past max_new, leave their rows of out as they were (a row
+ * that starts gives to two requests holds the result of either).
+ * Positions at max_len and beyond, past the table's width, or in blocks that
+ * the cache does not have are never seen. A row that sees nothing is zeros.
+ *
+ * Rows of q are q_stride elements apart, heads contiguous; out [T][Hq]
+ * [head_dim] contiguous, not overlapping q (MNB_ERR_INVALID). Heads, limits,
+ * workspace and the rule that the same arguments give the same bits are
+ * mnb_paged_attn's; the workspace's size is that of a call of exactly this B,
+ * max_len and max_new.
+ *
+ * Scores, softmax statistics and sums over keys are float32. A query row that
+ * holds an infinity or a NaN gives NaN (zeros if it sees nothing), and so does
+ * a key or value row of scale NaN to every row that sees it.
+ */
+size_t mnb_paged_attn_i8_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t max_len,
+                                         int64_t max_new, int dtype);
+int mnb_paged_attn_i8(const void *q, int64_t q_stride, const mnb_kv_cache_i8 *cache, const int32_t *block_table,
+                      const int32_t *lens, const int32_t *starts, int64_t T, int64_t B, int64_t Hq,
+                      int64_t max_blocks, int64_t max_len, int64_t max_new, float scale, void *workspace,
+                      size_t workspace_bytes, void *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

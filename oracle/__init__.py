@@ -48,6 +48,12 @@ notes. The functions and what pins each one (tests/test_oracle_pins.py):
   cross_attention     (attn_oracle, the decoder's attention) pinned in
                       tests/test_attn_oracle.py: worked tables, closed forms
                       of the softmax, equality of the paged and plain forms
+  rope, quantize_rows,
+  attention_i8, visible
+                      (cache8_oracle, the 8-bit cache and rotary positions)
+                      pinned in tests/test_cache8_oracle.py: complex
+                      rotations, exact rationals, worked rows, equality with
+                      paged_attention where one token is new
 """
 
 from .mnb_oracle import (  # noqa: F401
@@ -78,4 +84,10 @@ from .attn_oracle import (  # noqa: F401
     kv_tables,
     paged_attention,
     paged_rows,
+)
+from .cache8_oracle import (  # noqa: F401
+    attention_i8,
+    quantize_rows,
+    rope,
+    visible,
 )
