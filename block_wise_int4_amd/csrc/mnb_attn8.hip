@@ -1,8 +1,27 @@
 // Attention over the 8-bit cache: o = sum_t w_t vs_t cv_t / sum_t w_t, w_t =
-// exp(s_t - m), s_t = scale * ks_t * (q . ck_t), codes ck, cv and scales ks, vs.
+// exp(s_t - m), s_t = scale * ks_t * (q . ck_t), codes ck, cv and scales ks, vs,
+// m the running maximum.
 //
-// First form: a wave takes one query row (token, head) and walks over its keys 64
-// at a time, a key a lane for the scores, D / 64 dimensions a lane for the sums.
+// Both products are whole numbers. A query row is held as its largest element's
+// power of two times 22-bit numbers and a sign, these as three digits of 8 bits;
+// a tile's weights w_t vs_t as the power of two of the tile's largest times 22-bit
+// numbers, in three digits as well. So codes enter the matrix unit as they are
+// stored, nothing is rounded between the digits and the 32-bit sums, and float16
+// and float32 calls differ in their first loads and last stores alone.
+//
+// Work: a row of tiles is up to 16 query rows of one (request, key-value head);
+// its keys are cut into chunks, and a chunk's tiles of 64 keys are taken in turn
+// by the waves of one workgroup, codes through a place of the wave's own in LDS:
+//   S^T = CK Q^T  A = codes (lane: key l % 16, 16 bytes of its row), B = a digit of
+//                 the queries; per lane four keys 4 (l / 16) + i of one query
+//                 l % 16, for each of the tile's four 16-key parts
+//   O^T = CV^T P^T  contraction over those 64 keys: a digit of the weights is the
+//                 lane's own 16 bytes, packed by byte permutes; A's rows are
+//                 dimensions, which come out of LDS through the transposing
+//                 8-byte reads.
+// The next tile's key codes are requested as soon as this one's are in registers,
+// its value codes after the second product's reads.
+// The waves' sums are joined in LDS, and the chunks' by a second launch.
 #include "mnb_cache8.h"
 #include "mnb_device.h"
 
@@ -10,15 +29,45 @@ namespace mnb {
 
 namespace {
 
-constexpr float kLowest = -3.402823466e38f;
+constexpr int kWaves = 4;
+constexpr int kQ = 16;       // query rows per row of tiles
+constexpr int kParts = 4;    // 16-key parts of a tile
+constexpr int kKeys = 16 * kParts;
+constexpr float kLowest = -3.402823466e38f;   // the maximum before any key
 constexpr float kLog2e = 1.4426950408889634f;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ i32x4 mma64(i32x4 a, i32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// The largest over the four lanes of a column (l % 16).
+__device__ __forceinline__ uint32_t column_max(uint32_t x) {
+    u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(x, x, false, false));
+    x = r.x > r.y ? r.x : r.y;
+    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, x, false, false));
+    return r.x > r.y ? r.x : r.y;
+}
+__device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
+__device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float column_max(float x) {
+    // (elements through functions: a bit cast of a vector's element reads the first)
+    u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
+    x = fmaxf(as_float(r.x), as_float(r.y));
+    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false));
+    return fmaxf(as_float(r.x), as_float(r.y));
+}
+
+__device__ __forceinline__ float weight(float x, float m) { return __builtin_amdgcn_exp2f((x - m) * kLog2e); }
 
 // New tokens of request b, and its first row of q.
 __device__ __forceinline__ int rows_of(const Attn8Args &a, int64_t b, int64_t &first) {
-    if (!a.starts) {
-        first = b;
-        return 1;
-    }
+    first = b;
+    if (!a.starts) return 1;
     int64_t from = a.starts[b], to = a.starts[b + 1];
     from = from < 0 ? 0 : from > a.tokens ? a.tokens : from;
     to = to < from ? from : to > a.tokens ? a.tokens : to;
@@ -26,88 +75,584 @@ __device__ __forceinline__ int rows_of(const Attn8Args &a, int64_t b, int64_t &f
     return (int)(to - from);
 }
 
+// Keys that new token i of n of request b sees.
+__device__ __forceinline__ int sees(const Attn8Args &a, int len, int n, int i) {
+    const int64_t s = (int64_t)len - n + i + 1;
+    return s < 0 ? 0 : s < a.max_len ? (int)s : a.max_len;
+}
+
+// Blocks before a part of 16 keys.
+__device__ __forceinline__ uint32_t blocks_before(uint32_t part, uint32_t magic) {
+    const uint32_t place = __umulhi(part, magic);
+    return magic ? place : part;
+}
+
+// Where 16-byte piece c of LDS row `row` is: c ^ swizzle(row). The first product's
+// reads (16 rows, one piece) and the transposing ones (8 of 32 rows, one piece)
+// each touch all banks evenly.
+template <int D> __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (D == 128) return ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
+    else return ((row >> 2) & 3) ^ ((row >> 4) & 1) << 1;
+}
+
+// Token and query head of row r of a (request, key-value head).
+__device__ __forceinline__ int token_of(const Attn8Args &a, int r) {
+    return a.max_new == 1 ? 0 : (int)((uint32_t)r / (uint32_t)a.group);
+}
+
+// Four outputs from dimension d on of row r.
+template <typename T, int D>
+__device__ __forceinline__ void store_out(const Attn8Args &a, int64_t first, int h, int r, int d, f4 sum, float total) {
+    const int token = token_of(a, r);
+    T *out = static_cast<T *>(a.out) +
+             ((first + token) * ((int64_t)a.cache.heads * a.group) + (int64_t)h * a.group + r - token * a.group) * D + d;
+    if (total == 0.0f) sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    else sum *= 1.0f / total;
+    if constexpr (sizeof(T) == 2) {
+        const u32x2 w = {as_u32(h2{(_Float16)sum.x, (_Float16)sum.y}), as_u32(h2{(_Float16)sum.z, (_Float16)sum.w})};
+        *reinterpret_cast<u32x2 *>(out) = w;
+    } else {
+        *reinterpret_cast<f4 *>(out) = sum;
+    }
+}
+
+// Sixteen numbers of a query row as three digits each, most significant last:
+// x * 2^up, up to 2^22, rounded.
+__device__ __forceinline__ void digits_of(const float *x, float up, i32x4 *digit) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t d0 = 0, d1 = 0, d2 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // (the low two bytes' digits are signed: 128 too much, and less again)
+            const uint32_t n = (uint32_t)((int)__builtin_rintf(x[4 * w + i] * up) + 0x8080);
+            d0 |= (n & 0xFF) << (8 * i);
+            d1 |= (n >> 8 & 0xFF) << (8 * i);
+            d2 |= (n >> 16 & 0xFF) << (8 * i);
+        }
+        digit[0][w] = (int)(d0 ^ 0x80808080u);
+        digit[1][w] = (int)(d1 ^ 0x80808080u);
+        digit[2][w] = (int)d2;
+    }
+}
+
 }  // namespace
 
-template <typename T, int D> __global__ __launch_bounds__(64) void attn8_kernel(Attn8Args a) {
-    __shared__ float s_q[D], s_w[64];
-    __shared__ const int8_t *s_v[64];
-    const int lane = threadIdx.x, h = blockIdx.x, i = blockIdx.z;
+// How a launch is cut. Pieces of rows of more than one chunk: per (request,
+// head, query row, chunk) D sums, and a maximum and the weights' sum.
+struct Attn8Split {
+    int32_t chunk;        // keys per chunk
+    int32_t chunks;       // of max_len
+    int32_t rows;         // bound of the rows per (request, head)
+    int32_t q_tiles;
+    uint32_t page_magic;  // ceil(2^32 / (page / 16)), 0 for pages of 16: part * magic >> 32 is
+                          // part / (page / 16) for part < 2^26
+    float *sums, *stats;
+};
+
+template <typename T, int D, bool STREAM>
+__device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8Split &sp) {
+    constexpr int kLoads = D / 64;      // of 1 KB per part
+    constexpr int kPieces = D / 16;     // of a row of codes
+    constexpr int kTile = kKeys * D;    // bytes
+    constexpr int kOut = D / 16;        // 16-dimension parts of the output
+    // the waves' tiles of key and value codes (arrays of their own: the compiler then
+    // knows that reads of one need not wait for loads into the other); in the end their
+    // sums [kWaves][kQ][D], and maxima and weights' sums [kWaves][kQ]
+    __shared__ __attribute__((aligned(16))) uint8_t s_keys[kWaves][kTile], s_values[kWaves][kTile];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int h = blockIdx.x, chunk = blockIdx.z / sp.q_tiles, q_tile = blockIdx.z - chunk * sp.q_tiles;
     const int64_t b = blockIdx.y;
-    int64_t first;
-    const int rows = rows_of(a, b, first);
-    if (i >= rows) return;
-    int64_t n = (int64_t)a.lens[b] - rows + i + 1;
-    n = n < a.max_len ? n : a.max_len;
-    const int kv = h / a.group;
     const Cache8 &c = a.cache;
-    const T *q = static_cast<const T *>(a.q) + (first + i) * a.q_stride + (int64_t)h * D;
-    bool finite = true;
-    for (int d = lane; d < D; d += 64) {
-        s_q[d] = (float)q[d];
-        finite &= __builtin_fabsf(s_q[d]) <= -kLowest;
+    const int begin = chunk * sp.chunk;
+    int key = begin + wave * kKeys;
+    // (no kernel writes the table while this one reads it: scalar loads)
+    typedef __attribute__((address_space(4))) const int32_t table_entry;
+    table_entry *table = (table_entry *)(a.table + b * a.table_width);
+    // The table entries of the tile at key0 (past the table's end its last
+    // entry, which is not used).
+    int32_t ids[kParts];
+    auto look_up = [&](int key0) {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+            const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + s, sp.page_magic);
+            ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
+        }
+    };
+    look_up(key);
+    int64_t first;
+    const int len = a.lens[b], n_new = rows_of(a, b, first);
+    const int row0 = q_tile * kQ;
+    int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group - row0;
+    if (rows <= 0) return;
+    if (rows > kQ) rows = kQ;
+    // keys that the tile's rows see: the last row most, the first least
+    const int n = sees(a, len, n_new, token_of(a, row0 + rows - 1)), least = sees(a, len, n_new, token_of(a, row0));
+    if (begin >= n && chunk > 0) return;
+    const int end = n - begin < sp.chunk ? n : begin + sp.chunk;
+    const int r = row0 + (col < rows ? col : 0), token = token_of(a, r);
+    const int mine = sees(a, len, n_new, token);
+
+    // queries: lane (query col, pieces 4 j + g of 16 dimensions), in digits
+    i32x4 q[kLoads][3];
+    float mul;   // of a sum of digit products, to a score without the key's scale
+    {
+        const T *src = static_cast<const T *>(a.q) + (first + token) * a.q_stride +
+                       ((int64_t)h * a.group + r - token * a.group) * D + g * 16;
+        float x[kLoads][16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int p = 0; p < (int)sizeof(T); ++p) {
+                const u32x4 w = reinterpret_cast<const u32x4 *>(src + 64 * j)[p];
+#pragma unroll
+                for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+                    float v;
+                    if constexpr (sizeof(T) == 2) v = (float)__builtin_bit_cast(h8, w)[i];
+                    else v = __builtin_bit_cast(f4, w)[i];
+                    x[j][p * (16 / (int)sizeof(T)) + i] = v;
+                    // (as whole numbers: infinities and NaN are above every finite one)
+                    const uint32_t bits = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+                    top = bits > top ? bits : top;
+                }
+            }
+        top = column_max(top);
+        const bool finite = top < 0x7F800000u;
+        // 2^(e - 127) <= largest < 2^(e - 126), twice as large numbers for the smallest
+        int lift = 0;
+        if (top < (64u << 23)) {
+            lift = 64;
+            top = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, top) * 0x1p64f);
+        }
+        const int e = top ? (int)(top >> 23) : 127;
+        const float up = __builtin_bit_cast(float, (uint32_t)(127 + 21 + 127 - e) << 23);
+        mul = finite ? __builtin_ldexpf(a.scale, e - 127 - 21 - lift) : __builtin_nanf("");
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[j][i] = finite ? (lift ? x[j][i] * 0x1p64f : x[j][i]) : 0.0f;
+            digits_of(x[j], up, q[j]);
+        }
     }
-    const float spoil = __all(finite) ? 0.0f : __builtin_nanf("");
-    __syncthreads();
-    float o[D / 64] = {}, l = 0.0f, m = kLowest;
-    for (int64_t base = 0; base < n; base += 64) {
-        const int64_t t = base + lane;
-        float x = -__builtin_inff(), vs = 0.0f;
-        const int8_t *vp = nullptr;
-        if (t < n) {
-            const int id = a.table[b * a.table_width + t / c.page];
-            const int offset = (int)(t % c.page);
-            if (id >= 0 && id < c.num_blocks) {
-                const int64_t at = id * c.block_stride + kv * c.head_stride + offset * c.token_stride;
-                const int64_t sat = id * c.scale_block + kv * c.scale_head + offset;
-                const int8_t *kp = c.k + at;
-                vp = c.v + at;
-                float sum = 0.0f;
-                for (int d = 0; d < D; ++d) sum = __builtin_fmaf(s_q[d], (float)kp[d], sum);
-                x = sum * c.k_scale[sat] * a.scale + spoil;
-                vs = c.v_scale[sat];
+
+    // One tile: a part (16 keys) is read through buffers that end with its last key
+    // that any row sees; a part without keys reads nothing.
+    const int8_t *kp = c.k + h * c.head_stride, *vp = c.v + h * c.head_stride;
+    const float *ksp = c.k_scale + h * c.scale_head, *vsp = c.v_scale + h * c.scale_head;
+    const uint32_t stride = (uint32_t)c.token_stride;
+    int valid[kParts], valid_next[kParts];   // leading keys of each part
+    uint32_t block[kParts], row[kParts]; // where it is
+    auto locate = [&](int key0, int *valid) {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+            const int first_key = key0 + 16 * s;
+            int ok = end - first_key;
+            ok = ok < 0 ? 0 : ok > 16 ? 16 : ok;
+            const uint32_t part = (uint32_t)first_key >> 4;
+            block[s] = ids[s];
+            row[s] = (part - blocks_before(part, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
+            valid[s] = __builtin_amdgcn_readfirstlane(block[s] < (uint64_t)c.num_blocks ? ok : 0);
+        }
+    };
+    auto buffer = [&](const void *base, uint32_t bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
+    };
+    // A load to LDS takes whole rows, 64 lanes on 1 KB after another.
+    constexpr int kRows = 64 / kPieces;   // of a load
+    uint8_t *s_k = s_keys[wave], *s_v = s_values[wave];
+    uint32_t at[2][kLoads];               // for even and odd parts
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int row = j * kRows + lane / kPieces;
+            at[odd][j] = (uint32_t)row * stride + ((lane % kPieces) ^ swizzle<D>(16 * odd + row)) * 16;
+        }
+    auto load_codes = [&](const int8_t *base, uint8_t *to, const int *valid) {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+            const auto rows_in = buffer(base + (int64_t)block[s] * c.block_stride + (int64_t)row[s] * stride,
+                                        valid[s] > 0 ? (uint32_t)(valid[s] - 1) * stride + D : 0u);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_in, (lds_void *)(to + (s * kLoads + j) * 1024), 16,
+                                                         at[s & 1][j], 0, 0, STREAM ? 2 : 0);
+        }
+    };
+    auto load_scales = [&](const float *base, f4 *to, const int *valid) {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+            to[s] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               buffer(base + (int64_t)block[s] * c.scale_block + row[s],
+                                                      valid[s] > 0 ? 64u : 0u),
+                                               g * 16, 0, 0));
+    };
+    // (the places are worked out again for the values: kept, they take 24 scalar
+    // registers more than there are)
+    auto forget = [&]() {
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) asm volatile("" : "+s"(block[s]), "+s"(row[s]), "+s"(valid_next[s]));
+    };
+
+    // Values, turned: 16 lanes read eight keys by 16 dimensions. Lane L supplies key
+    // L / 2, eight dimensions 8 (L % 2) on, and receives dimension L of the eight keys
+    // 16 (2 u + j / 4) + 4 g + j % 4. Four parts of 16 dimensions at a time, and their
+    // wait with them: through the builtin the compiler waits for all loads first, the
+    // next keys' among them.
+    const int v_row = 16 * (col >> 3) + 4 * g + ((col >> 1) & 3);   // (u = 0; u = 1 is 32 rows on)
+    const uint32_t v_at = (uint32_t)(size_t)(lds_void *)s_v + v_row * D + (col & 1) * 8;
+    auto read_values = [&](i32x2 (*v)[2], uint32_t base, int d) {
+        uint32_t at[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[e] = base + ((d + e) ^ swizzle<D>(v_row)) * 16;
+        asm volatile(
+            "ds_read_b64_tr_b8 %0, %8\n\tds_read_b64_tr_b8 %1, %8 offset:%12\n\t"
+            "ds_read_b64_tr_b8 %2, %9\n\tds_read_b64_tr_b8 %3, %9 offset:%12\n\t"
+            "ds_read_b64_tr_b8 %4, %10\n\tds_read_b64_tr_b8 %5, %10 offset:%12\n\t"
+            "ds_read_b64_tr_b8 %6, %11\n\tds_read_b64_tr_b8 %7, %11 offset:%12\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
+              "=&v"(v[3][0]), "=&v"(v[3][1])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(32 * D)
+            : "memory");
+    };
+
+    f4 o[kOut];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) o[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kLowest, l = 0.0f;
+    f4 ks[kParts], vs[kParts];
+    const int step = kWaves * kKeys;
+    if (key < end) {
+        locate(key, valid_next);
+        load_scales(ksp, ks, valid_next);
+        load_codes(kp, s_k, valid_next);
+        asm volatile("" ::: "memory");   // (in this order: the waits below count them)
+        look_up(key + step);
+        forget();
+        load_scales(vsp, vs, valid_next);
+        load_codes(vp, s_v, valid_next);
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) valid[s] = valid_next[s];
+    }
+    for (; key < end; key += step) {
+        // this tile's key codes are in LDS: all but the loads after theirs have come
+        // back (the compiler does not wait for loads to LDS)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kParts + kParts * kLoads) : "memory");
+        float x[kParts][4];
+        {
+            i32x4 kk[kParts][kLoads];
+#pragma unroll
+            for (int s = 0; s < kParts; ++s)
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    const int row = 16 * s + col;
+                    kk[s][j] = *reinterpret_cast<const i32x4 *>(s_k + row * D + ((4 * j + g) ^ swizzle<D>(row)) * 16);
+                }
+#pragma unroll
+            for (int s = 0; s < kParts; ++s) {
+                i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    lo = mma64(kk[s][j], q[j][0], lo);
+                    hi = mma64(kk[s][j], q[j][2], hi);
+                }
+                // (below 2^21 * 2^8: the two upper digits in one number)
+                hi = hi << 8;
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) hi = mma64(kk[s][j], q[j][1], hi);
+                const f4 by = ks[s] * mul;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * by[i];
             }
         }
-        float top = x;
-        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-        const float to = fmaxf(m, top), keep = __builtin_amdgcn_exp2f((m - to) * kLog2e);
-        m = to;
-        const float w = __builtin_amdgcn_exp2f((x - m) * kLog2e);
-        float sum = w;
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        l = l * keep + sum;
-        __syncthreads();
-        s_w[lane] = vp ? w * vs : 0.0f;
-        s_v[lane] = vp;
-        __syncthreads();
-        for (int e = 0; e < D / 64; ++e) o[e] *= keep;
-        for (int j = 0; j < 64; ++j) {
-            if (!s_v[j]) continue;
-            for (int e = 0; e < D / 64; ++e)
-                o[e] = __builtin_fmaf(s_w[j], (float)s_v[j][lane + 64 * e], o[e]);
+        locate(key + step, valid_next);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the reads of these codes are over
+        load_scales(ksp, ks, valid_next);
+        load_codes(kp, s_k, valid_next);
+        asm volatile("" ::: "memory");
+        look_up(key + 2 * step);
+        bool partial = key + kKeys > least;
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) partial |= valid[s] < 16;
+        if (partial) {   // uniform: the end of a row, or a missing block
+#pragma unroll
+            for (int s = 0; s < kParts; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at_part = 4 * g + i;
+                    const bool seen = at_part < valid[s] && key + 16 * s + at_part < mine;
+                    x[s][i] = seen ? x[s][i] : -__builtin_inff();
+                    vs[s][i] = seen ? vs[s][i] : 0.0f;
+                }
+        }
+        float top = x[0][0];
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, x[s][i]);
+        top = column_max(top);
+        if (__any(top > m)) {
+            const float to = fmaxf(m, top), keep = weight(m, to);
+            m = to;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) o[i] *= keep;
+        }
+        // weights times value scales, and the largest of the tile (as whole numbers:
+        // they are not negative, and NaN is above all)
+        uint32_t most = 0;
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = weight(x[s][i], m);
+                l += w;
+                x[s][i] = w * vs[s][i];
+                const uint32_t bits = as_bits(x[s][i]) & 0x7FFFFFFFu;
+                most = bits > most ? bits : most;
+            }
+        most = column_max(most);
+        // numbers below 2^22: times 2^(21 - exponent), a touch less so that none rounds
+        // up to it; at 2^23 + 0x8080 their bytes are the digits, 128 too much in two
+        const bool finite = most < 0x7F800000u;
+        int e = (int)(most >> 23);
+        e = e < 24 ? 24 : e;
+        const float up = __builtin_bit_cast(float, (uint32_t)(127 + 21 + 127 - e) << 23) * (1.0f - 0x1p-21f);
+        const float down = finite ? __builtin_bit_cast(float, (uint32_t)(e - 21) << 23) * (1.0f + 0x1p-21f)
+                                  : __builtin_nanf("");
+        i32x4 p[3];
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = as_bits(__builtin_fmaf(x[s][i], up, 8388608.0f + 32896.0f));
+            const uint32_t a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);   // bytes 0, 0, 1, 1
+            const uint32_t a23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+            const uint32_t b01 = __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0602u);   // bytes 2, 2
+            const uint32_t b23 = __builtin_amdgcn_perm(w[3], w[2], 0x06020C0Cu);
+            p[0][s] = (int)(__builtin_amdgcn_perm(a23, a01, 0x05040100u) ^ 0x80808080u);
+            p[1][s] = (int)(__builtin_amdgcn_perm(a23, a01, 0x07060302u) ^ 0x80808080u);
+            p[2][s] = (int)(b01 | b23);
+        }
+        // this tile's value codes are in LDS: all but the next keys' loads
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kParts + kParts * kLoads) : "memory");
+#pragma unroll
+        for (int d = 0; d < kOut; d += 4) {
+            i32x2 v[4][2];
+            read_values(v, v_at, d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const i32x4 zero = {0, 0, 0, 0}, vv = {v[e][0].x, v[e][0].y, v[e][1].x, v[e][1].y};
+                const i32x4 lo = mma64(vv, p[0], zero), hi = mma64(vv, p[1], mma64(vv, p[2], zero) << 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[d + e][i] = __builtin_fmaf(__builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]), down, o[d + e][i]);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        forget();
+        load_scales(vsp, vs, valid_next);
+        load_codes(vp, s_v, valid_next);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) valid[s] = valid_next[s];
+    }
+
+    // (the tile past the end has arrived everywhere: its place is free)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+
+    // join the waves (those that have keys)
+    static_assert(sizeof(s_keys) == kWaves * kQ * D * sizeof(float), "the waves' sums take the key tiles' place");
+    float *s_m = reinterpret_cast<float *>(s_values), *s_l = s_m + kWaves * kQ;
+    // (four dimensions 4 p of a row; rows turned against one another in the banks)
+    auto sums = [&](int wave, int row, int p) {
+        return reinterpret_cast<f4 *>(s_keys) + (wave * kQ + row) * (D / 4) + (p ^ (row & 7));
+    };
+    const int tiles = n <= kKeys ? 1 : (end - begin + kKeys - 1) / kKeys;
+    const int waves = tiles < kWaves ? tiles : kWaves;
+    if (wave < waves) {
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (g == 0) {
+            s_m[wave * kQ + col] = m;
+            s_l[wave * kQ + col] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) *sums(wave, col, 4 * d + g) = o[d];
+    }
+    __syncthreads();
+    const bool whole = n <= sp.chunk;   // this chunk is the rows' only one
+    for (int e = threadIdx.x; e < rows * (D / 4); e += 64 * kWaves) {
+        const int i = e / (D / 4), p = e % (D / 4);
+        float top = s_m[i];
+        for (int w = 1; w < waves; ++w) top = fmaxf(top, s_m[w * kQ + i]);
+        f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        float total = 0.0f;
+        for (int w = 0; w < waves; ++w) {
+            const float f = weight(s_m[w * kQ + i], top);
+            sum += *sums(w, i, p) * f;
+            total += s_l[w * kQ + i] * f;
+        }
+        if (whole) {
+            store_out<T, D>(a, first, h, row0 + i, 4 * p, sum, total);
+        } else {
+            const int64_t piece = ((b * c.heads + h) * sp.rows + row0 + i) * sp.chunks + chunk;
+            *reinterpret_cast<f4 *>(sp.sums + piece * D + 4 * p) = sum;
+            if (p == 0) {
+                sp.stats[2 * piece] = top;
+                sp.stats[2 * piece + 1] = total;
+            }
         }
     }
-    T *out = static_cast<T *>(a.out) + ((first + i) * (int64_t)(c.heads * a.group) + h) * D;
-    for (int e = 0; e < D / 64; ++e) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
 }
 
-int64_t attn8_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int, int) { return 0; }
-
-bool attn8_fits(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t, int, int) {
-    return kv_heads * group <= (1 << 22) && batch <= 65536 && max_new <= 65535;
+template <typename T, int D, bool STREAM>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn8_kernel(Attn8Args a, Attn8Split sp) {
+    attn8_workgroup<T, D, STREAM>(a, sp);
 }
 
-hipError_t launch_attn8(const Attn8Args &a, int head_dim, int dtype, void *, hipStream_t st) {
-    Attn8Args c = a;
-    if (c.max_len > (int64_t)a.table_width * a.cache.page) c.max_len = a.table_width * a.cache.page;
-    const int64_t most = a.tokens < a.max_new ? a.tokens : a.max_new;
-    const dim3 grid(a.cache.heads * a.group, a.batch, (unsigned)most);
-    if (dtype == 1)
-        head_dim == 128 ? attn8_kernel<_Float16, 128><<<grid, 64, 0, st>>>(c)
-                        : attn8_kernel<_Float16, 64><<<grid, 64, 0, st>>>(c);
-    else
-        head_dim == 128 ? attn8_kernel<float, 128><<<grid, 64, 0, st>>>(c)
-                        : attn8_kernel<float, 64><<<grid, 64, 0, st>>>(c);
+// Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
+// D / 4 lanes, which take every 2^shift-th chunk; then their sums are added.
+constexpr int kJoin = 256;
+template <typename T, int D>
+__global__ __launch_bounds__(kJoin) void attn8_join_kernel(Attn8Args a, Attn8Split sp, int shift) {
+    constexpr int kLanes = D / 4, kLaneBits = D == 128 ? 5 : 4;
+    __shared__ f4 s_sum[kJoin];
+    __shared__ float s_m[kJoin], s_l[kJoin];
+    const int tid = threadIdx.x, d = tid % kLanes * 4, groups = 1 << shift;
+    const int group = (tid >> kLaneBits) & (groups - 1);
+    const int row = blockIdx.z * (kJoin >> (kLaneBits + shift)) + (tid >> (kLaneBits + shift));
+    const int h = blockIdx.x;
+    const int64_t b = blockIdx.y;
+    int64_t first;
+    const int len = a.lens[b], n_new = rows_of(a, b, first);
+    const int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group;
+    const bool on = row < rows;
+    // the keys of the row's tile: its last row's
+    int last = (row / kQ + 1) * kQ - 1;
+    last = last < rows ? last : rows - 1;
+    const int n = on ? sees(a, len, n_new, token_of(a, last)) : 0;
+    const int64_t from_piece = ((b * a.cache.heads + h) * sp.rows + (on ? row : 0)) * sp.chunks;
+    f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kLowest, l = 0.0f;
+    for (int k = group; k < sp.chunks && k * sp.chunk < n; k += groups) {
+        const float *stats = sp.stats + 2 * (from_piece + k);
+        const float pm = stats[0], pl = stats[1];
+        const f4 ps = *reinterpret_cast<const f4 *>(sp.sums + (from_piece + k) * D + d);
+        const float to = fmaxf(m, pm), keep = weight(m, to), f = weight(pm, to);
+        sum = sum * keep + ps * f;
+        l = l * keep + pl * f;
+        m = to;
+    }
+    s_sum[tid] = sum;
+    s_m[tid] = m;
+    s_l[tid] = l;
+    __syncthreads();
+    if (group != 0 || !on || n <= sp.chunk) return;
+    for (int k = 1; k < groups; ++k) {
+        const int other = tid + (k << kLaneBits);
+        const float to = fmaxf(m, s_m[other]), keep = weight(m, to), f = weight(s_m[other], to);
+        sum = sum * keep + s_sum[other] * f;
+        l = l * keep + s_l[other] * f;
+        m = to;
+    }
+    store_out<T, D>(a, first, h, row, d, sum, l);
+}
+
+namespace {
+
+struct Plan {
+    int64_t chunk, chunks, rows, q_tiles;
+};
+
+// How a call is cut into workgroups over `chunk` keys: a row of up to kWholeBytes
+// of codes is one workgroup, and the call one launch (up to kFullBytes from
+// kFullUnits rows on); then kMany workgroups of kLeast keys or more, and at least
+// kFew of them.
+constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 512, kFew = 256,
+                  kFullUnits = 192;
+Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim) {
+    Plan p;
+    p.rows = max_new * group;
+    p.q_tiles = (p.rows + kQ - 1) / kQ;
+    const int64_t units = batch * kv_heads * p.q_tiles, step = kWaves * kKeys;
+    const int64_t keys = (max_len + step - 1) / step * step;
+    int64_t chunk = keys;
+    const int64_t whole = (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim);
+    if (max_len > whole) {
+        // (in float64: requests x heads x rows x keys may pass 64 bits)
+        const double all = (double)units * (double)keys;
+        chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
+        if (chunk < kLeast) chunk = kLeast;
+        if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = (int64_t)(all / kFew);
+    }
+    if (chunk < step) chunk = step;
+    chunk = (chunk + step - 1) / step * step;
+    p.chunk = chunk < keys ? chunk : keys > step ? keys : step;
+    p.chunks = keys > 0 ? (keys + p.chunk - 1) / p.chunk : 1;
+    return p;
+}
+
+template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
+    // (no more tiles of rows than the tokens at hand can fill)
+    const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
+    const int64_t q_tiles = (rows + kQ - 1) / kQ;
+    Attn8Split s = sp;
+    s.q_tiles = (int32_t)q_tiles;
+    const dim3 grid(a.cache.heads, a.batch, (unsigned)(q_tiles * sp.chunks));
+    // Codes that the L2 (32 MB in all) cannot hold are read past it.
+    const double bytes = 2.0 * a.batch * a.cache.heads * a.max_len * D;
+    if (q_tiles == 1 && bytes > 32e6) attn8_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, s);
+    else attn8_kernel<T, D, false><<<grid, 64 * kWaves, 0, st>>>(a, s);
+    if (sp.chunks > 1) {
+        int shift = 0;   // a group of lanes per chunk of the row, as far as a workgroup goes
+        while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin) ++shift;
+        const int64_t per = kJoin / (D / 4) >> shift;   // rows per workgroup
+        const dim3 rows_grid(a.cache.heads, a.batch, (unsigned)((rows + per - 1) / per));
+        attn8_join_kernel<T, D><<<rows_grid, kJoin, 0, st>>>(a, s, shift);
+    }
     return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t attn8_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len,
+                              int head_dim, int dtype) {
+    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim);
+    return p.chunks > 1 ? batch * kv_heads * p.rows * p.chunks * (head_dim + 2) * 4 : 0;
+}
+
+bool attn8_fits(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim,
+                int dtype) {
+    // a launch's grid: threads of x in 32 bits, 65536 workgroups in y and z
+    if (batch == 0) return true;
+    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim);
+    if (kv_heads > (1 << 22) - 1 || batch > 65535 + 1 || p.q_tiles > 65535 || p.q_tiles * p.chunks > 65535) return false;
+    return p.chunks == 1 || p.rows <= 65535;
+}
+
+hipError_t launch_attn8(const Attn8Args &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
+    const Plan p = plan(a.batch, a.cache.heads, a.group, a.max_new, a.max_len, head_dim);
+    Attn8Split sp{};
+    sp.chunk = (int32_t)p.chunk;
+    sp.chunks = (int32_t)p.chunks;
+    sp.rows = (int32_t)p.rows;
+    const int32_t parts = a.cache.page / 16;
+    sp.page_magic = parts == 1 ? 0 : (uint32_t)(((1ull << 32) + parts - 1) / parts);
+    if (p.chunks > 1) {
+        sp.sums = static_cast<float *>(workspace);
+        sp.stats = sp.sums + (int64_t)a.batch * a.cache.heads * p.rows * p.chunks * head_dim;
+    }
+    Attn8Args c = a;
+    // (no key past the table's width is seen)
+    if (c.max_len > (int64_t)a.table_width * a.cache.page) c.max_len = a.table_width * a.cache.page;
+    if (dtype == 1) return head_dim == 128 ? launch<_Float16, 128>(c, sp, st) : launch<_Float16, 64>(c, sp, st);
+    return head_dim == 128 ? launch<float, 128>(c, sp, st) : launch<float, 64>(c, sp, st);
 }
 
 }  // namespace mnb
