@@ -22,8 +22,7 @@
 // The next tile's key codes are requested as soon as this one's are in registers,
 // its value codes after the second product's reads.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
-#include "mnb_cache8.h"
-#include "mnb_device.h"
+#include "mnb_attn8.h"
 
 namespace mnb {
 
@@ -33,10 +32,7 @@ constexpr int kWaves = 4;
 constexpr int kQ = 16;       // query rows per row of tiles
 constexpr int kParts = 4;    // 16-key parts of a tile
 constexpr int kKeys = 16 * kParts;
-constexpr float kLowest = -3.402823466e38f;   // the maximum before any key
-constexpr float kLog2e = 1.4426950408889634f;
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -52,8 +48,6 @@ __device__ __forceinline__ uint32_t column_max(uint32_t x) {
     r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, x, false, false));
     return r.x > r.y ? r.x : r.y;
 }
-__device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
-__device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ float column_max(float x) {
     // (elements through functions: a bit cast of a vector's element reads the first)
     u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
@@ -64,56 +58,12 @@ __device__ __forceinline__ float column_max(float x) {
 
 __device__ __forceinline__ float weight(float x, float m) { return __builtin_amdgcn_exp2f((x - m) * kLog2e); }
 
-// New tokens of request b, and its first row of q.
-__device__ __forceinline__ int rows_of(const Attn8Args &a, int64_t b, int64_t &first) {
-    first = b;
-    if (!a.starts) return 1;
-    int64_t from = a.starts[b], to = a.starts[b + 1];
-    from = from < 0 ? 0 : from > a.tokens ? a.tokens : from;
-    to = to < from ? from : to > a.tokens ? a.tokens : to;
-    first = from;
-    return (int)(to - from);
-}
-
-// Keys that new token i of n of request b sees.
-__device__ __forceinline__ int sees(const Attn8Args &a, int len, int n, int i) {
-    const int64_t s = (int64_t)len - n + i + 1;
-    return s < 0 ? 0 : s < a.max_len ? (int)s : a.max_len;
-}
-
-// Blocks before a part of 16 keys.
-__device__ __forceinline__ uint32_t blocks_before(uint32_t part, uint32_t magic) {
-    const uint32_t place = __umulhi(part, magic);
-    return magic ? place : part;
-}
-
 // Where 16-byte piece c of LDS row `row` is: c ^ swizzle(row). The first product's
 // reads (16 rows, one piece) and the transposing ones (8 of 32 rows, one piece)
 // each touch all banks evenly.
 template <int D> __device__ __forceinline__ int swizzle(int row) {
     if constexpr (D == 128) return ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
     else return ((row >> 2) & 3) ^ ((row >> 4) & 1) << 1;
-}
-
-// Token and query head of row r of a (request, key-value head).
-__device__ __forceinline__ int token_of(const Attn8Args &a, int r) {
-    return a.max_new == 1 ? 0 : (int)((uint32_t)r / (uint32_t)a.group);
-}
-
-// Four outputs from dimension d on of row r.
-template <typename T, int D>
-__device__ __forceinline__ void store_out(const Attn8Args &a, int64_t first, int h, int r, int d, f4 sum, float total) {
-    const int token = token_of(a, r);
-    T *out = static_cast<T *>(a.out) +
-             ((first + token) * ((int64_t)a.cache.heads * a.group) + (int64_t)h * a.group + r - token * a.group) * D + d;
-    if (total == 0.0f) sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    else sum *= 1.0f / total;
-    if constexpr (sizeof(T) == 2) {
-        const u32x2 w = {as_u32(h2{(_Float16)sum.x, (_Float16)sum.y}), as_u32(h2{(_Float16)sum.z, (_Float16)sum.w})};
-        *reinterpret_cast<u32x2 *>(out) = w;
-    } else {
-        *reinterpret_cast<f4 *>(out) = sum;
-    }
 }
 
 // Sixteen numbers of a query row as three digits each, most significant last:
@@ -137,18 +87,6 @@ __device__ __forceinline__ void digits_of(const float *x, float up, i32x4 *digit
 }
 
 }  // namespace
-
-// How a launch is cut. Pieces of rows of more than one chunk: per (request,
-// head, query row, chunk) D sums, and a maximum and the weights' sum.
-struct Attn8Split {
-    int32_t chunk;        // keys per chunk
-    int32_t chunks;       // of max_len
-    int32_t rows;         // bound of the rows per (request, head)
-    int32_t q_tiles;
-    uint32_t page_magic;  // ceil(2^32 / (page / 16)), 0 for pages of 16: part * magic >> 32 is
-                          // part / (page / 16) for part < 2^26
-    float *sums, *stats;
-};
 
 template <typename T, int D, bool STREAM>
 __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8Split &sp) {
@@ -519,9 +457,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn8_kernel(Attn8Args a, Attn
 // Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
 // D / 4 lanes, which take every 2^shift-th chunk; then their sums are added.
 constexpr int kJoin = 256;
-template <typename T, int D>
+template <typename T, int D, bool LOG2>
 __global__ __launch_bounds__(kJoin) void attn8_join_kernel(Attn8Args a, Attn8Split sp, int shift) {
     constexpr int kLanes = D / 4, kLaneBits = D == 128 ? 5 : 4;
+    auto weight = [](float x, float m) { return __builtin_amdgcn_exp2f(LOG2 ? x - m : (x - m) * kLog2e); };
     __shared__ f4 s_sum[kJoin];
     __shared__ float s_m[kJoin], s_l[kJoin];
     const int tid = threadIdx.x, d = tid % kLanes * 4, groups = 1 << shift;
@@ -534,7 +473,7 @@ __global__ __launch_bounds__(kJoin) void attn8_join_kernel(Attn8Args a, Attn8Spl
     const int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group;
     const bool on = row < rows;
     // the keys of the row's tile: its last row's
-    int last = (row / kQ + 1) * kQ - 1;
+    int last = (int)((uint32_t)row / (uint32_t)sp.tile + 1) * sp.tile - 1;
     last = last < rows ? last : rows - 1;
     const int n = on ? sees(a, len, n_new, token_of(a, last)) : 0;
     const int64_t from_piece = ((b * a.cache.heads + h) * sp.rows + (on ? row : 0)) * sp.chunks;
@@ -567,26 +506,32 @@ __global__ __launch_bounds__(kJoin) void attn8_join_kernel(Attn8Args a, Attn8Spl
 namespace {
 
 struct Plan {
-    int64_t chunk, chunks, rows, q_tiles;
+    int64_t chunk, chunks, rows, q_tiles, tile;
+    bool many;
 };
 
-// How a call is cut into workgroups over `chunk` keys: a row of up to kWholeBytes
-// of codes is one workgroup, and the call one launch (up to kFullBytes from
-// kFullUnits rows on); then kMany workgroups of kLeast keys or more, and at least
-// kFew of them.
+// Which kernel, and how a call is cut into workgroups over `chunk` keys. Few rows: a
+// row of up to kWholeBytes of codes is one workgroup, and the call one launch (up
+// to kFullBytes from kFullUnits rows on); then kMany workgroups of kLeast keys or
+// more, and at least kFew of them. Many rows: kManyWgs workgroups, of kManyKeys
+// keys or more.
 constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 512, kFew = 256,
-                  kFullUnits = 192;
-Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim) {
+                  kFullUnits = 192, kManyWgs = 512, kManyKeys = 256, kManyRows = 33;
+Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.rows = max_new * group;
-    p.q_tiles = (p.rows + kQ - 1) / kQ;
-    const int64_t units = batch * kv_heads * p.q_tiles, step = kWaves * kKeys;
+    p.many = dtype == 1 && p.rows >= kManyRows;
+    p.tile = p.many ? kRowTile : kQ;
+    p.q_tiles = (p.rows + p.tile - 1) / p.tile;
+    const int64_t units = batch * kv_heads * p.q_tiles, step = p.many ? 64 : kWaves * kKeys;
     const int64_t keys = (max_len + step - 1) / step * step;
     int64_t chunk = keys;
-    const int64_t whole = (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim);
-    if (max_len > whole) {
-        // (in float64: requests x heads x rows x keys may pass 64 bits)
-        const double all = (double)units * (double)keys;
+    // (in float64: requests x heads x rows x keys may pass 64 bits)
+    const double all = (double)units * (double)keys;
+    if (p.many) {
+        if (all / kManyWgs < (double)keys) chunk = (int64_t)(all / kManyWgs);
+        if (chunk < kManyKeys) chunk = kManyKeys;
+    } else if (max_len > (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim)) {
         chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
         if (chunk < kLeast) chunk = kLeast;
         if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = (int64_t)(all / kFew);
@@ -598,24 +543,33 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64
     return p;
 }
 
-template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
-    // (no more tiles of rows than the tokens at hand can fill)
-    const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
-    const int64_t q_tiles = (rows + kQ - 1) / kQ;
-    Attn8Split s = sp;
-    s.q_tiles = (int32_t)q_tiles;
-    const dim3 grid(a.cache.heads, a.batch, (unsigned)(q_tiles * sp.chunks));
+template <typename T, int D> void launch_few(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
+    const dim3 grid(a.cache.heads, a.batch, (unsigned)(sp.q_tiles * sp.chunks));
     // Codes that the L2 (32 MB in all) cannot hold are read past it.
     const double bytes = 2.0 * a.batch * a.cache.heads * a.max_len * D;
-    if (q_tiles == 1 && bytes > 32e6) attn8_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, s);
-    else attn8_kernel<T, D, false><<<grid, 64 * kWaves, 0, st>>>(a, s);
-    if (sp.chunks > 1) {
-        int shift = 0;   // a group of lanes per chunk of the row, as far as a workgroup goes
-        while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin) ++shift;
-        const int64_t per = kJoin / (D / 4) >> shift;   // rows per workgroup
-        const dim3 rows_grid(a.cache.heads, a.batch, (unsigned)((rows + per - 1) / per));
-        attn8_join_kernel<T, D><<<rows_grid, kJoin, 0, st>>>(a, s, shift);
+    if (sp.q_tiles == 1 && bytes > 32e6) attn8_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, sp);
+    else attn8_kernel<T, D, false><<<grid, 64 * kWaves, 0, st>>>(a, sp);
+}
+
+template <typename T, int D, bool LOG2> void launch_join(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
+    int shift = 0;   // a group of lanes per chunk of the row, as far as a workgroup goes
+    while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin) ++shift;
+    const int64_t per = kJoin / (D / 4) >> shift;   // rows per workgroup
+    const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
+    const dim3 grid(a.cache.heads, a.batch, (unsigned)((rows + per - 1) / per));
+    attn8_join_kernel<T, D, LOG2><<<grid, kJoin, 0, st>>>(a, sp, shift);
+}
+
+template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Split &sp, bool many, hipStream_t st) {
+    if constexpr (sizeof(T) == 2) {
+        if (many) {
+            if (hipError_t e = launch_attn8_rows(a, sp, D, st)) return e;
+            if (sp.chunks > 1) launch_join<T, D, true>(a, sp, st);
+            return hipGetLastError();
+        }
     }
+    launch_few<T, D>(a, sp, st);
+    if (sp.chunks > 1) launch_join<T, D, false>(a, sp, st);
     return hipGetLastError();
 }
 
@@ -623,7 +577,7 @@ template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Sp
 
 int64_t attn8_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len,
                               int head_dim, int dtype) {
-    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim);
+    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim, dtype);
     return p.chunks > 1 ? batch * kv_heads * p.rows * p.chunks * (head_dim + 2) * 4 : 0;
 }
 
@@ -631,17 +585,21 @@ bool attn8_fits(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new,
                 int dtype) {
     // a launch's grid: threads of x in 32 bits, 65536 workgroups in y and z
     if (batch == 0) return true;
-    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim);
-    if (kv_heads > (1 << 22) - 1 || batch > 65535 + 1 || p.q_tiles > 65535 || p.q_tiles * p.chunks > 65535) return false;
+    const Plan p = plan(batch, kv_heads, group, max_new, max_len, head_dim, dtype);
+    if (kv_heads > (1 << 22) - 1 || batch > 65536 || p.q_tiles > 65535 || p.q_tiles * p.chunks > 65535) return false;
     return p.chunks == 1 || p.rows <= 65535;
 }
 
 hipError_t launch_attn8(const Attn8Args &a, int head_dim, int dtype, void *workspace, hipStream_t st) {
-    const Plan p = plan(a.batch, a.cache.heads, a.group, a.max_new, a.max_len, head_dim);
+    const Plan p = plan(a.batch, a.cache.heads, a.group, a.max_new, a.max_len, head_dim, dtype);
     Attn8Split sp{};
     sp.chunk = (int32_t)p.chunk;
     sp.chunks = (int32_t)p.chunks;
     sp.rows = (int32_t)p.rows;
+    sp.tile = (int32_t)p.tile;
+    // (no more tiles of rows than the tokens at hand can fill)
+    const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
+    sp.q_tiles = (int32_t)((rows + p.tile - 1) / p.tile);
     const int32_t parts = a.cache.page / 16;
     sp.page_magic = parts == 1 ? 0 : (uint32_t)(((1ull << 32) + parts - 1) / parts);
     if (p.chunks > 1) {
@@ -651,8 +609,9 @@ hipError_t launch_attn8(const Attn8Args &a, int head_dim, int dtype, void *works
     Attn8Args c = a;
     // (no key past the table's width is seen)
     if (c.max_len > (int64_t)a.table_width * a.cache.page) c.max_len = a.table_width * a.cache.page;
-    if (dtype == 1) return head_dim == 128 ? launch<_Float16, 128>(c, sp, st) : launch<_Float16, 64>(c, sp, st);
-    return head_dim == 128 ? launch<float, 128>(c, sp, st) : launch<float, 64>(c, sp, st);
+    if (dtype == 1)
+        return head_dim == 128 ? launch<_Float16, 128>(c, sp, p.many, st) : launch<_Float16, 64>(c, sp, p.many, st);
+    return head_dim == 128 ? launch<float, 128>(c, sp, p.many, st) : launch<float, 64>(c, sp, p.many, st);
 }
 
 }  // namespace mnb

@@ -36,14 +36,6 @@ int check_heads(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int6
     return attn_fits(B, Hkv, rows, Tk, (int)head_dim, dtype) ? MNB_OK : MNB_ERR_SHAPE;
 }
 
-// The scale the kernels take. Float16 scores are multiplied by scale * log2(e) at
-// once, which must not overflow: products of float16 rows are whole multiples of
-// 2^-48 and below 2^40, so at 2^80 all scores are finite and different ones 2^32
-// apart, and a larger scale has the same softmax.
-float kernel_scale(float scale, int dtype) {
-    return dtype == MNB_F16 ? copysignf(fminf(fabsf(scale), 0x1p80f), scale) : scale;
-}
-
 // Workspace of a cross attention call: by sizes alone, whichever kernel its
 // strides allow.
 int64_t cross_workspace(int64_t B, int64_t Hkv, int64_t rows, int64_t Tk, int head_dim, int dtype) {

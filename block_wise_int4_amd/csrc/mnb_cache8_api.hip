@@ -231,7 +231,7 @@ int mnb_paged_attn_i8(const void *q, int64_t q_stride, const mnb_kv_cache_i8 *ca
     a.max_new = (int32_t)max_new;
     a.max_len = (int32_t)max_len;
     a.table_width = (int32_t)max_blocks;
-    a.scale = scale;
+    a.scale = kernel_scale(scale, cache->dtype);
     return hip_status(launch_attn8(a, head_dim, cache->dtype, workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -2,6 +2,7 @@
 // the 8-bit cache and of the rotary positions. Host only.
 #pragma once
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/mnb.h"
@@ -41,6 +42,14 @@ inline int check_strides(int64_t a, int64_t b, int64_t c, int dtype) {
     if (a < 0 || b < 0 || c < 0 || a > most || b > most || c > most) return MNB_ERR_SHAPE;
     if (a % unit || b % unit || c % unit) return MNB_ERR_ALIGN;
     return MNB_OK;
+}
+
+// The scale the kernels take. Float16 scores are multiplied by scale * log2(e) at
+// once, which must not overflow: products of float16 rows are whole multiples of
+// 2^-48 and below 2^40, so at 2^80 all scores are finite and different ones 2^32
+// apart, and a larger scale has the same softmax.
+inline float kernel_scale(float scale, int dtype) {
+    return dtype == MNB_F16 ? copysignf(fminf(fabsf(scale), 0x1p80f), scale) : scale;
 }
 
 inline int check_workspace(int64_t need, const void *workspace, size_t bytes) {
