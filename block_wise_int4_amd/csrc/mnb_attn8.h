@@ -18,7 +18,8 @@ __device__ __forceinline__ uint32_t as_bits(float x) { return __builtin_bit_cast
 __device__ __forceinline__ int rows_of(const Attn8Args &a, int64_t b, int64_t &first) {
     first = b;
     if (!a.starts) return 1;
-    int64_t from = a.starts[b], to = a.starts[b + 1];
+    typedef __attribute__((address_space(4))) const int32_t entry;   // (a scalar load)
+    int64_t from = ((entry *)a.starts)[b], to = ((entry *)a.starts)[b + 1];
     from = from < 0 ? 0 : from > a.tokens ? a.tokens : from;
     to = to < from ? from : to > a.tokens ? a.tokens : to;
     first = from;

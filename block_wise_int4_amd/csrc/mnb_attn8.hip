@@ -66,24 +66,16 @@ template <int D> __device__ __forceinline__ int swizzle(int row) {
     else return ((row >> 2) & 3) ^ ((row >> 4) & 1) << 1;
 }
 
-// Sixteen numbers of a query row as three digits each, most significant last:
-// x * 2^up, up to 2^22, rounded.
-__device__ __forceinline__ void digits_of(const float *x, float up, i32x4 *digit) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint32_t d0 = 0, d1 = 0, d2 = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (the low two bytes' digits are signed: 128 too much, and less again)
-            const uint32_t n = (uint32_t)((int)__builtin_rintf(x[4 * w + i] * up) + 0x8080);
-            d0 |= (n & 0xFF) << (8 * i);
-            d1 |= (n >> 8 & 0xFF) << (8 * i);
-            d2 |= (n >> 16 & 0xFF) << (8 * i);
-        }
-        digit[0][w] = (int)(d0 ^ 0x80808080u);
-        digit[1][w] = (int)(d1 ^ 0x80808080u);
-        digit[2][w] = (int)d2;
-    }
+// The lower three bytes of four numbers w = n + 0x8080 by their place: signed digits of
+// n, the lower two 128 too much, and less again by the sign bit.
+__device__ __forceinline__ void digits_of(const uint32_t *w, uint32_t *digit) {
+    const uint32_t a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);   // bytes 0, 0, 1, 1
+    const uint32_t a23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+    const uint32_t b01 = __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0602u);   // bytes 2, 2
+    const uint32_t b23 = __builtin_amdgcn_perm(w[3], w[2], 0x06020C0Cu);
+    digit[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100u) ^ 0x80808080u;
+    digit[1] = __builtin_amdgcn_perm(a23, a01, 0x07060302u) ^ 0x80808080u;
+    digit[2] = b01 | b23;
 }
 
 }  // namespace
@@ -94,6 +86,7 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     constexpr int kPieces = D / 16;     // of a row of codes
     constexpr int kTile = kKeys * D;    // bytes
     constexpr int kOut = D / 16;        // 16-dimension parts of the output
+    constexpr int kBehind = kParts + kParts * kLoads;   // loads of a tile's scales and codes, keys or values
     // the waves' tiles of key and value codes (arrays of their own: the compiler then
     // knows that reads of one need not wait for loads into the other); in the end their
     // sums [kWaves][kQ][D], and maxima and weights' sums [kWaves][kQ]
@@ -103,24 +96,12 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     const int h = blockIdx.x, chunk = blockIdx.z / sp.q_tiles, q_tile = blockIdx.z - chunk * sp.q_tiles;
     const int64_t b = blockIdx.y;
     const Cache8 &c = a.cache;
-    const int begin = chunk * sp.chunk;
-    int key = begin + wave * kKeys;
-    // (no kernel writes the table while this one reads it: scalar loads)
-    typedef __attribute__((address_space(4))) const int32_t table_entry;
-    table_entry *table = (table_entry *)(a.table + b * a.table_width);
-    // The table entries of the tile at key0 (past the table's end its last
-    // entry, which is not used).
-    int32_t ids[kParts];
-    auto look_up = [&](int key0) {
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-            const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + s, sp.page_magic);
-            ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
-        }
-    };
-    look_up(key);
+    const int begin = chunk * sp.chunk, step = kWaves * kKeys;
+    int key = begin + wave * kKeys - step;   // (the loop's first turn only requests)
+    // (no kernel writes the lengths while this one reads them: a scalar load)
+    typedef __attribute__((address_space(4))) const int32_t entry;
     int64_t first;
-    const int len = a.lens[b], n_new = rows_of(a, b, first);
+    const int len = ((entry *)a.lens)[b], n_new = rows_of(a, b, first);
     const int row0 = q_tile * kQ;
     int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group - row0;
     if (rows <= 0) return;
@@ -131,6 +112,16 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;
     const int r = row0 + (col < rows ? col : 0), token = token_of(a, r);
     const int mine = sees(a, len, n_new, token);
+
+    // Lanes l look after part l % 4 of the next tile: its table entry (past the table's
+    // end the last one, which is not used) is requested a step ahead.
+    const int my_part = lane & (kParts - 1);
+    const int32_t *table = a.table + b * a.table_width;
+    auto entry_of = [&](int key0) {
+        const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + my_part, sp.page_magic);
+        return table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
+    };
+    int32_t id = entry_of(key + step);
 
     // queries: lane (query col, pieces 4 j + g of 16 dimensions), in digits
     i32x4 q[kLoads][3];
@@ -152,51 +143,70 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                     else v = __builtin_bit_cast(f4, w)[i];
                     x[j][p * (16 / (int)sizeof(T)) + i] = v;
                     // (as whole numbers: infinities and NaN are above every finite one)
-                    const uint32_t bits = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+                    const uint32_t bits = as_bits(v) & 0x7FFFFFFFu;
                     top = bits > top ? bits : top;
                 }
             }
         top = column_max(top);
         const bool finite = top < 0x7F800000u;
-        // 2^(e - 127) <= largest < 2^(e - 126), twice as large numbers for the smallest
-        int lift = 0;
-        if (top < (64u << 23)) {
-            lift = 64;
-            top = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, top) * 0x1p64f);
-        }
+        // 2^(e - 127) <= largest < 2^(e - 126), the smallest ones 2^64 times as large
+        const bool small = top < (64u << 23);
+        const float lift = small ? 0x1p64f : 1.0f;
+        if (small) top = as_bits(as_float(top) * 0x1p64f);
         const int e = top ? (int)(top >> 23) : 127;
-        const float up = __builtin_bit_cast(float, (uint32_t)(127 + 21 + 127 - e) << 23);
-        mul = finite ? __builtin_ldexpf(a.scale, e - 127 - 21 - lift) : __builtin_nanf("");
+        const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
+        mul = finite ? __builtin_ldexpf(a.scale, e - 127 - 21 - (small ? 64 : 0)) : __builtin_nanf("");
+        // whole numbers n, |n| < 2^22 (one that would round to 2^22 stays one below), as
+        // the bits of 2^23 + 2^22 + n less those of n = 0
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < kLoads; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[j][i] = finite ? (lift ? x[j][i] * 0x1p64f : x[j][i]) : 0.0f;
-            digits_of(x[j], up, q[j]);
-        }
+            for (int k = 0; k < 4; ++k) {
+                uint32_t w[4], digit[3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = finite ? x[j][4 * k + i] * lift * up : 0.0f;
+                    w[i] = as_bits(__builtin_amdgcn_fmed3f(v, -4194303.0f, 4194303.0f) + 12582912.0f) +
+                           (0x8080u - 0x4B400000u);
+                }
+                digits_of(w, digit);
+                q[j][0][k] = (int)digit[0];
+                q[j][1][k] = (int)digit[1];
+                q[j][2][k] = (int)digit[2];
+            }
     }
 
-    // One tile: a part (16 keys) is read through buffers that end with its last key
-    // that any row sees; a part without keys reads nothing.
-    const int8_t *kp = c.k + h * c.head_stride, *vp = c.v + h * c.head_stride;
-    const float *ksp = c.k_scale + h * c.scale_head, *vsp = c.v_scale + h * c.scale_head;
-    const uint32_t stride = (uint32_t)c.token_stride;
-    int valid[kParts], valid_next[kParts];   // leading keys of each part
-    uint32_t block[kParts], row[kParts]; // where it is
-    auto locate = [&](int key0, int *valid) {
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-            const int first_key = key0 + 16 * s;
-            int ok = end - first_key;
-            ok = ok < 0 ? 0 : ok > 16 ? 16 : ok;
-            const uint32_t part = (uint32_t)first_key >> 4;
-            block[s] = ids[s];
-            row[s] = (part - blocks_before(part, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
-            valid[s] = __builtin_amdgcn_readfirstlane(block[s] < (uint64_t)c.num_blocks ? ok : 0);
-        }
+    asm volatile("" : "+v"(id));   // (the entry is there: no wait for it in the loop's first turn)
+
+    // Where the next tile is: bytes to its parts' codes and scales (of keys and of values
+    // alike), and how many codes there are: a part past the last key, or without a
+    // block, is read through a buffer of no bytes. (Rows of a page past the last key are
+    // read, and weigh nothing.) Worked out by the parts' lanes, read from there where a
+    // load needs it: in scalar registers it takes 400 instructions a tile, and more
+    // registers than there are.
+    const uint32_t stride = (uint32_t)c.token_stride, part_bytes = 15 * stride + D;
+    uint64_t from = 0, from_scales = 0;
+    uint32_t bytes = 0;
+    uint32_t there = 0, there_next = 0;   // a bit for each part
+    auto locate = [&](int key0) {
+        const uint32_t part = ((uint32_t)key0 >> 4) + my_part;
+        const uint32_t row = (part - blocks_before(part, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
+        const bool ok = (uint32_t)id < (uint32_t)c.num_blocks && key0 + 16 * my_part < end;
+        const uint64_t block = ok ? (uint32_t)id : 0u;
+        bytes = ok ? part_bytes : 0u;
+        from = block * (uint64_t)c.block_stride + (uint64_t)row * stride;
+        from_scales = (block * (uint64_t)c.scale_block + row) * 4;
+        there_next = (uint32_t)__ballot(ok) & ((1u << kParts) - 1);
     };
-    auto buffer = [&](const void *base, uint32_t bytes) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
+    auto of_part = [&](uint32_t x, int s) { return (uint32_t)__builtin_amdgcn_readlane((int)x, s); };
+    auto buffer = [&](const void *base, uint64_t at, int s, uint32_t most) {
+        const uint64_t there = (uint64_t)of_part((uint32_t)(at >> 32), s) << 32 | of_part((uint32_t)at, s);
+        const uint32_t n = of_part(bytes, s);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + there, 0,
+                                                 n < most ? n : most, 0x00020000);
     };
+    const int8_t *keys = c.k + h * c.head_stride, *values = c.v + h * c.head_stride;
+    const float *key_scales = c.k_scale + h * c.scale_head, *value_scales = c.v_scale + h * c.scale_head;
     // A load to LDS takes whole rows, 64 lanes on 1 KB after another.
     constexpr int kRows = 64 / kPieces;   // of a load
     uint8_t *s_k = s_keys[wave], *s_v = s_values[wave];
@@ -208,30 +218,54 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
             const int row = j * kRows + lane / kPieces;
             at[odd][j] = (uint32_t)row * stride + ((lane % kPieces) ^ swizzle<D>(16 * odd + row)) * 16;
         }
-    auto load_codes = [&](const int8_t *base, uint8_t *to, const int *valid) {
+    auto load_codes = [&](const int8_t *base, uint8_t *to) {
 #pragma unroll
         for (int s = 0; s < kParts; ++s) {
-            const auto rows_in = buffer(base + (int64_t)block[s] * c.block_stride + (int64_t)row[s] * stride,
-                                        valid[s] > 0 ? (uint32_t)(valid[s] - 1) * stride + D : 0u);
+            const auto rows_in = buffer(base, from, s, ~0u);
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_in, (lds_void *)(to + (s * kLoads + j) * 1024), 16,
                                                          at[s & 1][j], 0, 0, STREAM ? 2 : 0);
         }
     };
-    auto load_scales = [&](const float *base, f4 *to, const int *valid) {
+    auto load_scales = [&](const float *base, f4 *to) {
 #pragma unroll
         for (int s = 0; s < kParts; ++s)
-            to[s] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               buffer(base + (int64_t)block[s] * c.scale_block + row[s],
-                                                      valid[s] > 0 ? 64u : 0u),
-                                               g * 16, 0, 0));
+            to[s] = __builtin_bit_cast(
+                f4, __builtin_amdgcn_raw_buffer_load_b128(buffer(base, from_scales, s, 64u), g * 16, 0, 0));
     };
-    // (the places are worked out again for the values: kept, they take 24 scalar
-    // registers more than there are)
-    auto forget = [&]() {
+    // Keys: lane (key col, g) takes piece 4 j + g of its row in each part. (With its waits:
+    // the compiler waits for the values' loads as well, which come after.)
+    uint32_t k_at[2][kLoads];
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) asm volatile("" : "+s"(block[s]), "+s"(row[s]), "+s"(valid_next[s]));
+    for (int odd = 0; odd < 2; ++odd)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int row = 16 * odd + col;
+            k_at[odd][j] = (uint32_t)(size_t)(lds_void *)s_k + row * D + ((4 * j + g) ^ swizzle<D>(row)) * 16;
+        }
+    auto read_keys = [&](i32x4 (*k)[kLoads]) {
+        if constexpr (kLoads == 2)
+            asm volatile(
+                "s_waitcnt vmcnt(%13)\n\t"
+                "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+                "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\t"
+                "ds_read_b128 %6, %10 offset:%12\n\tds_read_b128 %7, %11 offset:%12\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(k[0][0]), "=&v"(k[0][kLoads - 1]), "=&v"(k[1][0]), "=&v"(k[1][kLoads - 1]), "=&v"(k[2][0]),
+                  "=&v"(k[2][kLoads - 1]), "=&v"(k[3][0]), "=&v"(k[3][kLoads - 1])
+                : "v"(k_at[0][0]), "v"(k_at[0][kLoads - 1]), "v"(k_at[1][0]), "v"(k_at[1][kLoads - 1]), "n"(32 * D),
+                  "n"(kBehind)
+                : "memory");
+        else
+            asm volatile(
+                "s_waitcnt vmcnt(%7)\n\t"
+                "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
+                "ds_read_b128 %2, %4 offset:%6\n\tds_read_b128 %3, %5 offset:%6\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(k[0][0]), "=&v"(k[1][0]), "=&v"(k[2][0]), "=&v"(k[3][0])
+                : "v"(k_at[0][0]), "v"(k_at[1][0]), "n"(32 * D), "n"(kBehind)
+                : "memory");
     };
 
     // Values, turned: 16 lanes read eight keys by 16 dimensions. Lane L supplies key
@@ -241,10 +275,10 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     // next keys' among them.
     const int v_row = 16 * (col >> 3) + 4 * g + ((col >> 1) & 3);   // (u = 0; u = 1 is 32 rows on)
     const uint32_t v_at = (uint32_t)(size_t)(lds_void *)s_v + v_row * D + (col & 1) * 8;
-    auto read_values = [&](i32x2 (*v)[2], uint32_t base, int d) {
+    auto read_values = [&](i32x2 (*v)[2], int d) {
         uint32_t at[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) at[e] = base + ((d + e) ^ swizzle<D>(v_row)) * 16;
+        for (int e = 0; e < 4; ++e) at[e] = v_at + ((d + e) ^ swizzle<D>(v_row)) * 16;
         asm volatile(
             "ds_read_b64_tr_b8 %0, %8\n\tds_read_b64_tr_b8 %1, %8 offset:%12\n\t"
             "ds_read_b64_tr_b8 %2, %9\n\tds_read_b64_tr_b8 %3, %9 offset:%12\n\t"
@@ -262,33 +296,15 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     for (int i = 0; i < kOut; ++i) o[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLowest, l = 0.0f;
     f4 ks[kParts], vs[kParts];
-    const int step = kWaves * kKeys;
-    if (key < end) {
-        locate(key, valid_next);
-        load_scales(ksp, ks, valid_next);
-        load_codes(kp, s_k, valid_next);
-        asm volatile("" ::: "memory");   // (in this order: the waits below count them)
-        look_up(key + step);
-        forget();
-        load_scales(vsp, vs, valid_next);
-        load_codes(vp, s_v, valid_next);
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) valid[s] = valid_next[s];
-    }
-    for (; key < end; key += step) {
-        // this tile's key codes are in LDS: all but the loads after theirs have come
-        // back (the compiler does not wait for loads to LDS)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kParts + kParts * kLoads) : "memory");
+    // (past the last tile loads of no bytes are requested: with a way around them the
+    // compiler counts none, and waits too long for those before)
+    do {
+        const bool real = key >= begin;   // (uniform)
         float x[kParts][4];
-        {
+        if (real) {
+            // (this tile's key codes are in LDS when all but its values' loads have come back)
             i32x4 kk[kParts][kLoads];
-#pragma unroll
-            for (int s = 0; s < kParts; ++s)
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) {
-                    const int row = 16 * s + col;
-                    kk[s][j] = *reinterpret_cast<const i32x4 *>(s_k + row * D + ((4 * j + g) ^ swizzle<D>(row)) * 16);
-                }
+            read_keys(kk);
 #pragma unroll
             for (int s = 0; s < kParts; ++s) {
                 i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
@@ -306,101 +322,91 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                 for (int i = 0; i < 4; ++i) x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * by[i];
             }
         }
-        locate(key + step, valid_next);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the reads of these codes are over
-        load_scales(ksp, ks, valid_next);
-        load_codes(kp, s_k, valid_next);
-        asm volatile("" ::: "memory");
-        look_up(key + 2 * step);
-        bool partial = key + kKeys > least;
+        locate(key + step);
+        load_scales(key_scales, ks);
+        load_codes(keys, s_k);
+        id = entry_of(key + 2 * step);
+        asm volatile("" ::: "memory");   // (in this order: the waits count them)
+        if (real) {
+            if (key + kKeys > least || there != (1u << kParts) - 1)   // uniform: the end of a row, or a missing block
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) partial |= valid[s] < 16;
-        if (partial) {   // uniform: the end of a row, or a missing block
+                for (int s = 0; s < kParts; ++s) {
+                    const int left = there >> s & 1 ? mine - key - 16 * s - 4 * g : 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[s][i] = i < left ? x[s][i] : -__builtin_inff();
+                        vs[s][i] = i < left ? vs[s][i] : 0.0f;
+                    }
+                }
+            float top = x[0][0];
+#pragma unroll
+            for (int s = 0; s < kParts; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[s][i]);
+            top = column_max(top);
+            if (__any(top > m)) {
+                const float to = fmaxf(m, top), keep = weight(m, to);
+                m = to;
+                l *= keep;
+#pragma unroll
+                for (int i = 0; i < kOut; ++i) o[i] *= keep;
+            }
+            // weights times value scales, and the largest of the tile (as whole numbers:
+            // they are not negative, and NaN is above all)
+            uint32_t most = 0;
 #pragma unroll
             for (int s = 0; s < kParts; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int at_part = 4 * g + i;
-                    const bool seen = at_part < valid[s] && key + 16 * s + at_part < mine;
-                    x[s][i] = seen ? x[s][i] : -__builtin_inff();
-                    vs[s][i] = seen ? vs[s][i] : 0.0f;
+                    const float w = weight(x[s][i], m);
+                    l += w;
+                    x[s][i] = w * vs[s][i];
+                    const uint32_t bits = as_bits(x[s][i]) & 0x7FFFFFFFu;
+                    most = bits > most ? bits : most;
                 }
-        }
-        float top = x[0][0];
+            most = column_max(most);
+            // numbers below 2^22: times 2^(21 - exponent), a touch less so that none rounds
+            // up to it
+            const bool finite = most < 0x7F800000u;
+            int e = (int)(most >> 23);
+            e = e < 24 ? 24 : e;
+            const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23) * (1.0f - 0x1p-21f);
+            const float down = finite ? as_float((uint32_t)(e - 21) << 23) * (1.0f + 0x1p-21f) : __builtin_nanf("");
+            i32x4 p[3];
 #pragma unroll
-        for (int s = 0; s < kParts; ++s)
+            for (int s = 0; s < kParts; ++s) {
+                uint32_t w[4], digit[3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, x[s][i]);
-        top = column_max(top);
-        if (__any(top > m)) {
-            const float to = fmaxf(m, top), keep = weight(m, to);
-            m = to;
-            l *= keep;
+                for (int i = 0; i < 4; ++i) w[i] = as_bits(__builtin_fmaf(x[s][i], up, 8388608.0f + 32896.0f));
+                digits_of(w, digit);
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) o[i] *= keep;
-        }
-        // weights times value scales, and the largest of the tile (as whole numbers:
-        // they are not negative, and NaN is above all)
-        uint32_t most = 0;
-#pragma unroll
-        for (int s = 0; s < kParts; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w = weight(x[s][i], m);
-                l += w;
-                x[s][i] = w * vs[s][i];
-                const uint32_t bits = as_bits(x[s][i]) & 0x7FFFFFFFu;
-                most = bits > most ? bits : most;
+                for (int t = 0; t < 3; ++t) p[t][s] = (int)digit[t];
             }
-        most = column_max(most);
-        // numbers below 2^22: times 2^(21 - exponent), a touch less so that none rounds
-        // up to it; at 2^23 + 0x8080 their bytes are the digits, 128 too much in two
-        const bool finite = most < 0x7F800000u;
-        int e = (int)(most >> 23);
-        e = e < 24 ? 24 : e;
-        const float up = __builtin_bit_cast(float, (uint32_t)(127 + 21 + 127 - e) << 23) * (1.0f - 0x1p-21f);
-        const float down = finite ? __builtin_bit_cast(float, (uint32_t)(e - 21) << 23) * (1.0f + 0x1p-21f)
-                                  : __builtin_nanf("");
-        i32x4 p[3];
+            // this tile's value codes are in LDS: all but the next keys' loads, and the entry's
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBehind + 1) : "memory");
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-            uint32_t w[4];
+            for (int d = 0; d < kOut; d += 4) {
+                i32x2 v[4][2];
+                read_values(v, d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = as_bits(__builtin_fmaf(x[s][i], up, 8388608.0f + 32896.0f));
-            const uint32_t a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);   // bytes 0, 0, 1, 1
-            const uint32_t a23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
-            const uint32_t b01 = __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0602u);   // bytes 2, 2
-            const uint32_t b23 = __builtin_amdgcn_perm(w[3], w[2], 0x06020C0Cu);
-            p[0][s] = (int)(__builtin_amdgcn_perm(a23, a01, 0x05040100u) ^ 0x80808080u);
-            p[1][s] = (int)(__builtin_amdgcn_perm(a23, a01, 0x07060302u) ^ 0x80808080u);
-            p[2][s] = (int)(b01 | b23);
-        }
-        // this tile's value codes are in LDS: all but the next keys' loads
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kParts + kParts * kLoads) : "memory");
+                for (int k = 0; k < 4; ++k) {
+                    const i32x4 zero = {0, 0, 0, 0}, vv = {v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y};
+                    const i32x4 lo = mma64(vv, p[0], zero), hi = mma64(vv, p[1], mma64(vv, p[2], zero) << 8);
 #pragma unroll
-        for (int d = 0; d < kOut; d += 4) {
-            i32x2 v[4][2];
-            read_values(v, v_at, d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const i32x4 zero = {0, 0, 0, 0}, vv = {v[e][0].x, v[e][0].y, v[e][1].x, v[e][1].y};
-                const i32x4 lo = mma64(vv, p[0], zero), hi = mma64(vv, p[1], mma64(vv, p[2], zero) << 8);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[d + e][i] = __builtin_fmaf(__builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]), down, o[d + e][i]);
+                    for (int i = 0; i < 4; ++i)
+                        o[d + k][i] =
+                            __builtin_fmaf(__builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]), down, o[d + k][i]);
+                }
             }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        forget();
-        load_scales(vsp, vs, valid_next);
-        load_codes(vp, s_v, valid_next);
+        load_scales(value_scales, vs);
+        load_codes(values, s_v);
         asm volatile("" ::: "memory");
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) valid[s] = valid_next[s];
-    }
+        there = there_next;
+        key += step;
+    } while (key < end);
 
-    // (the tile past the end has arrived everywhere: its place is free)
+    // (the tile past the end, no bytes, has arrived everywhere: its place is free)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
@@ -457,6 +463,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn8_kernel(Attn8Args a, Attn
 // Joins the chunks of query rows, in a fixed order: a row has 2^shift groups of
 // D / 4 lanes, which take every 2^shift-th chunk; then their sums are added.
 constexpr int kJoin = 256;
+constexpr int64_t kJoinLanes = 1 << 18;
 template <typename T, int D, bool LOG2>
 __global__ __launch_bounds__(kJoin) void attn8_join_kernel(Attn8Args a, Attn8Split sp, int shift) {
     constexpr int kLanes = D / 4, kLaneBits = D == 128 ? 5 : 4;
@@ -552,10 +559,13 @@ template <typename T, int D> void launch_few(const Attn8Args &a, const Attn8Spli
 }
 
 template <typename T, int D, bool LOG2> void launch_join(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
-    int shift = 0;   // a group of lanes per chunk of the row, as far as a workgroup goes
-    while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin) ++shift;
-    const int64_t per = kJoin / (D / 4) >> shift;   // rows per workgroup
     const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
+    // a group of lanes per chunk of the row, as far as a workgroup goes and rows do not
+    // fill the card by themselves
+    const int64_t lanes = (int64_t)a.batch * a.cache.heads * rows * (D / 4);
+    int shift = 0;
+    while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin && lanes << shift < kJoinLanes) ++shift;
+    const int64_t per = kJoin / (D / 4) >> shift;   // rows per workgroup
     const dim3 grid(a.cache.heads, a.batch, (unsigned)((rows + per - 1) / per));
     attn8_join_kernel<T, D, LOG2><<<grid, kJoin, 0, st>>>(a, sp, shift);
 }

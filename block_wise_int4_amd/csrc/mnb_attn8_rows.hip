@@ -49,6 +49,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t *to) {
     to[1] = as_u32(as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) - off);
 }
 
+// (zeros by choice where no key has weight: the sum may be 0 * infinity)
+__device__ __forceinline__ _Float16 result(float sum, float by) { return (_Float16)(by == 0.0f ? 0.0f : sum * by); }
+
 __device__ __forceinline__ float halves_max(float x) {
     const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
     return fmaxf(as_float(r.x), as_float(r.y));
@@ -58,12 +61,13 @@ __device__ __forceinline__ float halves_max(float x) {
 
 template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args &a, const Attn8Split &sp) {
     constexpr int kPieces = D / 16;             // of a row of codes
-    constexpr int kHalf = kKeys * kPieces;      // threads that carry a tile's keys (or values)
     constexpr int kTile = kKeys * D;
-    constexpr int kEach = 2 * kHalf / 256;      // pieces per thread, keys and values
-    __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kTile], s_v[2][kTile];
+    // two tiles of keys and two of values; before and after the loop a quarter for each
+    // wave, through which its rows of q come in and its rows of results go out whole
+    __shared__ __attribute__((aligned(16))) _Float16 s_tiles[4 * kTile];
+    _Float16(*const s_k)[kTile] = reinterpret_cast<_Float16(*)[kTile]>(s_tiles);
+    _Float16(*const s_v)[kTile] = s_k + 2;
     __shared__ __attribute__((aligned(16))) float s_ks[2][kKeys], s_vs[2][kKeys];
-    __shared__ uint32_t s_valid[2], s_most[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int h = blockIdx.x, chunk = blockIdx.z / sp.q_tiles;
@@ -71,14 +75,27 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     const int q_tile = sp.q_tiles - 1 - (blockIdx.z - chunk * sp.q_tiles);
     const int64_t b = blockIdx.y;
     const Cache8 &c = a.cache;
+    const int begin = chunk * sp.chunk;
+    // (no kernel writes the table, the lengths and the starts while this one reads them:
+    // scalar loads)
+    typedef __attribute__((address_space(4))) const int32_t entry;
+    entry *table = (entry *)(a.table + b * a.table_width);
+    int32_t ids[2];      // of the next step's parts
+    auto look_up = [&](int key0) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + s, sp.page_magic);
+            ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
+        }
+    };
+    look_up(begin);
     int64_t first;
-    const int len = a.lens[b], n_new = rows_of(a, b, first);
+    const int len = ((entry *)a.lens)[b], n_new = rows_of(a, b, first);
     const int row0 = q_tile * kRowTile;
     int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group - row0;
     if (rows <= 0) return;
     if (rows > kRowTile) rows = kRowTile;
     const int n = sees(a, len, n_new, token_of(a, row0 + rows - 1));
-    const int begin = chunk * sp.chunk;
     if (begin >= n && chunk > 0) return;
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;
     // this lane's row
@@ -89,20 +106,110 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     // (uniform: keys that all of this wave's rows see)
     const int least = __builtin_amdgcn_readfirstlane(
         sees(a, len, n_new, token_of(a, row0 + (wave * 32 < rows ? wave * 32 : 0))));
+    const float mul = a.scale * kLog2e;
+
+    // Staging. A wave carries 512 codes of one 16-key part a step, 16 a lane: rows of the
+    // keys and the same of the values (D = 128), or of one of them (D = 64); its lanes
+    // 0..15 besides that part's scales, the keys' or the values'. So a wave's block is
+    // uniform, looked up two steps ahead; its codes are requested one step ahead,
+    // through buffers that end with the last key that any row sees.
+    constexpr bool kBoth = D == 128;
+    const int part = kBoth ? wave >> 1 : wave & 1, value = kBoth ? wave & 1 : wave >> 1;   // (value: of the scales)
+    const uint32_t stride = (uint32_t)c.token_stride;
+    const int row = kBoth ? wave * 8 + lane / kPieces : (wave & 1) * 16 + lane / kPieces, piece = lane % kPieces;
+    const uint32_t at_row = (uint32_t)(row & 15) * stride + piece * 16;
+    u32x4 codes[kBoth ? 2 : 1];
+    float scale;
+    uint32_t valid, valid_next;   // bit k: key k of the step has a block, and some row sees it
+    auto fetch = [&](int key0) {
+        int ok[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int left = end - key0 - 16 * s;
+            ok[s] = __builtin_amdgcn_readfirstlane(
+                left < 0 || (uint64_t)(int64_t)ids[s] >= (uint64_t)c.num_blocks ? 0 : left > 16 ? 16 : left);
+        }
+        valid_next = ((1u << ok[0]) - 1) | ((1u << ok[1]) - 1) << 16;
+        const int id = part ? ids[1] : ids[0], mine_ok = part ? ok[1] : ok[0];
+        const uint32_t number = ((uint32_t)key0 >> 4) + part;
+        const uint32_t in_page = (number - blocks_before(number, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
+        const int64_t from = id * c.block_stride + h * c.head_stride + (int64_t)in_page * stride;
+        const uint32_t bytes = mine_ok > 0 ? (uint32_t)(mine_ok - 1) * stride + D : 0u;
+        auto request = [&](const int8_t *base) {
+            return __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base + from), 0, bytes, 0x00020000),
+                           at_row, 0, 0));
+        };
+        if constexpr (kBoth) {
+            codes[0] = request(c.k);
+            codes[1] = request(c.v);
+        } else {
+            codes[0] = request(value ? c.v : c.k);
+        }
+        const float *scales = (value ? c.v_scale : c.k_scale) + id * c.scale_block + h * c.scale_head + in_page;
+        scale = as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scales), 0, mine_ok * 4u, 0x00020000),
+            (lane & 15) * 4, 0, 0));
+    };
+    const int put_at = row * D, lo = ((2 * piece) ^ swizzle<D>(row)) * 8, hi = ((2 * piece + 1) ^ swizzle<D>(row)) * 8;
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int e = 0; e < (kBoth ? 2 : 1); ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) widen(codes[e][k], w + 2 * k);
+            _Float16 *to = ((kBoth ? e == 1 : value == 1) ? s_v[buf] : s_k[buf]) + put_at;
+            *reinterpret_cast<u32x4 *>(to + lo) = u32x4{w[0], w[1], w[2], w[3]};
+            *reinterpret_cast<u32x4 *>(to + hi) = u32x4{w[4], w[5], w[6], w[7]};
+        }
+        if (lane < 16) (value ? s_vs : s_ks)[buf][16 * part + lane] = value ? scale : scale * mul;
+    };
+
+    const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
+    if (steps > 0) {
+        fetch(begin);
+        look_up(begin + kKeys);
+    }
+
+    // Whole rows of a [token][head][D] tensor: lane l of step k carries 16 bytes, piece
+    // l % (D / 8), of the wave's row k * kRowsAtOnce + l / (D / 8). In LDS a row's pieces are
+    // permuted by the row.
+    constexpr int kRowPieces = D / 8, kRowsAtOnce = 64 / kRowPieces, kCarries = 32 / kRowsAtOnce;
+    _Float16 *s_mine = s_tiles + wave * (32 * D);
+    auto in_rows = [&](int row, int piece) { return s_mine + row * D + (piece ^ (row & (kRowPieces - 1))) * 8; };
+    const int carried = lane / kRowPieces, carried_piece = lane % kRowPieces;
+    auto token_head = [&](int row, int64_t &of, int64_t &head) {   // of the wave's row
+        const int at = row0 + wave * 32 + row, t = token_of(a, at);
+        of = first + t;
+        head = (int64_t)h * a.group + at - t * a.group;
+    };
 
     h8 q[D / 16];
     bool finite = true;
     {
-        const _Float16 *src = static_cast<const _Float16 *>(a.q) + (first + token) * a.q_stride +
-                              ((int64_t)h * a.group + r - token * a.group) * D;
+        u32x4 w[kCarries];
+#pragma unroll
+        for (int k = 0; k < kCarries; ++k) {
+            const int row = k * kRowsAtOnce + carried;
+            int64_t of, head;
+            token_head(row, of, head);
+            w[k] = u32x4{0, 0, 0, 0};
+            if (wave * 32 + row < rows)
+                w[k] = *reinterpret_cast<const u32x4 *>(static_cast<const _Float16 *>(a.q) + of * a.q_stride + head * D +
+                                                        carried_piece * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < kCarries; ++k)
+            *reinterpret_cast<u32x4 *>(in_rows(k * kRowsAtOnce + carried, carried_piece)) = w[k];
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            q[j] = *reinterpret_cast<const h8 *>(src + 16 * j + 8 * half);
-            const u32x4 w = __builtin_bit_cast(u32x4, q[j]);
+            q[j] = *reinterpret_cast<const h8 *>(in_rows(col, 2 * j + half));
+            const u32x4 x = __builtin_bit_cast(u32x4, q[j]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = w[e] & 0x7FFFu, hi = w[e] >> 16 & 0x7FFFu;
+                const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
                 top = lo > top ? lo : top;
                 top = hi > top ? hi : top;
             }
@@ -113,70 +220,11 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) q[j] = h8{};
     }
-    const float mul = a.scale * kLog2e;
-
-    // Staging. Thread t carries piece t % kPieces of key t / kPieces (of the keys, then
-    // of the values); wave 0's lanes the scales besides: lane l of key l % 32, its
-    // key's scale or (from 32 on) its value's.
-    const int32_t *table = a.table + b * a.table_width;
-    u32x4 codes[kEach];
-    float scale = 0.0f;
-    bool there = false;
-    auto place = [&](int key, int64_t &id, uint32_t &row) {
-        const uint32_t part = (uint32_t)key >> 4, before = blocks_before(part, sp.page_magic);
-        id = key < end ? table[before] : -1;
-        row = (uint32_t)key - before * (uint32_t)c.page;
-        return (uint64_t)id < (uint64_t)c.num_blocks;
-    };
-    auto fetch = [&](int key0) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int t = tid + 256 * e, value = t >= kHalf, at = value ? t - kHalf : t;
-            int64_t id;
-            uint32_t row;
-            codes[e] = u32x4{0, 0, 0, 0};
-            if (place(key0 + at / kPieces, id, row))
-                codes[e] = *reinterpret_cast<const u32x4 *>((value ? c.v : c.k) + id * c.block_stride +
-                                                            h * c.head_stride + (int64_t)row * c.token_stride +
-                                                            at % kPieces * 16);
-        }
-        if (wave == 0) {
-            int64_t id;
-            uint32_t row;
-            there = place(key0 + col, id, row);
-            scale = 0.0f;
-            if (there) scale = (half ? c.v_scale : c.k_scale)[id * c.scale_block + h * c.scale_head + row];
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int t = tid + 256 * e, value = t >= kHalf, at = value ? t - kHalf : t;
-            const int row = at / kPieces, piece = at % kPieces;
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) widen(codes[e][k], w + 2 * k);
-            _Float16 *to = (value ? s_v[buf] : s_k[buf]) + row * D;
-            *reinterpret_cast<u32x4 *>(to + ((2 * piece) ^ swizzle<D>(row)) * 8) = u32x4{w[0], w[1], w[2], w[3]};
-            *reinterpret_cast<u32x4 *>(to + ((2 * piece + 1) ^ swizzle<D>(row)) * 8) = u32x4{w[4], w[5], w[6], w[7]};
-        }
-        if (wave == 0) {
-            if (half) s_vs[buf][col] = scale;
-            else s_ks[buf][col] = scale * mul;
-            // the largest value scale that is a number
-            uint32_t top = half && as_bits(scale) < 0x7F800000u ? as_bits(scale) : 0u;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t other = (uint32_t)__shfl_xor((int)top, d);
-                top = other > top ? other : top;
-            }
-            const uint64_t valid = __ballot(there);
-            if (lane == 0) {
-                s_valid[buf] = (uint32_t)valid;
-                s_most[buf] = top;
-            }
-        }
-    };
+    __syncthreads();   // (the tiles' place is free)
+    if (steps > 0) {
+        put(0);
+        valid = valid_next;
+    }
 
     f16v o[D / 32];
 #pragma unroll
@@ -185,15 +233,13 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float ref = kLowest, l = 0.0f;
     int unit = 1;   // biased exponent of the value scales' unit
-    const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
-    if (steps > 0) {
-        fetch(begin);
-        put(0);
-    }
     for (int step = 0; step < steps; ++step) {
         const int buf = step & 1, key0 = begin + step * kKeys;
         __syncthreads();
-        if (step + 1 < steps) fetch(key0 + kKeys);
+        if (step + 1 < steps) {
+            fetch(key0 + kKeys);
+            look_up(key0 + 2 * kKeys);
+        }
         f16v s;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = 0.0f;
@@ -209,11 +255,17 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             ks[j] = *reinterpret_cast<const f4 *>(s_ks[buf] + 8 * j + 4 * half);
             vs[j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 8 * j + 4 * half);
         }
-        const uint32_t valid = __builtin_amdgcn_readfirstlane(s_valid[buf]);
-        // (from 2^125 on float16 outputs overflow in any case)
-        const int scale_bits = __builtin_amdgcn_readfirstlane(s_most[buf]) >> 23, most = scale_bits < 252 ? scale_bits : 252;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] *= ks[e / 4][e % 4];
+        // the largest value scale that is a number; from 2^125 on float16 outputs overflow
+        // in any case
+        float scales = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[j][e]);
+        int most = __builtin_amdgcn_readfirstlane((int)as_bits(halves_max(scales))) >> 23;
+        most = most < 252 ? most : 252;
         const bool partial = valid != 0xFFFFFFFFu || key0 + kKeys > least;
         if (partial)   // uniform: the end of a row, or a missing block
 #pragma unroll
@@ -276,32 +328,60 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 }
                 o[d] = mma32(w, __builtin_bit_cast(h8, p[k]), o[d]);
             }
-        if (step + 1 < steps) put(buf ^ 1);
+        if (step + 1 < steps) {
+            put(buf ^ 1);
+            valid = valid_next;
+        }
     }
     const u32x2 ls = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(l), as_bits(l), false, false));
     l = as_float(ls.x) + as_float(ls.y);
-    if (!on) return;
     if (!finite && l != 0.0f) l = __builtin_nanf("");   // (its products were taken with zeros)
     const float back = as_float((uint32_t)(unit + 1) << 23);   // 2^(unit - 126)
+    __syncthreads();   // (the tiles' last reads are over)
     if (n <= sp.chunk) {
+        const float by = l == 0.0f ? 0.0f : back / l;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                store_out<_Float16, D>(a, first, h, r, 32 * d + 2 * e + 4 * half,
-                                       f4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]} * back, l);
-    } else {
-        const int64_t piece = ((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk;
+            for (int e = 0; e < 16; e += 4) {
+                const u32x2 w = {as_u32(h2{result(o[d][e], by), result(o[d][e + 1], by)}),
+                                 as_u32(h2{result(o[d][e + 2], by), result(o[d][e + 3], by)})};
+                *reinterpret_cast<u32x2 *>(in_rows(col, 4 * d + e / 4) + 4 * half) = w;
+            }
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<f4 *>(sp.sums + piece * D + 32 * d + 2 * e + 4 * half) =
-                    f4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]} * back;
-        if (half == 0) {
-            sp.stats[2 * piece] = ref;
-            sp.stats[2 * piece + 1] = l;
+        for (int k = 0; k < kCarries; ++k) {
+            const int row = k * kRowsAtOnce + carried;
+            int64_t of, head;
+            token_head(row, of, head);
+            if (wave * 32 + row < rows)
+                *reinterpret_cast<u32x4 *>(static_cast<_Float16 *>(a.out) +
+                                           (of * ((int64_t)c.heads * a.group) + head) * D + carried_piece * 8) =
+                    *reinterpret_cast<const u32x4 *>(in_rows(row, carried_piece));
         }
+        return;
+    }
+    // a piece: the sums in two halves of D / 2 dimensions, 4 bytes each
+    float *sums = sp.sums + (((b * c.heads + h) * sp.rows + row0 + wave * 32) * sp.chunks + chunk) * D;
+#pragma unroll
+    for (int d0 = 0; d0 < D / 32; d0 += D / 64) {
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
+                    f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
+#pragma unroll
+        for (int k = 0; k < kCarries; ++k) {
+            const int row = k * kRowsAtOnce + carried;
+            if (wave * 32 + row < rows)
+                *reinterpret_cast<f4 *>(sums + (int64_t)row * sp.chunks * D + 32 * d0 + carried_piece * 4) =
+                    *reinterpret_cast<const f4 *>(in_rows(row, carried_piece));
+        }
+    }
+    if (on && half == 0) {
+        float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
+        stats[0] = ref;
+        stats[1] = l;
     }
 }
 
