@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmnb.so")
 SOURCES = ("mnb_api.hip", "mnb_aux.hip", "mnb_gemv.hip", "mnb_gemm.hip", "mnb_embed.hip", "mnb_int8.hip",
            "mnb_attn_api.hip", "mnb_attn.hip", "mnb_cross.hip", "mnb_kv.hip", "mnb_cache8_api.hip", "mnb_kv8.hip",
-           "mnb_rope.hip", "mnb_attn8.hip", "mnb_attn8_rows.hip")
+           "mnb_rope.hip", "mnb_attn8.hip", "mnb_attn8_few.hip",
+           "mnb_attn8_rows.hip")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -75,6 +75,12 @@ struct Attn8Split {
 hipError_t launch_attn8_join(const Attn8Args &a, const Attn8Split &sp, int head_dim, int dtype, bool log2,
                              hipStream_t st);
 
+// The same sums for up to kFewRows query rows of a (request, key-value head)
+// (mnb_attn8_few.hip).
+constexpr int kFewRows = 5;
+hipError_t launch_attn8_few(const Attn8Args &a, const Attn8Split &sp, int head_dim, int dtype, bool stream,
+                            hipStream_t st);
+
 // The same sums for float16 calls with many query rows (mnb_attn8_rows.hip), tiles of
 // kRowTile rows.
 constexpr int kRowTile = 128;

@@ -22,7 +22,7 @@
 // The next tile's key codes are requested as soon as this one's are in registers,
 // its value codes after the second product's reads.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
-#include "mnb_attn8.h"
+#include "mnb_attn8_tiles.h"
 
 namespace mnb {
 
@@ -30,63 +30,15 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kQ = 16;       // query rows per row of tiles
-constexpr int kParts = 4;    // 16-key parts of a tile
-constexpr int kKeys = 16 * kParts;
-
-typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
-
-__device__ __forceinline__ i32x4 mma64(i32x4 a, i32x4 b, i32x4 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-}
-
-// The largest over the four lanes of a column (l % 16).
-__device__ __forceinline__ uint32_t column_max(uint32_t x) {
-    u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(x, x, false, false));
-    x = r.x > r.y ? r.x : r.y;
-    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, x, false, false));
-    return r.x > r.y ? r.x : r.y;
-}
-__device__ __forceinline__ float column_max(float x) {
-    // (elements through functions: a bit cast of a vector's element reads the first)
-    u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
-    x = fmaxf(as_float(r.x), as_float(r.y));
-    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false));
-    return fmaxf(as_float(r.x), as_float(r.y));
-}
-
-__device__ __forceinline__ float weight(float x, float m) { return __builtin_amdgcn_exp2f((x - m) * kLog2e); }
-
-// Where 16-byte piece c of LDS row `row` is: c ^ swizzle(row). The first product's
-// reads (16 rows, one piece) and the transposing ones (8 of 32 rows, one piece)
-// each touch all banks evenly.
-template <int D> __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (D == 128) return ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
-    else return ((row >> 2) & 3) ^ ((row >> 4) & 1) << 1;
-}
-
-// The lower three bytes of four numbers w = n + 0x8080 by their place: signed digits of
-// n, the lower two 128 too much, and less again by the sign bit.
-__device__ __forceinline__ void digits_of(const uint32_t *w, uint32_t *digit) {
-    const uint32_t a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);   // bytes 0, 0, 1, 1
-    const uint32_t a23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
-    const uint32_t b01 = __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0602u);   // bytes 2, 2
-    const uint32_t b23 = __builtin_amdgcn_perm(w[3], w[2], 0x06020C0Cu);
-    digit[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100u) ^ 0x80808080u;
-    digit[1] = __builtin_amdgcn_perm(a23, a01, 0x07060302u) ^ 0x80808080u;
-    digit[2] = b01 | b23;
-}
 
 }  // namespace
 
 template <typename T, int D, bool STREAM>
 __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8Split &sp) {
-    constexpr int kLoads = D / 64;      // of 1 KB per part
-    constexpr int kPieces = D / 16;     // of a row of codes
-    constexpr int kTile = kKeys * D;    // bytes
+    using Tile = CodeTile<D, STREAM>;
+    constexpr int kLoads = Tile::kLoads, kTile = Tile::kBytes;
     constexpr int kOut = D / 16;        // 16-dimension parts of the output
-    constexpr int kBehind = kParts + kParts * kLoads;   // loads of a tile's scales and codes, keys or values
+    constexpr int kBehind = kParts + Tile::kCodeLoads;   // loads of a tile's scales and codes, keys or values
     // the waves' tiles of key and value codes (arrays of their own: the compiler then
     // knows that reads of one need not wait for loads into the other); in the end their
     // sums [kWaves][kQ][D], and maxima and weights' sums [kWaves][kQ]
@@ -113,182 +65,23 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     const int r = row0 + (col < rows ? col : 0), token = token_of(a, r);
     const int mine = sees(a, len, n_new, token);
 
-    // Lanes l look after part l % 4 of the next tile: its table entry (past the table's
-    // end the last one, which is not used) is requested a step ahead.
-    const int my_part = lane & (kParts - 1);
-    const int32_t *table = a.table + b * a.table_width;
-    auto entry_of = [&](int key0) {
-        const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + my_part, sp.page_magic);
-        return table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
-    };
-    int32_t id = entry_of(key + step);
-
-    // queries: lane (query col, pieces 4 j + g of 16 dimensions), in digits
+    Tile tile(a, sp, b, lane, end, s_keys[wave], s_values[wave]);
+    tile.look_up(key + step);
+    // queries, in digits: lane (query col, pieces 4 j + g)
     i32x4 q[kLoads][3];
-    float mul;   // of a sum of digit products, to a score without the key's scale
-    {
-        const T *src = static_cast<const T *>(a.q) + (first + token) * a.q_stride +
-                       ((int64_t)h * a.group + r - token * a.group) * D + g * 16;
-        float x[kLoads][16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-            for (int p = 0; p < (int)sizeof(T); ++p) {
-                const u32x4 w = reinterpret_cast<const u32x4 *>(src + 64 * j)[p];
-#pragma unroll
-                for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
-                    float v;
-                    if constexpr (sizeof(T) == 2) v = (float)__builtin_bit_cast(h8, w)[i];
-                    else v = __builtin_bit_cast(f4, w)[i];
-                    x[j][p * (16 / (int)sizeof(T)) + i] = v;
-                    // (as whole numbers: infinities and NaN are above every finite one)
-                    const uint32_t bits = as_bits(v) & 0x7FFFFFFFu;
-                    top = bits > top ? bits : top;
-                }
-            }
-        top = column_max(top);
-        const bool finite = top < 0x7F800000u;
-        // 2^(e - 127) <= largest < 2^(e - 126), the smallest ones 2^64 times as large
-        const bool small = top < (64u << 23);
-        const float lift = small ? 0x1p64f : 1.0f;
-        if (small) top = as_bits(as_float(top) * 0x1p64f);
-        const int e = top ? (int)(top >> 23) : 127;
-        const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
-        mul = finite ? __builtin_ldexpf(a.scale, e - 127 - 21 - (small ? 64 : 0)) : __builtin_nanf("");
-        // whole numbers n, |n| < 2^22 (one that would round to 2^22 stays one below), as
-        // the bits of 2^23 + 2^22 + n less those of n = 0
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t w[4], digit[3];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = finite ? x[j][4 * k + i] * lift * up : 0.0f;
-                    w[i] = as_bits(__builtin_amdgcn_fmed3f(v, -4194303.0f, 4194303.0f) + 12582912.0f) +
-                           (0x8080u - 0x4B400000u);
-                }
-                digits_of(w, digit);
-                q[j][0][k] = (int)digit[0];
-                q[j][1][k] = (int)digit[1];
-                q[j][2][k] = (int)digit[2];
-            }
-    }
+    float mul;
+    query_digits<T, D>(static_cast<const T *>(a.q) + (first + token) * a.q_stride +
+                           ((int64_t)h * a.group + r - token * a.group) * D + g * 16,
+                       a.scale, q, mul);
+    asm volatile("" : "+v"(tile.id));   // (the entries are there: no wait for them in the loop's first turn)
 
-    asm volatile("" : "+v"(id));   // (the entry is there: no wait for it in the loop's first turn)
-
-    // Where the next tile is: bytes to its parts' codes and scales (of keys and of values
-    // alike), and how many codes there are: a part past the last key, or without a
-    // block, is read through a buffer of no bytes. (Rows of a page past the last key are
-    // read, and weigh nothing.) Worked out by the parts' lanes, read from there where a
-    // load needs it: in scalar registers it takes 400 instructions a tile, and more
-    // registers than there are.
-    const uint32_t stride = (uint32_t)c.token_stride, part_bytes = 15 * stride + D;
-    uint64_t from = 0, from_scales = 0;
-    uint32_t bytes = 0;
-    uint32_t there = 0, there_next = 0;   // a bit for each part
-    auto locate = [&](int key0) {
-        const uint32_t part = ((uint32_t)key0 >> 4) + my_part;
-        const uint32_t row = (part - blocks_before(part, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
-        const bool ok = (uint32_t)id < (uint32_t)c.num_blocks && key0 + 16 * my_part < end;
-        const uint64_t block = ok ? (uint32_t)id : 0u;
-        bytes = ok ? part_bytes : 0u;
-        from = block * (uint64_t)c.block_stride + (uint64_t)row * stride;
-        from_scales = (block * (uint64_t)c.scale_block + row) * 4;
-        there_next = (uint32_t)__ballot(ok) & ((1u << kParts) - 1);
-    };
-    auto of_part = [&](uint32_t x, int s) { return (uint32_t)__builtin_amdgcn_readlane((int)x, s); };
-    auto buffer = [&](const void *base, uint64_t at, int s, uint32_t most) {
-        const uint64_t there = (uint64_t)of_part((uint32_t)(at >> 32), s) << 32 | of_part((uint32_t)at, s);
-        const uint32_t n = of_part(bytes, s);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + there, 0,
-                                                 n < most ? n : most, 0x00020000);
-    };
     const int8_t *keys = c.k + h * c.head_stride, *values = c.v + h * c.head_stride;
     const float *key_scales = c.k_scale + h * c.scale_head, *value_scales = c.v_scale + h * c.scale_head;
-    // A load to LDS takes whole rows, 64 lanes on 1 KB after another.
-    constexpr int kRows = 64 / kPieces;   // of a load
-    uint8_t *s_k = s_keys[wave], *s_v = s_values[wave];
-    uint32_t at[2][kLoads];               // for even and odd parts
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd)
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int row = j * kRows + lane / kPieces;
-            at[odd][j] = (uint32_t)row * stride + ((lane % kPieces) ^ swizzle<D>(16 * odd + row)) * 16;
-        }
-    auto load_codes = [&](const int8_t *base, uint8_t *to) {
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-            const auto rows_in = buffer(base, from, s, ~0u);
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_in, (lds_void *)(to + (s * kLoads + j) * 1024), 16,
-                                                         at[s & 1][j], 0, 0, STREAM ? 2 : 0);
-        }
-    };
     auto load_scales = [&](const float *base, f4 *to) {
 #pragma unroll
         for (int s = 0; s < kParts; ++s)
             to[s] = __builtin_bit_cast(
-                f4, __builtin_amdgcn_raw_buffer_load_b128(buffer(base, from_scales, s, 64u), g * 16, 0, 0));
-    };
-    // Keys: lane (key col, g) takes piece 4 j + g of its row in each part. (With its waits:
-    // the compiler waits for the values' loads as well, which come after.)
-    uint32_t k_at[2][kLoads];
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd)
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int row = 16 * odd + col;
-            k_at[odd][j] = (uint32_t)(size_t)(lds_void *)s_k + row * D + ((4 * j + g) ^ swizzle<D>(row)) * 16;
-        }
-    auto read_keys = [&](i32x4 (*k)[kLoads]) {
-        if constexpr (kLoads == 2)
-            asm volatile(
-                "s_waitcnt vmcnt(%13)\n\t"
-                "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
-                "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\t"
-                "ds_read_b128 %6, %10 offset:%12\n\tds_read_b128 %7, %11 offset:%12\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(k[0][0]), "=&v"(k[0][kLoads - 1]), "=&v"(k[1][0]), "=&v"(k[1][kLoads - 1]), "=&v"(k[2][0]),
-                  "=&v"(k[2][kLoads - 1]), "=&v"(k[3][0]), "=&v"(k[3][kLoads - 1])
-                : "v"(k_at[0][0]), "v"(k_at[0][kLoads - 1]), "v"(k_at[1][0]), "v"(k_at[1][kLoads - 1]), "n"(32 * D),
-                  "n"(kBehind)
-                : "memory");
-        else
-            asm volatile(
-                "s_waitcnt vmcnt(%7)\n\t"
-                "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
-                "ds_read_b128 %2, %4 offset:%6\n\tds_read_b128 %3, %5 offset:%6\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(k[0][0]), "=&v"(k[1][0]), "=&v"(k[2][0]), "=&v"(k[3][0])
-                : "v"(k_at[0][0]), "v"(k_at[1][0]), "n"(32 * D), "n"(kBehind)
-                : "memory");
-    };
-
-    // Values, turned: 16 lanes read eight keys by 16 dimensions. Lane L supplies key
-    // L / 2, eight dimensions 8 (L % 2) on, and receives dimension L of the eight keys
-    // 16 (2 u + j / 4) + 4 g + j % 4. Four parts of 16 dimensions at a time, and their
-    // wait with them: through the builtin the compiler waits for all loads first, the
-    // next keys' among them.
-    const int v_row = 16 * (col >> 3) + 4 * g + ((col >> 1) & 3);   // (u = 0; u = 1 is 32 rows on)
-    const uint32_t v_at = (uint32_t)(size_t)(lds_void *)s_v + v_row * D + (col & 1) * 8;
-    auto read_values = [&](i32x2 (*v)[2], int d) {
-        uint32_t at[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) at[e] = v_at + ((d + e) ^ swizzle<D>(v_row)) * 16;
-        asm volatile(
-            "ds_read_b64_tr_b8 %0, %8\n\tds_read_b64_tr_b8 %1, %8 offset:%12\n\t"
-            "ds_read_b64_tr_b8 %2, %9\n\tds_read_b64_tr_b8 %3, %9 offset:%12\n\t"
-            "ds_read_b64_tr_b8 %4, %10\n\tds_read_b64_tr_b8 %5, %10 offset:%12\n\t"
-            "ds_read_b64_tr_b8 %6, %11\n\tds_read_b64_tr_b8 %7, %11 offset:%12\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
-              "=&v"(v[3][0]), "=&v"(v[3][1])
-            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(32 * D)
-            : "memory");
+                f4, __builtin_amdgcn_raw_buffer_load_b128(tile.buffer(base, tile.from_scales, s, 64u), g * 16, 0, 0));
     };
 
     f4 o[kOut];
@@ -304,7 +97,7 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
         if (real) {
             // (this tile's key codes are in LDS when all but its values' loads have come back)
             i32x4 kk[kParts][kLoads];
-            read_keys(kk);
+            tile.template read_keys<kBehind>(kk);
 #pragma unroll
             for (int s = 0; s < kParts; ++s) {
                 i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
@@ -322,10 +115,11 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                 for (int i = 0; i < 4; ++i) x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * by[i];
             }
         }
-        locate(key + step);
+        const uint32_t there = tile.there;
+        tile.locate(key + step);
         load_scales(key_scales, ks);
-        load_codes(keys, s_k);
-        id = entry_of(key + 2 * step);
+        tile.load_codes(keys, s_keys[wave]);
+        tile.look_up(key + 2 * step);
         asm volatile("" ::: "memory");   // (in this order: the waits count them)
         if (real) {
             if (key + kKeys > least || there != (1u << kParts) - 1)   // uniform: the end of a row, or a missing block
@@ -365,29 +159,24 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                     most = bits > most ? bits : most;
                 }
             most = column_max(most);
-            // numbers below 2^22: times 2^(21 - exponent), a touch less so that none rounds
-            // up to it
-            const bool finite = most < 0x7F800000u;
-            int e = (int)(most >> 23);
-            e = e < 24 ? 24 : e;
-            const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23) * (1.0f - 0x1p-21f);
-            const float down = finite ? as_float((uint32_t)(e - 21) << 23) * (1.0f + 0x1p-21f) : __builtin_nanf("");
+            float up, down;
+            weight_steps(most, up, down);
             i32x4 p[3];
 #pragma unroll
             for (int s = 0; s < kParts; ++s) {
                 uint32_t w[4], digit[3];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = as_bits(__builtin_fmaf(x[s][i], up, 8388608.0f + 32896.0f));
+                for (int i = 0; i < 4; ++i) w[i] = as_bits(__builtin_fmaf(x[s][i], up, kDigits));
                 digits_of(w, digit);
 #pragma unroll
                 for (int t = 0; t < 3; ++t) p[t][s] = (int)digit[t];
             }
             // this tile's value codes are in LDS: all but the next keys' loads, and the entry's
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBehind + 1) : "memory");
+            wait_loads<kBehind + 1>();
 #pragma unroll
             for (int d = 0; d < kOut; d += 4) {
                 i32x2 v[4][2];
-                read_values(v, d);
+                tile.template read_values<false>(v, d);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const i32x4 zero = {0, 0, 0, 0}, vv = {v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y};
@@ -400,14 +189,13 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
             }
         }
         load_scales(value_scales, vs);
-        load_codes(values, s_v);
+        tile.load_codes(values, s_values[wave]);
         asm volatile("" ::: "memory");
-        there = there_next;
         key += step;
     } while (key < end);
 
     // (the tile past the end, no bytes, has arrived everywhere: its place is free)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait_loads<0>();
     __syncthreads();
 
     // join the waves (those that have keys)
@@ -550,11 +338,9 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64
     return p;
 }
 
-template <typename T, int D> void launch_few(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
+template <typename T, int D> void launch_some(const Attn8Args &a, const Attn8Split &sp, bool stream, hipStream_t st) {
     const dim3 grid(a.cache.heads, a.batch, (unsigned)(sp.q_tiles * sp.chunks));
-    // Codes that the L2 (32 MB in all) cannot hold are read past it.
-    const double bytes = 2.0 * a.batch * a.cache.heads * a.max_len * D;
-    if (sp.q_tiles == 1 && bytes > 32e6) attn8_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, sp);
+    if (stream) attn8_kernel<T, D, true><<<grid, 64 * kWaves, 0, st>>>(a, sp);
     else attn8_kernel<T, D, false><<<grid, 64 * kWaves, 0, st>>>(a, sp);
 }
 
@@ -578,7 +364,13 @@ template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Sp
             return hipGetLastError();
         }
     }
-    launch_few<T, D>(a, sp, st);
+    // Codes that the L2 (32 MB in all) cannot hold are read past it.
+    const bool stream = sp.q_tiles == 1 && 2.0 * a.batch * a.cache.heads * a.max_len * D > 32e6;
+    if (sp.rows <= kFewRows) {
+        if (hipError_t e = launch_attn8_few(a, sp, D, sizeof(T) == 2 ? 1 : 0, stream, st)) return e;
+    } else {
+        launch_some<T, D>(a, sp, stream, st);
+    }
     if (sp.chunks > 1) launch_join<T, D, false>(a, sp, st);
     return hipGetLastError();
 }
