@@ -38,9 +38,13 @@ __device__ __forceinline__ uint32_t blocks_before(uint32_t part, uint32_t magic)
     return magic ? place : part;
 }
 
-// Token and query head of row r of a (request, key-value head).
+// Token of row r (< 2^24) of a (request, key-value head): r / group, by a reciprocal
+// that is off by at most one.
 __device__ __forceinline__ int token_of(const Attn8Args &a, int r) {
-    return a.max_new == 1 ? 0 : (int)((uint32_t)r / (uint32_t)a.group);
+    int t = (int)((float)r * a.per_group);
+    const int rest = r - t * a.group;
+    t += rest >= a.group ? 1 : 0;
+    return rest < 0 ? t - 1 : t;
 }
 
 // Four outputs from dimension d on of row r.

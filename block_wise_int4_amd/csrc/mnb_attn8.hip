@@ -409,6 +409,7 @@ hipError_t launch_attn8(const Attn8Args &a, int head_dim, int dtype, void *works
         sp.stats = sp.sums + (int64_t)a.batch * a.cache.heads * p.rows * p.chunks * head_dim;
     }
     Attn8Args c = a;
+    c.per_group = 1.0f / (float)a.group;
     // (no key past the table's width is seen)
     if (c.max_len > (int64_t)a.table_width * a.cache.page) c.max_len = a.table_width * a.cache.page;
     if (dtype == 1)

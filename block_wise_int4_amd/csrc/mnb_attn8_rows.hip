@@ -49,9 +49,6 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t *to) {
     to[1] = as_u32(as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) - off);
 }
 
-// (zeros by choice where no key has weight: the sum may be 0 * infinity)
-__device__ __forceinline__ _Float16 result(float sum, float by) { return (_Float16)(by == 0.0f ? 0.0f : sum * by); }
-
 __device__ __forceinline__ float halves_max(float x) {
     const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
     return fmaxf(as_float(r.x), as_float(r.y));
@@ -120,7 +117,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     const uint32_t at_row = (uint32_t)(row & 15) * stride + piece * 16;
     u32x4 codes[kBoth ? 2 : 1];
     float scale;
-    uint32_t valid, valid_next;   // bit k: key k of the step has a block, and some row sees it
+    uint32_t valid, valid_next = 0;   // bit k: key k of the step has a block, and some row sees it
     auto fetch = [&](int key0) {
         int ok[2];
 #pragma unroll
@@ -166,15 +163,10 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         if (lane < 16) (value ? s_vs : s_ks)[buf][16 * part + lane] = value ? scale : scale * mul;
     };
 
-    const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
-    if (steps > 0) {
-        fetch(begin);
-        look_up(begin + kKeys);
-    }
-
-    // Whole rows of a [token][head][D] tensor: lane l of step k carries 16 bytes, piece
-    // l % (D / 8), of the wave's row k * kRowsAtOnce + l / (D / 8). In LDS a row's pieces are
-    // permuted by the row.
+    // Whole rows of a [token][head][D] tensor: lane l of step k carries 16 bytes of the
+    // wave's row k * kRowsAtOnce + l / (D / 8); where it is in memory, and in LDS, where a
+    // row's 16-byte pieces are permuted by the row. (Loops over k stay loops: the code is
+    // run once a launch, out of a cold instruction cache.)
     constexpr int kRowPieces = D / 8, kRowsAtOnce = 64 / kRowPieces, kCarries = 32 / kRowsAtOnce;
     _Float16 *s_mine = s_tiles + wave * (32 * D);
     auto in_rows = [&](int row, int piece) { return s_mine + row * D + (piece ^ (row & (kRowPieces - 1))) * 8; };
@@ -184,48 +176,21 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         of = first + t;
         head = (int64_t)h * a.group + at - t * a.group;
     };
+    typedef __attribute__((address_space(3))) void lds_void;
+    typedef __attribute__((address_space(1))) void global_void;
+#pragma unroll 1
+    for (int k = 0; k < kCarries; ++k) {
+        // (rows behind the last stand for it)
+        const int row = k * kRowsAtOnce + carried, last = rows - 1 - wave * 32;
+        int64_t of, head;
+        token_head(row < last ? row : last, of, head);
+        const _Float16 *from = static_cast<const _Float16 *>(a.q) + of * a.q_stride + head * D +
+                               (carried_piece ^ (row & (kRowPieces - 1))) * 8;
+        __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)(s_mine + k * 512), 16, 0, 0);
+    }
 
     h8 q[D / 16];
     bool finite = true;
-    {
-        u32x4 w[kCarries];
-#pragma unroll
-        for (int k = 0; k < kCarries; ++k) {
-            const int row = k * kRowsAtOnce + carried;
-            int64_t of, head;
-            token_head(row, of, head);
-            w[k] = u32x4{0, 0, 0, 0};
-            if (wave * 32 + row < rows)
-                w[k] = *reinterpret_cast<const u32x4 *>(static_cast<const _Float16 *>(a.q) + of * a.q_stride + head * D +
-                                                        carried_piece * 8);
-        }
-#pragma unroll
-        for (int k = 0; k < kCarries; ++k)
-            *reinterpret_cast<u32x4 *>(in_rows(k * kRowsAtOnce + carried, carried_piece)) = w[k];
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            q[j] = *reinterpret_cast<const h8 *>(in_rows(col, 2 * j + half));
-            const u32x4 x = __builtin_bit_cast(u32x4, q[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
-                top = lo > top ? lo : top;
-                top = hi > top ? hi : top;
-            }
-        }
-        const u32x2 both = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(top, top, false, false));
-        finite = both.x < 0x7C00u && both.y < 0x7C00u;
-        if (!finite)
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) q[j] = h8{};
-    }
-    __syncthreads();   // (the tiles' place is free)
-    if (steps > 0) {
-        put(0);
-        valid = valid_next;
-    }
-
     f16v o[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -233,10 +198,37 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float ref = kLowest, l = 0.0f;
     int unit = 1;   // biased exponent of the value scales' unit
-    for (int step = 0; step < steps; ++step) {
-        const int buf = step & 1, key0 = begin + step * kKeys;
+    int buf = 0;
+    const bool any = begin < end;
+    if (any) {
+        fetch(begin);
+        look_up(begin + kKeys);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the compiler does not count loads to LDS)
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        q[j] = *reinterpret_cast<const h8 *>(in_rows(col, 2 * j + half));
+        const u32x4 x = __builtin_bit_cast(u32x4, q[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
+            top = lo > top ? lo : top;
+            top = hi > top ? hi : top;
+        }
+    }
+    const u32x2 both = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(top, top, false, false));
+    finite = both.x < 0x7C00u && both.y < 0x7C00u;
+    if (!finite)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) q[j] = h8{};
+    __syncthreads();   // (the tiles' place is free)
+    if (any) put(0);
+    valid = valid_next;
+    for (int key0 = begin; key0 < end; key0 += kKeys) {
         __syncthreads();
-        if (step + 1 < steps) {
+        const bool more = key0 + kKeys < end;
+        if (more) {
             fetch(key0 + kKeys);
             look_up(key0 + 2 * kKeys);
         }
@@ -266,32 +258,27 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[j][e]);
         int most = __builtin_amdgcn_readfirstlane((int)as_bits(halves_max(scales))) >> 23;
         most = most < 252 ? most : 252;
-        const bool partial = valid != 0xFFFFFFFFu || key0 + kKeys > least;
-        if (partial)   // uniform: the end of a row, or a missing block
+        if (valid != 0xFFFFFFFFu || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
+            const int left = mine - key0;
+            uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
+            bits = (bits & valid) >> (4 * half);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int at = e % 4 + 8 * (e / 4) + 4 * half;
-                const bool seen = (valid >> at & 1) && key0 + at < mine;
-                s[e] = seen ? s[e] : -__builtin_inff();
-                vs[e / 4][e % 4] = seen ? vs[e / 4][e % 4] : 0.0f;
+                const uint32_t seen = (uint32_t)((int)(bits << (31 - e % 4 - 8 * (e / 4))) >> 31);
+                s[e] = as_float((as_bits(s[e]) & seen) | (0xFF800000u & ~seen));
+                vs[e / 4][e % 4] = as_float(as_bits(vs[e / 4][e % 4]) & seen);
             }
+        }
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
-        if (__any(top > ref + kSlack)) {
-            float to = fmaxf(ref, top - kLift);
-            to = halves_max(to);
-            const float keep = __builtin_amdgcn_exp2f(ref - to);
+        if (__any(top > ref + kSlack) || most > unit) {
+            const float to = halves_max(fmaxf(ref, top - kLift));
+            const int raised = most > unit ? most : unit, less = unit - raised + 127;
+            const float keep = __builtin_amdgcn_exp2f(ref - to) * as_float((uint32_t)(less > 0 ? less : 0) << 23);
+            l *= __builtin_amdgcn_exp2f(ref - to);
             ref = to;
-            l *= keep;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[d][e] *= keep;
-        }
-        if (most > unit) {   // uniform: a larger value scale than any before
-            const float keep = as_float((uint32_t)(unit - most + 127 > 0 ? unit - most + 127 : 0) << 23);
-            unit = most;
+            unit = raised;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -328,10 +315,9 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 }
                 o[d] = mma32(w, __builtin_bit_cast(h8, p[k]), o[d]);
             }
-        if (step + 1 < steps) {
-            put(buf ^ 1);
-            valid = valid_next;
-        }
+        buf ^= 1;
+        if (more) put(buf);
+        valid = valid_next;
     }
     const u32x2 ls = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(l), as_bits(l), false, false));
     l = as_float(ls.x) + as_float(ls.y);
@@ -339,16 +325,16 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     const float back = as_float((uint32_t)(unit + 1) << 23);   // 2^(unit - 126)
     __syncthreads();   // (the tiles' last reads are over)
     if (n <= sp.chunk) {
-        const float by = l == 0.0f ? 0.0f : back / l;
+        const float by = l == 0.0f ? 0.0f : back / l;   // (sums are zeros where no key has weight)
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-                const u32x2 w = {as_u32(h2{result(o[d][e], by), result(o[d][e + 1], by)}),
-                                 as_u32(h2{result(o[d][e + 2], by), result(o[d][e + 3], by)})};
+                const u32x2 w = {as_u32(h2{(_Float16)(o[d][e] * by), (_Float16)(o[d][e + 1] * by)}),
+                                 as_u32(h2{(_Float16)(o[d][e + 2] * by), (_Float16)(o[d][e + 3] * by)})};
                 *reinterpret_cast<u32x2 *>(in_rows(col, 4 * d + e / 4) + 4 * half) = w;
             }
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
             int64_t of, head;
@@ -370,7 +356,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
                     f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
             if (wave * 32 + row < rows)

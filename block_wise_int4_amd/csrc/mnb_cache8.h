@@ -49,6 +49,7 @@ struct Attn8Args {
     int64_t q_stride, tokens;
     int32_t batch, group, max_new, max_len, table_width;
     float scale;
+    float per_group;   // (1 / group; set by the launcher)
 };
 // Float32 partial results the launch needs (0: it splits nothing).
 int64_t attn8_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len,
