@@ -29,6 +29,8 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
+template <int N> struct Number { static constexpr int value = N; };
+
 __device__ __forceinline__ f16v mma32(h8 a, h8 b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
@@ -108,17 +110,18 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     // Staging. A wave carries 512 codes of one 16-key part a step, 16 a lane: rows of the
     // keys and the same of the values (D = 128), or of one of them (D = 64); its lanes
     // 0..15 besides that part's scales, the keys' or the values'. So a wave's block is
-    // uniform, looked up two steps ahead; its codes are requested one step ahead,
+    // uniform, looked up three steps ahead; its codes are requested two steps ahead,
     // through buffers that end with the last key that any row sees.
     constexpr bool kBoth = D == 128;
     const int part = kBoth ? wave >> 1 : wave & 1, value = kBoth ? wave & 1 : wave >> 1;   // (value: of the scales)
     const uint32_t stride = (uint32_t)c.token_stride;
     const int row = kBoth ? wave * 8 + lane / kPieces : (wave & 1) * 16 + lane / kPieces, piece = lane % kPieces;
     const uint32_t at_row = (uint32_t)(row & 15) * stride + piece * 16;
-    u32x4 codes[kBoth ? 2 : 1];
-    float scale;
-    uint32_t valid, valid_next = 0;   // bit k: key k of the step has a block, and some row sees it
-    auto fetch = [&](int key0) {
+    u32x4 codes[2][kBoth ? 2 : 1];   // of even and odd steps
+    float scale[2];
+    uint32_t valid[2];   // bit k: key k of the step has a block, and some row sees it
+    auto fetch = [&](auto parity, int key0) {
+        constexpr int buf = decltype(parity)::value;
         int ok[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -126,7 +129,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             ok[s] = __builtin_amdgcn_readfirstlane(
                 left < 0 || (uint64_t)(int64_t)ids[s] >= (uint64_t)c.num_blocks ? 0 : left > 16 ? 16 : left);
         }
-        valid_next = ((1u << ok[0]) - 1) | ((1u << ok[1]) - 1) << 16;
+        valid[buf] = ((1u << ok[0]) - 1) | ((1u << ok[1]) - 1) << 16;
         const int id = part ? ids[1] : ids[0], mine_ok = part ? ok[1] : ok[0];
         const uint32_t number = ((uint32_t)key0 >> 4) + part;
         const uint32_t in_page = (number - blocks_before(number, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
@@ -139,28 +142,29 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                            at_row, 0, 0));
         };
         if constexpr (kBoth) {
-            codes[0] = request(c.k);
-            codes[1] = request(c.v);
+            codes[buf][0] = request(c.k);
+            codes[buf][1] = request(c.v);
         } else {
-            codes[0] = request(value ? c.v : c.k);
+            codes[buf][0] = request(value ? c.v : c.k);
         }
         const float *scales = (value ? c.v_scale : c.k_scale) + id * c.scale_block + h * c.scale_head + in_page;
-        scale = as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        scale[buf] = as_float(__builtin_amdgcn_raw_buffer_load_b32(
             __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scales), 0, mine_ok * 4u, 0x00020000),
             (lane & 15) * 4, 0, 0));
     };
     const int put_at = row * D, lo = ((2 * piece) ^ swizzle<D>(row)) * 8, hi = ((2 * piece + 1) ^ swizzle<D>(row)) * 8;
-    auto put = [&](int buf) {
+    auto put = [&](auto parity) {
+        constexpr int buf = decltype(parity)::value;
 #pragma unroll
         for (int e = 0; e < (kBoth ? 2 : 1); ++e) {
             uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) widen(codes[e][k], w + 2 * k);
+            for (int k = 0; k < 4; ++k) widen(codes[buf][e][k], w + 2 * k);
             _Float16 *to = ((kBoth ? e == 1 : value == 1) ? s_v[buf] : s_k[buf]) + put_at;
             *reinterpret_cast<u32x4 *>(to + lo) = u32x4{w[0], w[1], w[2], w[3]};
             *reinterpret_cast<u32x4 *>(to + hi) = u32x4{w[4], w[5], w[6], w[7]};
         }
-        if (lane < 16) (value ? s_vs : s_ks)[buf][16 * part + lane] = value ? scale : scale * mul;
+        if (lane < 16) (value ? s_vs : s_ks)[buf][16 * part + lane] = value ? scale[buf] : scale[buf] * mul;
     };
 
     // Whole rows of a [token][head][D] tensor: lane l of step k carries 16 bytes of the
@@ -196,14 +200,13 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
-    float ref = kLowest, l = 0.0f;
-    int unit = 1;   // biased exponent of the value scales' unit
-    int buf = 0;
-    const bool any = begin < end;
-    if (any) {
-        fetch(begin);
-        look_up(begin + kKeys);
-    }
+    // The reference of this lane's row (once a key is seen), the sum of weights
+    // exp2(score - ref), of this lane's keys; biased exponent of the value scales' unit.
+    float ref = 0.0f, l = 0.0f;
+    bool started = false;
+    int unit = 1;
+    fetch(Number<0>{}, begin);
+    look_up(begin + kKeys);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the compiler does not count loads to LDS)
     uint32_t top = 0;
 #pragma unroll
@@ -222,16 +225,17 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     if (!finite)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) q[j] = h8{};
+    fetch(Number<1>{}, begin + kKeys);
+    look_up(begin + 2 * kKeys);
     __syncthreads();   // (the tiles' place is free)
-    if (any) put(0);
-    valid = valid_next;
-    for (int key0 = begin; key0 < end; key0 += kKeys) {
+    put(Number<0>{});
+    auto take = [&](auto parity, int key0) __attribute__((always_inline)) {
+        constexpr int buf = decltype(parity)::value;
         __syncthreads();
-        const bool more = key0 + kKeys < end;
-        if (more) {
-            fetch(key0 + kKeys);
-            look_up(key0 + 2 * kKeys);
-        }
+        const uint32_t seen_keys = valid[buf];
+        // (past the last key: no bytes)
+        fetch(parity, key0 + 2 * kKeys);
+        look_up(key0 + 3 * kKeys);
         f16v s;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = 0.0f;
@@ -247,8 +251,6 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             ks[j] = *reinterpret_cast<const f4 *>(s_ks[buf] + 8 * j + 4 * half);
             vs[j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 8 * j + 4 * half);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] *= ks[e / 4][e % 4];
         // the largest value scale that is a number; from 2^125 on float16 outputs overflow
         // in any case
         float scales = 0.0f;
@@ -258,10 +260,15 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[j][e]);
         int most = __builtin_amdgcn_readfirstlane((int)as_bits(halves_max(scales))) >> 23;
         most = most < 252 ? most : 252;
-        if (valid != 0xFFFFFFFFu || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
+        // scores less the reference, plus the unit's power of two: its inverse, 2^(126 -
+        // unit), then comes with the weights and leaves value scales below one
+        float shift = (float)(126 - unit);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], ks[e / 4][e % 4], shift - ref);
+        if (seen_keys != 0xFFFFFFFFu || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
             const int left = mine - key0;
             uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
-            bits = (bits & valid) >> (4 * half);
+            bits = (bits & seen_keys) >> (4 * half);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const uint32_t seen = (uint32_t)((int)(bits << (31 - e % 4 - 8 * (e / 4))) >> 31);
@@ -272,28 +279,38 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
-        if (__any(top > ref + kSlack) || most > unit) {
-            const float to = halves_max(fmaxf(ref, top - kLift));
+        if (__any(top > (started ? shift + kSlack : -__builtin_inff())) || most > unit) {
+            top = halves_max(top);
+            const bool some = top > -__builtin_inff();
+            float by = top - shift - kLift;   // how far the reference moves
+            by = started ? fmaxf(by, 0.0f) : some ? by : 0.0f;
             const int raised = most > unit ? most : unit, less = unit - raised + 127;
-            const float keep = __builtin_amdgcn_exp2f(ref - to) * as_float((uint32_t)(less > 0 ? less : 0) << 23);
-            l *= __builtin_amdgcn_exp2f(ref - to);
-            ref = to;
-            unit = raised;
+            const float keep = started ? __builtin_amdgcn_exp2f(-by) : 1.0f;   // (nothing to keep at the start)
+            const float keep_sums = keep * as_float((uint32_t)(less > 0 ? less : 0) << 23);
+            l *= keep;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[d][e] *= keep;
+                for (int e = 0; e < 16; ++e) o[d][e] *= keep_sums;
+            started |= some;
+            ref += by;
+            by += (float)(raised - unit);
+            unit = raised;
+            shift = (float)(126 - unit);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] -= by;
         }
-        const float by = as_float((uint32_t)(253 - unit) << 23);   // 2^(126 - unit): value scales below one
         u32x4 p[2];
+        float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-            const float w0 = __builtin_amdgcn_exp2f(s[e] - ref), w1 = __builtin_amdgcn_exp2f(s[e + 1] - ref);
-            l += w0;
-            l += w1;
-            const h2 w = {(_Float16)(w0 * (vs[e / 4][e % 4] * by)), (_Float16)(w1 * (vs[e / 4][e % 4 + 1] * by))};
+            const float w0 = __builtin_amdgcn_exp2f(s[e]), w1 = __builtin_amdgcn_exp2f(s[e + 1]);
+            sum += w0;
+            sum += w1;
+            const h2 w = {(_Float16)(w0 * vs[e / 4][e % 4]), (_Float16)(w1 * vs[e / 4][e % 4 + 1])};
             p[e / 8][e % 8 / 2] = as_u32(w);
         }
+        l = __builtin_fmaf(sum, as_float((uint32_t)(unit + 1) << 23), l);   // 2^(unit - 126)
         // p[k] element j of lane half h is key 16 k + 8 (j / 4) + 4 h + j % 4
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
@@ -315,9 +332,11 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 }
                 o[d] = mma32(w, __builtin_bit_cast(h8, p[k]), o[d]);
             }
-        buf ^= 1;
-        if (more) put(buf);
-        valid = valid_next;
+        put(Number<buf ^ 1>{});
+    };
+    for (int key0 = begin; key0 < end; key0 += 2 * kKeys) {
+        take(Number<0>{}, key0);
+        if (key0 + kKeys < end) take(Number<1>{}, key0 + kKeys);
     }
     const u32x2 ls = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(l), as_bits(l), false, false));
     l = as_float(ls.x) + as_float(ls.y);
@@ -366,7 +385,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     }
     if (on && half == 0) {
         float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
-        stats[0] = ref;
+        stats[0] = started ? ref : kLowest;
         stats[1] = l;
     }
 }
