@@ -3,7 +3,7 @@
 // chunks of them after a cached prefix).
 //
 // A workgroup is four waves on 128 query rows of one (request, key-value head), 32
-// rows a wave, walking over a chunk of the keys 32 at a time. Codes come from memory
+// rows a wave, walking over a chunk of the keys 64 at a time. Codes come from memory
 // to registers one step ahead, become float16 there (exactly: five instructions
 // for four) and go to one of two LDS tiles, whose rows' 16-byte pieces are permuted
 // by `swizzle`; the scales beside them. One barrier a step.
@@ -22,14 +22,12 @@ namespace mnb {
 
 namespace {
 
-constexpr int kKeys = 32;     // of a step
+constexpr int kKeys = 64;     // of a step: four 16-key parts
 constexpr float kLift = 7.0f, kSlack = 8.0f + kLift;
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
-
-template <int N> struct Number { static constexpr int value = N; };
 
 __device__ __forceinline__ f16v mma32(h8 a, h8 b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -79,10 +77,10 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     // scalar loads)
     typedef __attribute__((address_space(4))) const int32_t entry;
     entry *table = (entry *)(a.table + b * a.table_width);
-    int32_t ids[2];      // of the next step's parts
+    int32_t ids[4];      // of the next step's parts
     auto look_up = [&](int key0) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 4; ++s) {
             const uint32_t place = blocks_before(((uint32_t)key0 >> 4) + s, sp.page_magic);
             ids[s] = table[place < (uint32_t)a.table_width ? place : a.table_width - 1];
         }
@@ -107,64 +105,60 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         sees(a, len, n_new, token_of(a, row0 + (wave * 32 < rows ? wave * 32 : 0))));
     const float mul = a.scale * kLog2e;
 
-    // Staging. A wave carries 512 codes of one 16-key part a step, 16 a lane: rows of the
-    // keys and the same of the values (D = 128), or of one of them (D = 64); its lanes
-    // 0..15 besides that part's scales, the keys' or the values'. So a wave's block is
-    // uniform, looked up three steps ahead; its codes are requested two steps ahead,
-    // through buffers that end with the last key that any row sees.
-    constexpr bool kBoth = D == 128;
-    const int part = kBoth ? wave >> 1 : wave & 1, value = kBoth ? wave & 1 : wave >> 1;   // (value: of the scales)
+    // Staging. Wave w carries the keys and the values of the step's part w, 16 codes a
+    // lane and load, and their scales (lanes 0..15 the keys', 16..31 the values'). So a
+    // wave's block is uniform, looked up two steps ahead; its codes are requested one
+    // step ahead, through buffers that end with the last key that any row sees.
+    constexpr int kLoads = D / 64, kLoadRows = 16 / kLoads;
     const uint32_t stride = (uint32_t)c.token_stride;
-    const int row = kBoth ? wave * 8 + lane / kPieces : (wave & 1) * 16 + lane / kPieces, piece = lane % kPieces;
-    const uint32_t at_row = (uint32_t)(row & 15) * stride + piece * 16;
-    u32x4 codes[2][kBoth ? 2 : 1];   // of even and odd steps
-    float scale[2];
-    uint32_t valid[2];   // bit k: key k of the step has a block, and some row sees it
-    auto fetch = [&](auto parity, int key0) {
-        constexpr int buf = decltype(parity)::value;
-        int ok[2];
+    const int row = lane / kPieces, piece = lane % kPieces;   // of a load
+    u32x4 codes[2][kLoads];   // of the keys, of the values
+    float scale;
+    uint64_t valid, valid_next;   // bit k: key k of the step has a block, and some row sees it
+    auto fetch = [&](int key0) {
+        int ok[4];
+        valid_next = 0;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 4; ++s) {
             const int left = end - key0 - 16 * s;
             ok[s] = __builtin_amdgcn_readfirstlane(
-                left < 0 || (uint64_t)(int64_t)ids[s] >= (uint64_t)c.num_blocks ? 0 : left > 16 ? 16 : left);
+                left < 0 || (uint32_t)ids[s] >= (uint32_t)c.num_blocks ? 0 : left > 16 ? 16 : left);
+            valid_next |= (uint64_t)((1u << ok[s]) - 1) << (16 * s);
         }
-        valid[buf] = ((1u << ok[0]) - 1) | ((1u << ok[1]) - 1) << 16;
-        const int id = part ? ids[1] : ids[0], mine_ok = part ? ok[1] : ok[0];
-        const uint32_t number = ((uint32_t)key0 >> 4) + part;
+        const int id = wave == 0 ? ids[0] : wave == 1 ? ids[1] : wave == 2 ? ids[2] : ids[3];
+        const int mine_ok = wave == 0 ? ok[0] : wave == 1 ? ok[1] : wave == 2 ? ok[2] : ok[3];
+        const uint32_t number = ((uint32_t)key0 >> 4) + wave;
         const uint32_t in_page = (number - blocks_before(number, sp.page_magic) * (uint32_t)(c.page >> 4)) << 4;
         const int64_t from = id * c.block_stride + h * c.head_stride + (int64_t)in_page * stride;
         const uint32_t bytes = mine_ok > 0 ? (uint32_t)(mine_ok - 1) * stride + D : 0u;
-        auto request = [&](const int8_t *base) {
-            return __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                           __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base + from), 0, bytes, 0x00020000),
-                           at_row, 0, 0));
-        };
-        if constexpr (kBoth) {
-            codes[buf][0] = request(c.k);
-            codes[buf][1] = request(c.v);
-        } else {
-            codes[buf][0] = request(value ? c.v : c.k);
-        }
-        const float *scales = (value ? c.v_scale : c.k_scale) + id * c.scale_block + h * c.scale_head + in_page;
-        scale[buf] = as_float(__builtin_amdgcn_raw_buffer_load_b32(
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scales), 0, mine_ok * 4u, 0x00020000),
-            (lane & 15) * 4, 0, 0));
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                codes[v][i] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>((v ? c.v : c.k) + from), 0, bytes,
+                                                                 0x00020000),
+                               (uint32_t)(i * kLoadRows + row) * stride + piece * 16, 0, 0));
+        const int64_t at = id * c.scale_block + h * c.scale_head + in_page + (lane & 15);
+        scale = 0.0f;
+        if ((lane & 15) < mine_ok && lane < 32) scale = (lane < 16 ? c.k_scale : c.v_scale)[at];
     };
-    const int put_at = row * D, lo = ((2 * piece) ^ swizzle<D>(row)) * 8, hi = ((2 * piece + 1) ^ swizzle<D>(row)) * 8;
-    auto put = [&](auto parity) {
-        constexpr int buf = decltype(parity)::value;
+    auto put = [&](int buf) {
 #pragma unroll
-        for (int e = 0; e < (kBoth ? 2 : 1); ++e) {
-            uint32_t w[8];
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) widen(codes[buf][e][k], w + 2 * k);
-            _Float16 *to = ((kBoth ? e == 1 : value == 1) ? s_v[buf] : s_k[buf]) + put_at;
-            *reinterpret_cast<u32x4 *>(to + lo) = u32x4{w[0], w[1], w[2], w[3]};
-            *reinterpret_cast<u32x4 *>(to + hi) = u32x4{w[4], w[5], w[6], w[7]};
-        }
-        if (lane < 16) (value ? s_vs : s_ks)[buf][16 * part + lane] = value ? scale[buf] : scale[buf] * mul;
+            for (int i = 0; i < kLoads; ++i) {
+                const int to_row = 16 * wave + i * kLoadRows + row;
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) widen(codes[v][i][k], w + 2 * k);
+                _Float16 *to = (v ? s_v[buf] : s_k[buf]) + to_row * D;
+                *reinterpret_cast<u32x4 *>(to + ((2 * piece) ^ swizzle<D>(to_row)) * 8) = u32x4{w[0], w[1], w[2], w[3]};
+                *reinterpret_cast<u32x4 *>(to + ((2 * piece + 1) ^ swizzle<D>(to_row)) * 8) =
+                    u32x4{w[4], w[5], w[6], w[7]};
+            }
+        if (lane < 32) (lane < 16 ? s_ks : s_vs)[buf][16 * wave + (lane & 15)] = lane < 16 ? scale * mul : scale;
     };
 
     // Whole rows of a [token][head][D] tensor: lane l of step k carries 16 bytes of the
@@ -172,7 +166,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     // row's 16-byte pieces are permuted by the row. (Loops over k stay loops: the code is
     // run once a launch, out of a cold instruction cache.)
     constexpr int kRowPieces = D / 8, kRowsAtOnce = 64 / kRowPieces, kCarries = 32 / kRowsAtOnce;
-    _Float16 *s_mine = s_tiles + wave * (32 * D);
+    _Float16 *s_mine = s_tiles + wave * kTile;
     auto in_rows = [&](int row, int piece) { return s_mine + row * D + (piece ^ (row & (kRowPieces - 1))) * 8; };
     const int carried = lane / kRowPieces, carried_piece = lane % kRowPieces;
     auto token_head = [&](int row, int64_t &of, int64_t &head) {   // of the wave's row
@@ -205,7 +199,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     float ref = 0.0f, l = 0.0f;
     bool started = false;
     int unit = 1;
-    fetch(Number<0>{}, begin);
+    fetch(begin);
     look_up(begin + kKeys);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the compiler does not count loads to LDS)
     uint32_t top = 0;
@@ -225,60 +219,68 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     if (!finite)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) q[j] = h8{};
-    fetch(Number<1>{}, begin + kKeys);
-    look_up(begin + 2 * kKeys);
     __syncthreads();   // (the tiles' place is free)
-    put(Number<0>{});
-    auto take = [&](auto parity, int key0) __attribute__((always_inline)) {
-        constexpr int buf = decltype(parity)::value;
+    put(0);
+    valid = valid_next;
+    int buf = 0;
+    for (int key0 = begin; key0 < end; key0 += kKeys, buf ^= 1) {
         __syncthreads();
-        const uint32_t seen_keys = valid[buf];
         // (past the last key: no bytes)
-        fetch(parity, key0 + 2 * kKeys);
-        look_up(key0 + 3 * kKeys);
-        f16v s;
+        fetch(key0 + kKeys);
+        look_up(key0 + 2 * kKeys);
+        f16v s[2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            const int p = (2 * j + half) ^ swizzle<D>(col);
-            s = mma32(*reinterpret_cast<const h8 *>(s_k[buf] + col * D + p * 8), q[j], s);
-        }
-        // element e is key e % 4 + 8 (e / 4) + 4 half
-        f4 ks[4], vs[4];
+            const _Float16 *from = s_k[buf] + col * D + ((2 * j + half) ^ swizzle<D>(col)) * 8;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            ks[j] = *reinterpret_cast<const f4 *>(s_ks[buf] + 8 * j + 4 * half);
-            vs[j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 8 * j + 4 * half);
+            for (int t = 0; t < 2; ++t) s[t] = mma32(*reinterpret_cast<const h8 *>(from + 32 * t * D), q[j], s[t]);
         }
-        // the largest value scale that is a number; from 2^125 on float16 outputs overflow
-        // in any case
+        // element e of half t is key 32 t + e % 4 + 8 (e / 4) + 4 half. The largest value
+        // scale that is a number; from 2^125 on float16 outputs overflow in any case
+        f4 vs[2][4];
         float scales = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[j][e]);
+            for (int j = 0; j < 4; ++j) {
+                vs[t][j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 32 * t + 8 * j + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[t][j][e]);
+            }
         int most = __builtin_amdgcn_readfirstlane((int)as_bits(halves_max(scales))) >> 23;
         most = most < 252 ? most : 252;
         // scores less the reference, plus the unit's power of two: its inverse, 2^(126 -
         // unit), then comes with the weights and leaves value scales below one
         float shift = (float)(126 - unit);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], ks[e / 4][e % 4], shift - ref);
-        if (seen_keys != 0xFFFFFFFFu || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
-            const int left = mine - key0;
-            uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
-            bits = (bits & seen_keys) >> (4 * half);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t seen = (uint32_t)((int)(bits << (31 - e % 4 - 8 * (e / 4))) >> 31);
-                s[e] = as_float((as_bits(s[e]) & seen) | (0xFF800000u & ~seen));
-                vs[e / 4][e % 4] = as_float(as_bits(vs[e / 4][e % 4]) & seen);
+            for (int j = 0; j < 4; ++j) {
+                const f4 ks = *reinterpret_cast<const f4 *>(s_ks[buf] + 32 * t + 8 * j + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][4 * j + e] = __builtin_fmaf(s[t][4 * j + e], ks[e], shift - ref);
+            }
+        if (valid != ~0ull || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int left = mine - key0 - 32 * t;
+                uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
+                bits = (bits & (uint32_t)(valid >> (32 * t))) >> (4 * half);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t seen = (uint32_t)((int)(bits << (31 - e % 4 - 8 * (e / 4))) >> 31);
+                    s[t][e] = as_float((as_bits(s[t][e]) & seen) | (0xFF800000u & ~seen));
+                    vs[t][e / 4][e % 4] = as_float(as_bits(vs[t][e / 4][e % 4]) & seen);
+                }
             }
         }
-        float top = s[0];
+        float top = s[0][0];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+        for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
         if (__any(top > (started ? shift + kSlack : -__builtin_inff())) || most > unit) {
             top = halves_max(top);
             const bool some = top > -__builtin_inff();
@@ -296,47 +298,48 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             ref += by;
             by += (float)(raised - unit);
             unit = raised;
-            shift = (float)(126 - unit);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] -= by;
+            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] -= by;
         }
-        u32x4 p[2];
-        float sum = 0.0f;
+        u32x4 p[2][2];
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const float w0 = __builtin_amdgcn_exp2f(s[e]), w1 = __builtin_amdgcn_exp2f(s[e + 1]);
-            sum += w0;
-            sum += w1;
-            const h2 w = {(_Float16)(w0 * vs[e / 4][e % 4]), (_Float16)(w1 * vs[e / 4][e % 4 + 1])};
-            p[e / 8][e % 8 / 2] = as_u32(w);
-        }
-        l = __builtin_fmaf(sum, as_float((uint32_t)(unit + 1) << 23), l);   // 2^(unit - 126)
-        // p[k] element j of lane half h is key 16 k + 8 (j / 4) + 4 h + j % 4
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                h8 w;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    // 16 lanes read four keys by 16 dimensions: lane L supplies key
-                    // L / 4, four dimensions 4 (L % 4) on, and receives dimension L of
-                    // the four keys
-                    const int row = 16 * k + 8 * u + 4 * half + (lane & 15) / 4;
-                    const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                    const int at = row * D + (((dim >> 3) ^ swizzle<D>(row)) << 3) + (dim & 7);
-                    const h4 x = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                            (__attribute__((address_space(3))) s4 *)(s_v[buf] + at)));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) w[4 * u + j] = x[j];
-                }
-                o[d] = mma32(w, __builtin_bit_cast(h8, p[k]), o[d]);
+            for (int e = 0; e < 16; e += 2) {
+                const float w0 = __builtin_amdgcn_exp2f(s[t][e]), w1 = __builtin_amdgcn_exp2f(s[t][e + 1]);
+                sum[0] += w0;
+                sum[1] += w1;
+                const h2 w = {(_Float16)(w0 * vs[t][e / 4][e % 4]), (_Float16)(w1 * vs[t][e / 4][e % 4 + 1])};
+                p[t][e / 8][e % 8 / 2] = as_u32(w);
             }
-        put(Number<buf ^ 1>{});
-    };
-    for (int key0 = begin; key0 < end; key0 += 2 * kKeys) {
-        take(Number<0>{}, key0);
-        if (key0 + kKeys < end) take(Number<1>{}, key0 + kKeys);
+        l = __builtin_fmaf(sum[0] + sum[1], as_float((uint32_t)(unit + 1) << 23), l);   // 2^(unit - 126)
+        // p[t][k] element j of lane half h is key 32 t + 16 k + 8 (j / 4) + 4 h + j % 4
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) {
+                    h8 w;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        // 16 lanes read four keys by 16 dimensions: lane L supplies key
+                        // L / 4, four dimensions 4 (L % 4) on, and receives dimension L of
+                        // the four keys
+                        const int row = 32 * t + 16 * k + 8 * u + 4 * half + (lane & 15) / 4;
+                        const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+                        const int at = row * D + (((dim >> 3) ^ swizzle<D>(row)) << 3) + (dim & 7);
+                        const h4 x = __builtin_bit_cast(
+                            h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (__attribute__((address_space(3))) s4 *)(s_v[buf] + at)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[4 * u + j] = x[j];
+                    }
+                    o[d] = mma32(w, __builtin_bit_cast(h8, p[t][k]), o[d]);
+                }
+        put(buf ^ 1);
+        valid = valid_next;
     }
     const u32x2 ls = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(l), as_bits(l), false, false));
     l = as_float(ls.x) + as_float(ls.y);
