@@ -35,6 +35,7 @@ struct Kv8Args {
     int64_t k_stride, v_stride;
     const int64_t *slots;
     int64_t tokens;
+    uint32_t page_magic;    // (set by the launcher)
 };
 hipError_t launch_kv8_append(const Kv8Args &a, int head_dim, int dtype, hipStream_t st);
 hipError_t launch_kv8_read(const Kv8Args &a, int head_dim, int dtype, hipStream_t st);

@@ -10,151 +10,249 @@ namespace {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
-constexpr int kPart = 8;   // elements of a row per lane
+constexpr int kPart = 8;    // elements of a row per lane (append)
+constexpr int kAhead = 4;   // rows a lane has under way
 
 // Largest scale s with 127 s within float32.
 constexpr float kMostScale = 0x1.020406p+121f;
 
 // A slot's place: block, and offset within its page; false outside the cache.
-__device__ __forceinline__ bool place_of(const Cache8 &c, int64_t slot, int64_t &block, int &offset) {
+__device__ __forceinline__ bool place_of(const Kv8Args &a, int64_t slot, int64_t &block, int &offset) {
     if (slot < 0) return false;
-    // (pages are multiples of 16; slots of most caches fit 32 bits, and 64-bit
-    // divisions are slow)
+    // (slots of most caches are below 2^30, where a product gives the quotient: pages are
+    // multiples of 16)
     const uint64_t part = (uint64_t)slot >> 4;
-    const uint32_t parts = (uint32_t)c.page >> 4;
-    block = part >> 32 ? (int64_t)(part / parts) : (int64_t)((uint32_t)part / parts);
-    offset = (int)(slot - block * c.page);
-    return block < c.num_blocks;
+    if (part >> 26) block = (int64_t)(part / ((uint32_t)a.cache.page >> 4));
+    else block = a.page_magic ? __umulhi((uint32_t)part, a.page_magic) : (uint32_t)part;
+    offset = (int)(slot - block * a.cache.page);
+    return block < a.cache.num_blocks;
 }
 
-// Eight elements of a row as float32.
-template <typename T> __device__ __forceinline__ void load8(const uint8_t *from, float *x) {
-    if constexpr (sizeof(T) == 2) {
-        const h8 w = *reinterpret_cast<const h8 *>(from);
+// Which row of a workgroup's tokens: token, keys or values, head. r < 2^24, by a
+// reciprocal that is off by at most one.
+struct Row {
+    int64_t token;
+    int head;
+    bool second, on;
+};
+__device__ __forceinline__ Row row_of(const Kv8Args &a, int64_t t0, int r, int rows, float per_each) {
+    const int each = 2 * a.cache.heads;
+    int which = (int)((float)r * per_each);
+    const int rest = r - which * each;
+    which += rest >= each ? 1 : 0;
+    which -= rest < 0 ? 1 : 0;
+    int of = r - which * each;
+    Row x;
+    x.token = t0 + which;
+    x.second = of >= a.cache.heads;
+    x.head = x.second ? of - a.cache.heads : of;
+    x.on = r < rows && x.token < a.tokens;
+    return x;
+}
+
+// Eight elements of a row.
+template <typename T> struct Eight {
+    u32x4 w[sizeof(T) == 2 ? 1 : 2];
+    __device__ __forceinline__ void load(const uint8_t *from) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)w[i];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const f4 w = reinterpret_cast<const f4 *>(from)[j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * j + i] = w[i];
-        }
+        for (int j = 0; j < (sizeof(T) == 2 ? 1 : 2); ++j) w[j] = reinterpret_cast<const u32x4 *>(from)[j];
     }
-}
+    __device__ __forceinline__ void as_floats(float *x) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if constexpr (sizeof(T) == 2) x[i] = (float)__builtin_bit_cast(h8, w[0])[i];
+            else x[i] = __builtin_bit_cast(f4, w[i / 4])[i % 4];
+    }
+};
 
-// x / s to the nearest whole number, ties to even: the float32 quotient is within
-// one step of it, and the remainder (exact: it is a multiple of the smaller
-// operand's last place and at most s) says where the border lies.
-__device__ __forceinline__ int code_of(float x, float s) {
-    float c = __builtin_rintf(x / s);
+template <int N> __device__ __forceinline__ uint32_t turned(uint32_t x) {   // by N of 16 lanes
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, 0x120 + N, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) { return x > y ? x : y; }
+
+// x / s to the nearest whole number, ties to even, of c within one step of it: the
+// remainder (exact: it is a multiple of the smaller operand's last place and below
+// 2 s) says where the border lies.
+__device__ __forceinline__ float nearest(float c, float x, float s) {
     const float twice = 2.0f * __builtin_fmaf(-c, s, x);
     const bool odd = (int)c & 1;
     if (twice > s || (twice == s && odd)) c += 1.0f;
     else if (twice < -s || (twice == -s && odd)) c -= 1.0f;
-    return (int)fminf(fmaxf(c, -127.0f), 127.0f);
+    return c;
 }
 
 }  // namespace
 
-// A row of D elements is D / 8 lanes; workgroups take `per` tokens, keys and
-// values of all heads.
+// A row of D elements is D / 8 lanes; a workgroup takes `per` tokens, keys and values of
+// all heads, kAhead rows a lane at a time: a row's load waits for nothing, its slot
+// is needed only to store it. A code is x (1 / s) rounded by adding 1.5 * 2^23; only where
+// the remainder of one of a lane's eight comes within 2^-12 of half a step can the
+// reciprocal's rounding matter, and these are put right exactly.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Args a, int per) {
+__global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Args a, int per, float per_each) {
     constexpr int kLanes = D / kPart, kRows = kThreads / kLanes;
-    const int lane = threadIdx.x % kLanes, heads = a.cache.heads, rows = per * 2 * heads;
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per) {
-        for (int r = threadIdx.x / kLanes; r < rows; r += kRows) {
-            const int which = r / (2 * heads), of = r - which * 2 * heads;
-            const int64_t t = t0 + which;
-            if (t >= a.tokens) break;
-            int64_t block;
-            int offset;
-            if (!place_of(a.cache, a.slots[t], block, offset)) continue;
-            const bool second = of >= heads;
-            const int h = second ? of - heads : of;
-            const uint8_t *from = (second ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
-                                  ((int64_t)h * D + lane * kPart) * (int64_t)sizeof(T);
-            float x[kPart];
-            load8<T>(from, x);
-            // (as whole numbers: infinities and NaN are above every finite one)
-            uint32_t top = 0;
+    constexpr float kRound = 12582912.0f;
+    const int lane = threadIdx.x % kLanes, rows = per * 2 * a.cache.heads;
+    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per)
+        for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kRows * kAhead) {
+            Row row[kAhead];
+            Eight<T> in[kAhead];
+            int64_t slot[kAhead];
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-                const uint32_t bits = __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu;
-                top = bits > top ? bits : top;
+            for (int u = 0; u < kAhead; ++u) {
+                row[u] = row_of(a, t0, r0 + u * kRows, rows, per_each);
+                slot[u] = -1;
+                if (row[u].on) {
+                    slot[u] = a.slots[row[u].token];
+                    in[u].load((row[u].second ? a.v + row[u].token * a.v_stride : a.k + row[u].token * a.k_stride) +
+                               ((int64_t)row[u].head * D + lane * kPart) * (int64_t)sizeof(T));
+                }
             }
 #pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1) {
-                const uint32_t other = (uint32_t)__shfl_xor((int)top, d);
-                top = other > top ? other : top;
-            }
-            const bool finite = top < 0x7F800000u;
-            const float s = fminf(__builtin_bit_cast(float, top) / 127.0f, kMostScale);
-            uint32_t w[2] = {0, 0};
-            if (finite && s > 0.0f) {
+            for (int u = 0; u < kAhead; ++u) {
+                int64_t block;
+                int offset;
+                if (!place_of(a, slot[u], block, offset)) continue;   // (a row's lanes together)
+                float x[kPart];
+                in[u].as_floats(x);
+                // (as whole numbers: infinities and NaN are above every finite one)
+                uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < kPart; ++i) w[i / 4] |= (uint32_t)(code_of(x[i], s) & 0xFF) << (8 * (i % 4));
+                for (int i = 0; i < kPart; ++i) top = larger(top, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
+                if constexpr (kLanes == 16) {
+                    top = larger(top, turned<8>(top));
+                    top = larger(top, turned<4>(top));
+                    top = larger(top, turned<2>(top));
+                    top = larger(top, turned<1>(top));
+                } else {   // 8 lanes: the other half row's are another row's
+#pragma unroll
+                    for (int d = 1; d < kLanes; d <<= 1) top = larger(top, (uint32_t)__shfl_xor((int)top, d));
+                }
+                const bool finite = top < 0x7F800000u;
+                const float s = fminf(__builtin_bit_cast(float, top) / 127.0f, kMostScale);
+                uint32_t w[2] = {0, 0};
+                if (finite && s > 0.0f) {
+                    // (the smallest rows 2^64 times as large, which float16 has none of)
+                    const float lift = sizeof(T) == 4 && s < 0x1p-60f ? 0x1p64f : 1.0f, step = s * lift;
+                    const float by = __builtin_amdgcn_rcpf(step), close = step * (0.5f - 0x1p-12f);
+                    float c[kPart], far = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPart; ++i) {
+                        if constexpr (sizeof(T) == 4) x[i] *= lift;
+                        c[i] = __builtin_fmaf(x[i], by, kRound) - kRound;
+                        far = fmaxf(far, __builtin_fabsf(__builtin_fmaf(-c[i], step, x[i])));
+                    }
+                    if (far >= close)
+#pragma unroll
+                        for (int i = 0; i < kPart; ++i) c[i] = nearest(c[i], x[i], step);
+                    // (a scale below the normal range may be so much too small that 127 is not enough)
+#pragma unroll
+                    for (int i = 0; i < kPart; i += 4) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float code = c[i + j];
+                            if constexpr (sizeof(T) == 4) code = fminf(fmaxf(code, -127.0f), 127.0f);
+                            b[j] = __builtin_bit_cast(uint32_t, code + kRound);
+                        }
+                        w[i / 4] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                                                         __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
+                    }
+                }
+                int8_t *to = (row[u].second ? a.cache.v : a.cache.k) + block * a.cache.block_stride +
+                             row[u].head * a.cache.head_stride + offset * a.cache.token_stride + lane * kPart;
+                *reinterpret_cast<u32x2 *>(to) = u32x2{w[0], w[1]};
+                if (lane == 0)
+                    (row[u].second ? a.cache.v_scale
+                                   : a.cache.k_scale)[block * a.cache.scale_block + row[u].head * a.cache.scale_head +
+                                                      offset] = finite ? s : __builtin_nanf("");
             }
-            int8_t *to = (second ? a.cache.v : a.cache.k) + block * a.cache.block_stride + h * a.cache.head_stride +
-                         offset * a.cache.token_stride + lane * kPart;
-            *reinterpret_cast<u32x2 *>(to) = u32x2{w[0], w[1]};
-            if (lane == 0)
-                (second ? a.cache.v_scale : a.cache.k_scale)[block * a.cache.scale_block + h * a.cache.scale_head +
-                                                             offset] = finite ? s : __builtin_nanf("");
         }
-    }
 }
 
-// 16 bytes of output a lane.
+// Two codes times s, each exact product rounded once to float16, which the mixed multiply-
+// add does (a float32 product and its conversion would round twice).
+__device__ __forceinline__ uint32_t half_pair(float c0, float c1, float s) {
+    uint32_t y;
+    asm("v_fma_mixlo_f16 %0, %1, %2, 0" : "=v"(y) : "v"(c0), "v"(s));
+    asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(y) : "v"(c1), "v"(s));
+    return y;
+}
+
+// 16 bytes of output a lane, kAhead rows at a time.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Args a, int per) {
+__global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Args a, int per, float per_each) {
     constexpr int kOut = 16 / (int)sizeof(T), kLanes = D / kOut, kRows = kThreads / kLanes;
-    const int lane = threadIdx.x % kLanes, heads = a.cache.heads, rows = per * 2 * heads;
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per) {
-        for (int r = threadIdx.x / kLanes; r < rows; r += kRows) {
-            const int which = r / (2 * heads), of = r - which * 2 * heads;
-            const int64_t t = t0 + which;
-            if (t >= a.tokens) break;
-            const bool second = of >= heads;
-            const int h = second ? of - heads : of;
-            int64_t block;
-            int offset;
-            uint32_t w[kOut / 4] = {};
-            float s = 0.0f;
-            if (place_of(a.cache, a.slots[t], block, offset)) {
-                const int8_t *from = (second ? a.cache.v : a.cache.k) + block * a.cache.block_stride +
-                                     h * a.cache.head_stride + offset * a.cache.token_stride + lane * kOut;
+    const int lane = threadIdx.x % kLanes, rows = per * 2 * a.cache.heads;
+    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per)
+        for (int r0 = threadIdx.x / kLanes; r0 < rows; r0 += kRows * kAhead) {
+            Row row[kAhead];
+            int64_t slot[kAhead];
+            uint32_t w[kAhead][kOut / 4];
+            float s[kAhead];
 #pragma unroll
-                for (int i = 0; i < kOut / 4; ++i) w[i] = reinterpret_cast<const uint32_t *>(from)[i];
-                s = (second ? a.cache.v_scale : a.cache.k_scale)[block * a.cache.scale_block + h * a.cache.scale_head +
-                                                                 offset];
+            for (int u = 0; u < kAhead; ++u) {
+                row[u] = row_of(a, t0, r0 + u * kRows, rows, per_each);
+                slot[u] = row[u].on ? a.slots[row[u].token] : -1;
             }
-            T y[kOut];
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-                const float c = (float)(int8_t)(w[i / 4] >> (8 * (i % 4)));
-                if constexpr (sizeof(T) == 4) y[i] = c * s;
-                else y[i] = (T)mul_round_odd(c, s);
+            for (int u = 0; u < kAhead; ++u) {
+                int64_t block;
+                int offset;
+                s[u] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kOut / 4; ++i) w[u][i] = 0;
+                if (!place_of(a, slot[u], block, offset)) continue;
+                const int8_t *from = (row[u].second ? a.cache.v : a.cache.k) + block * a.cache.block_stride +
+                                     row[u].head * a.cache.head_stride + offset * a.cache.token_stride + lane * kOut;
+                if constexpr (kOut == 8) {
+                    const u32x2 both = *reinterpret_cast<const u32x2 *>(from);
+                    w[u][0] = both.x;
+                    w[u][1] = both.y;
+                } else {
+                    w[u][0] = *reinterpret_cast<const uint32_t *>(from);
+                }
+                s[u] = (row[u].second ? a.cache.v_scale
+                                      : a.cache.k_scale)[block * a.cache.scale_block +
+                                                         row[u].head * a.cache.scale_head + offset];
             }
-            uint8_t *to = const_cast<uint8_t *>(second ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
-                          ((int64_t)h * D + lane * kOut) * (int64_t)sizeof(T);
-            *reinterpret_cast<u32x4 *>(to) = *reinterpret_cast<const u32x4 *>(y);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (!row[u].on) continue;
+                u32x4 y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b = w[u][i * kOut / 16];
+                    auto code = [&](int at) { return (float)(int8_t)(b >> at); };
+                    if constexpr (sizeof(T) == 2) y[i] = half_pair(code(16 * (i & 1)), code(16 * (i & 1) + 8), s[u]);
+                    else y[i] = __builtin_bit_cast(uint32_t, code(8 * i) * s[u]);
+                }
+                uint8_t *to = const_cast<uint8_t *>(row[u].second ? a.v + row[u].token * a.v_stride
+                                                                  : a.k + row[u].token * a.k_stride) +
+                              ((int64_t)row[u].head * D + lane * kOut) * (int64_t)sizeof(T);
+                *reinterpret_cast<u32x4 *>(to) = y;
+            }
         }
-    }
 }
 
 namespace {
 
-// Tokens per workgroup: enough rows for its lanes.
+// Tokens per workgroup: rows for its lanes, kAhead times where there are tokens enough
+// to fill the card's 2048 places for workgroups besides.
 template <typename T, int D, bool APPEND> hipError_t launch(const Kv8Args &a, hipStream_t st) {
     constexpr int lanes = APPEND ? D / kPart : D * (int)sizeof(T) / 16, rows = kThreads / lanes;
     const int64_t each = 2 * (int64_t)a.cache.heads;
-    const int per = each < rows ? (int)(rows / each) : 1;
+    int64_t per = each < rows ? rows / each : 1;
+    const int64_t more = each < rows * kAhead ? rows * kAhead / each : 1;
+    if (more > per && a.tokens >= 2048 * more) per = more;
     const int64_t wgs = (a.tokens + per - 1) / per;
     const unsigned grid = (unsigned)(wgs < 65536 ? wgs : 65536);
-    if constexpr (APPEND) kv8_append_kernel<T, D><<<grid, kThreads, 0, st>>>(a, per);
-    else kv8_read_kernel<T, D><<<grid, kThreads, 0, st>>>(a, per);
+    const float per_each = 1.0f / (float)each;
+    Kv8Args c = a;
+    const uint32_t parts = (uint32_t)a.cache.page / 16;
+    c.page_magic = parts == 1 ? 0 : (uint32_t)(((1ull << 32) + parts - 1) / parts);
+    if constexpr (APPEND) kv8_append_kernel<T, D><<<grid, kThreads, 0, st>>>(c, (int)per, per_each);
+    else kv8_read_kernel<T, D><<<grid, kThreads, 0, st>>>(c, (int)per, per_each);
     return hipGetLastError();
 }
 
