@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kMostPairs = 512;
+constexpr int kAhead = 4;
 
 // gain * (cos, sin) of position * freq radians. The fraction of a turn is taken in
 // float64: of a float32 angle of 10^5 turns nothing would be left below 2^-7.
@@ -20,60 +21,88 @@ __device__ __forceinline__ float2 turn_of(int position, double freq, float gain)
     return float2{gain * c, gain * s};
 }
 
+// A float32 result rounded to T. (Hidden from the compiler, which would fold some of the
+// conversions, and not others, into multiply-adds of another rounding: a head's bits
+// would go by its place in the loop.)
+template <typename T> __device__ __forceinline__ T rounded(float x) {
+    asm("" : "+v"(x));
+    return (T)x;
+}
+
 }  // namespace
 
 // A wave takes one token: its lanes work out the pairs' cosines and sines into
-// LDS, then turn the heads, a unit a lane and step. VEC: 16-byte pieces (or, in
-// the half layout, two of them, one from each half); otherwise a unit is one
-// pair or one element behind them.
+// LDS, then turn the heads, a unit a lane, kAhead units under way. VEC: 16-byte pieces
+// (or, in the half layout, two of them, one from each half); otherwise a unit is one
+// pair, or one element behind them.
 template <typename T, bool INTERLEAVED, bool VEC>
-__global__ __launch_bounds__(64 * kWaves) void rope_kernel(RopeArgs a) {
+__global__ __launch_bounds__(64 * kWaves) void rope_kernel(RopeArgs a, float per_units) {
     constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;
+    constexpr bool kTwo = !(INTERLEAVED && VEC);   // a unit is two pieces
+    typedef T piece __attribute__((ext_vector_type(kPiece)));
     __shared__ float2 s_turn[kWaves][kMostPairs];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= a.tokens) return;
-    const int pairs = a.rot_dim / 2, position = a.positions[t];
-    for (int i = lane; i < pairs; i += 64) s_turn[wave][i] = turn_of(position, a.freqs[i], a.gain);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     // units of a head: those that turn, then those that are copied
-    const int turning = INTERLEAVED && VEC ? a.rot_dim / kPiece : pairs / kPiece;
+    const int pairs = a.rot_dim / 2, turning = kTwo ? pairs / kPiece : a.rot_dim / kPiece;
     const int units = turning + (a.head_dim - a.rot_dim) / kPiece;
     const int all = (a.q_heads + a.k_heads) * units;
-    for (int e = lane; e < all; e += 64) {
-        const int h = e / units, u = e - h * units;
-        const bool key = h >= a.q_heads;
-        const int at = (key ? h - a.q_heads : h) * a.head_dim;
-        const T *from = reinterpret_cast<const T *>(key ? a.k + t * a.k_stride : a.q + t * a.q_stride) + at;
-        T *to = reinterpret_cast<T *>(key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride) + at;
-        typedef T piece __attribute__((ext_vector_type(kPiece)));
-        if (u >= turning) {
-            const int d = a.rot_dim + (u - turning) * kPiece;
-            *reinterpret_cast<piece *>(to + d) = *reinterpret_cast<const piece *>(from + d);
-        } else if constexpr (INTERLEAVED && VEC) {
-            piece x = *reinterpret_cast<const piece *>(from + u * kPiece);
+    const int position = a.positions[t];
+    bool ready = false;
+    for (int e0 = lane; e0 < all + lane; e0 += 64 * kAhead) {   // (the wave's lanes together)
+        piece x0[kAhead], x1[kAhead];
+        T *to[kAhead];
+        int unit[kAhead];
 #pragma unroll
-            for (int i = 0; i < kPiece; i += 2) {
-                const float2 cs = s_turn[wave][(u * kPiece + i) / 2];
-                const float x0 = (float)x[i], x1 = (float)x[i + 1];
-                x[i] = (T)__builtin_fmaf(x0, cs.x, -(x1 * cs.y));
-                x[i + 1] = (T)__builtin_fmaf(x0, cs.y, x1 * cs.x);
+        for (int i = 0; i < kAhead; ++i) {
+            // (e < 2^24 by a reciprocal that is off by at most one, others by a division)
+            const int e = e0 + 64 * i;
+            int h = all < (1 << 24) ? (int)((float)e * per_units) : e / units, u = e - h * units;
+            if (u >= units) ++h, u -= units;
+            if (u < 0) --h, u += units;
+            const bool key = h >= a.q_heads;
+            const int at = (key ? h - a.q_heads : h) * a.head_dim;
+            const int d = u < turning ? (kTwo && INTERLEAVED ? 2 * u : u * kPiece) : a.rot_dim + (u - turning) * kPiece;
+            unit[i] = e < all ? u : -1;
+            to[i] = reinterpret_cast<T *>(key ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride) + at + d;
+            if (e < all) {
+                const T *from = reinterpret_cast<const T *>(key ? a.k + t * a.k_stride : a.q + t * a.q_stride) + at + d;
+                x0[i] = *reinterpret_cast<const piece *>(from);
+                if (kTwo && u < turning) x1[i] = *reinterpret_cast<const piece *>(from + (INTERLEAVED ? 1 : pairs));
             }
-            *reinterpret_cast<piece *>(to + u * kPiece) = x;
-        } else {
-            const int d0 = INTERLEAVED ? 2 * u : u * kPiece, d1 = INTERLEAVED ? d0 + 1 : d0 + pairs;
-            piece x0 = *reinterpret_cast<const piece *>(from + d0), x1 = *reinterpret_cast<const piece *>(from + d1);
-            piece y0, y1;
+        }
+        if (!ready) {   // (behind the first loads)
+            for (int i = lane; i < pairs; i += 64) s_turn[wave][i] = turn_of(position, a.freqs[i], a.gain);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            ready = true;
+        }
 #pragma unroll
-            for (int i = 0; i < kPiece; ++i) {
-                const float2 cs = s_turn[wave][u * kPiece + i];
-                const float f0 = (float)x0[i], f1 = (float)x1[i];
-                y0[i] = (T)__builtin_fmaf(f0, cs.x, -(f1 * cs.y));
-                y1[i] = (T)__builtin_fmaf(f0, cs.y, f1 * cs.x);
+        for (int i = 0; i < kAhead; ++i) {
+            if (unit[i] < 0) continue;
+            if (unit[i] < turning) {
+                if constexpr (kTwo) {
+                    piece y1;
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j) {
+                        const float2 cs = s_turn[wave][unit[i] * kPiece + j];
+                        const float f0 = (float)x0[i][j], f1 = (float)x1[i][j];
+                        x0[i][j] = rounded<T>(__builtin_fmaf(f0, cs.x, -(f1 * cs.y)));
+                        y1[j] = rounded<T>(__builtin_fmaf(f0, cs.y, f1 * cs.x));
+                    }
+                    *reinterpret_cast<piece *>(to[i] + (INTERLEAVED ? 1 : pairs)) = y1;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kPiece; j += 2) {
+                        const float2 cs = s_turn[wave][(unit[i] * kPiece + j) / 2];
+                        const float f0 = (float)x0[i][j], f1 = (float)x0[i][j + 1];
+                        x0[i][j] = rounded<T>(__builtin_fmaf(f0, cs.x, -(f1 * cs.y)));
+                        x0[i][j + 1] = rounded<T>(__builtin_fmaf(f0, cs.y, f1 * cs.x));
+                    }
+                }
             }
-            *reinterpret_cast<piece *>(to + d0) = y0;
-            *reinterpret_cast<piece *>(to + d1) = y1;
+            *reinterpret_cast<piece *>(to[i]) = x0[i];
         }
     }
 }
@@ -83,11 +112,12 @@ namespace {
 template <typename T, bool INTERLEAVED> hipError_t launch(const RopeArgs &a, hipStream_t st) {
     const unsigned grid = (unsigned)((a.tokens + kWaves - 1) / kWaves);
     constexpr int piece = 16 / (int)sizeof(T);
+    const bool vec = INTERLEAVED ? a.rot_dim % piece == 0 : a.rot_dim / 2 % piece == 0;
+    const int turning = !vec ? a.rot_dim / 2 : INTERLEAVED ? a.rot_dim / piece : a.rot_dim / 2 / piece;
+    const float per_units = 1.0f / (float)(turning + (a.head_dim - a.rot_dim) / (vec ? piece : 1));
     // (head_dim is a whole number of pieces)
-    if (INTERLEAVED ? a.rot_dim % piece == 0 : a.rot_dim / 2 % piece == 0)
-        rope_kernel<T, INTERLEAVED, true><<<grid, 64 * kWaves, 0, st>>>(a);
-    else
-        rope_kernel<T, INTERLEAVED, false><<<grid, 64 * kWaves, 0, st>>>(a);
+    if (vec) rope_kernel<T, INTERLEAVED, true><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
+    else rope_kernel<T, INTERLEAVED, false><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
     return hipGetLastError();
 }
 

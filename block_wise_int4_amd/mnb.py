@@ -853,6 +853,27 @@ def rope_frequencies(rot_dim, base=10000.0, linear=1.0, stretch=1.0, by_parts=No
     return torch.tensor(freqs, dtype=torch.float64, device=device), gain
 
 
+def _rope_rows(x, out, name, T, dim, dtype, index, device):
+    """(out, the library's arguments) of queries or keys x [T, heads, dim]."""
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    (rows, heads, width), (step, head_step, last) = x.shape, x.stride()
+    to_step, to_head_step, to_last = out.stride() if out.shape == x.shape else (0, 0, 0)
+    if (x.dtype is not dtype or out.dtype is not dtype or x.get_device() != index or out.get_device() != index
+            or rows != T or width != dim or last != 1 or to_last != 1
+            or (heads > 1 and (head_step != dim or to_head_step != dim))):
+        if rows != T or width != dim:
+            raise ValueError(f"{name} must be [{T}, heads, {dim}]")
+        if out.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape")
+        _check_buf(x, name, dtype, x.numel(), device)
+        _check_buf(out, name + "_out", dtype, x.numel(), device)
+        raise ValueError(f"{name} and {name}_out must have contiguous heads")
+    if T < 2:
+        step = to_step = 0
+    return out, (x.data_ptr(), step, out.data_ptr(), to_step, heads)
+
+
 def mnb_rope(q, k, positions, freqs, interleaved=False, gain=1.0, q_out=None, k_out=None):
     """Turns queries q [T, heads, dim] and keys k [T, kv_heads, dim] (either may
     be None; any token stride) by their positions (int32 [T]): the first
@@ -860,35 +881,23 @@ def mnb_rope(q, k, positions, freqs, interleaved=False, gain=1.0, q_out=None, k_
     (2 i, 2 i + 1); freqs float64 radians per position (rope_frequencies).
     q_out, k_out: new tensors unless given; q and k themselves turn in place.
     Returns (q_out, k_out)."""
-    one = q if q is not None else k
+    one = k if q is None else q
     if one is None:
         raise ValueError("q or k must be given")
-    if not isinstance(one, torch.Tensor) or one.dim() != 3:
-        raise ValueError("q and k must be [T, heads, dim]")
-    dtype, device, index = one.dtype, one.device, one.get_device()
+    for x, out in ((q, q_out), (k, k_out)):
+        if x is not None and (not isinstance(x, torch.Tensor) or x.dim() != 3):
+            raise ValueError("q and k must be [T, heads, dim]")
+        if out is not None and not isinstance(out, torch.Tensor):
+            raise TypeError("q_out and k_out must be torch.Tensors")
+    dtype, index, pairs = one.dtype, one.get_device(), freqs.numel()
     code, (T, _, dim) = dtype_code(dtype), one.shape
-    args = []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            args += [None, 0, None, 0, 0]
-            continue
-        if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.shape[0] != T:
-            raise ValueError(f"{name} must be [{T}, heads, {dim}]")
-        if out is None:
-            out = torch.empty(x.shape, dtype=dtype, device=device)
-        elif not isinstance(out, torch.Tensor) or out.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape")
-        heads = x.shape[1]
-        args += [*_head_rows(x, name, heads, dim, dtype, index, device),
-                 *_head_rows(out, name + "_out", heads, dim, dtype, index, device), heads]
-        if name == "q":
-            q_out = out
-        else:
-            k_out = out
-    _launch("mnb_rope", index, *args, _whole(positions, "positions", torch.int32, T, index, device),
-            _whole(freqs, "freqs", torch.float64, freqs.numel(), index, device), T, dim, 2 * freqs.numel(),
+    device, nothing = one.device, (None, (None, 0, None, 0, 0))
+    q_out, of_q = nothing if q is None else _rope_rows(q, q_out, "q", T, dim, dtype, index, device)
+    k_out, of_k = nothing if k is None else _rope_rows(k, k_out, "k", T, dim, dtype, index, device)
+    _launch("mnb_rope", index, *of_q, *of_k, _whole(positions, "positions", torch.int32, T, index, device),
+            _whole(freqs, "freqs", torch.float64, pairs, index, device), T, dim, 2 * pairs,
             ROPE_INTERLEAVED if interleaved else ROPE_HALF, gain, code)
-    return (None if q is None else q_out), (None if k is None else k_out)
+    return q_out, k_out
 
 
 class KvCacheI8:
