@@ -49,31 +49,29 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     const int64_t b = blockIdx.y;
     const Cache8 &c = a.cache;
     const int begin = chunk * sp.chunk, step = kWaves * kKeys;
-    int key = begin + wave * kKeys - step;   // (the loop's first turn only requests)
-    // (no kernel writes the lengths while this one reads them: a scalar load)
-    typedef __attribute__((address_space(4))) const int32_t entry;
+    int key = begin + wave * kKeys;
+    // (everything that waits for nothing is requested first)
+    Tile tile(a, sp, b, lane, s_keys[wave], s_values[wave]);
+    tile.look_up(key);
     int64_t first;
-    const int len = ((entry *)a.lens)[b], n_new = rows_of(a, b, first);
+    const int n_new = rows_of(a, b, first);
     const int row0 = q_tile * kQ;
     int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group - row0;
     if (rows <= 0) return;
     if (rows > kQ) rows = kQ;
+    const int r = row0 + (col < rows ? col : 0), token = token_of(a, r);
+    QueryRow<T, D> row;
+    row.load(static_cast<const T *>(a.q) + (first + token) * a.q_stride +
+             ((int64_t)h * a.group + r - token * a.group) * D + g * 16);
+    // (no kernel writes the lengths while this one reads them: a scalar load)
+    typedef __attribute__((address_space(4))) const int32_t entry;
+    const int len = ((entry *)a.lens)[b];
     // keys that the tile's rows see: the last row most, the first least
     const int n = sees(a, len, n_new, token_of(a, row0 + rows - 1)), least = sees(a, len, n_new, token_of(a, row0));
     if (begin >= n && chunk > 0) return;
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;
-    const int r = row0 + (col < rows ? col : 0), token = token_of(a, r);
     const int mine = sees(a, len, n_new, token);
-
-    Tile tile(a, sp, b, lane, end, s_keys[wave], s_values[wave]);
-    tile.look_up(key + step);
-    // queries, in digits: lane (query col, pieces 4 j + g)
-    i32x4 q[kLoads][3];
-    float mul;
-    query_digits<T, D>(static_cast<const T *>(a.q) + (first + token) * a.q_stride +
-                           ((int64_t)h * a.group + r - token * a.group) * D + g * 16,
-                       a.scale, q, mul);
-    asm volatile("" : "+v"(tile.id));   // (the entries are there: no wait for them in the loop's first turn)
+    tile.end = end;
 
     const int8_t *keys = c.k + h * c.head_stride, *values = c.v + h * c.head_stride;
     const float *key_scales = c.k_scale + h * c.scale_head, *value_scales = c.v_scale + h * c.scale_head;
@@ -89,12 +87,29 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     for (int i = 0; i < kOut; ++i) o[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLowest, l = 0.0f;
     f4 ks[kParts], vs[kParts];
-    // (past the last tile loads of no bytes are requested: with a way around them the
-    // compiler counts none, and waits too long for those before)
-    do {
-        const bool real = key >= begin;   // (uniform)
+    // Requests a tile's keys (and the next one's table entries), its values.
+    uint32_t there;
+    auto request_keys = [&](int key0) {
+        tile.locate(key0);
+        load_scales(key_scales, ks);
+        tile.load_codes(keys, s_keys[wave]);
+        tile.look_up(key0 + step);
+        asm volatile("" ::: "memory");   // (in this order: the waits count them)
+    };
+    auto request_values = [&]() {
+        load_scales(value_scales, vs);
+        tile.load_codes(values, s_values[wave]);
+        there = tile.there;
+        asm volatile("" ::: "memory");
+    };
+    request_keys(key);
+    request_values();
+    i32x4 q[kLoads][3];   // in digits: lane (query col, pieces 4 j + g)
+    float mul;
+    row.digits(a.scale, q, mul);
+    for (; key < end; key += step) {
         float x[kParts][4];
-        if (real) {
+        {
             // (this tile's key codes are in LDS when all but its values' loads have come back)
             i32x4 kk[kParts][kLoads];
             tile.template read_keys<kBehind>(kk);
@@ -115,13 +130,10 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                 for (int i = 0; i < 4; ++i) x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * by[i];
             }
         }
-        const uint32_t there = tile.there;
-        tile.locate(key + step);
-        load_scales(key_scales, ks);
-        tile.load_codes(keys, s_keys[wave]);
-        tile.look_up(key + 2 * step);
-        asm volatile("" ::: "memory");   // (in this order: the waits count them)
-        if (real) {
+        // (past the last tile loads of no bytes are requested: with a way around them the
+        // compiler counts none, and waits too long for those before)
+        request_keys(key + step);
+        {
             if (key + kKeys > least || there != (1u << kParts) - 1)   // uniform: the end of a row, or a missing block
 #pragma unroll
                 for (int s = 0; s < kParts; ++s) {
@@ -188,11 +200,8 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                 }
             }
         }
-        load_scales(value_scales, vs);
-        tile.load_codes(values, s_values[wave]);
-        asm volatile("" ::: "memory");
-        key += step;
-    } while (key < end);
+        request_values();
+    }
 
     // (the tile past the end, no bytes, has arrived everywhere: its place is free)
     wait_loads<0>();

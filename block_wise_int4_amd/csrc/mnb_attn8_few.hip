@@ -15,7 +15,6 @@ namespace mnb {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kMost = 5;                     // rows
 constexpr int kColumns = 3 * kMost;
 constexpr int kScoreStride = kKeys + 4;      // of a column of products, in words: columns turned in the banks
@@ -43,7 +42,7 @@ __device__ __forceinline__ float wave_max(float x) {
 
 }  // namespace
 
-template <typename T, int D, bool STREAM, int R>
+template <typename T, int D, bool STREAM, int R, int kWaves>
 __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Split &sp) {
     using Tile = CodeTile<D, STREAM>;
     constexpr int kLoads = Tile::kLoads, kOut = D / 16;
@@ -60,46 +59,27 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
     const int64_t b = blockIdx.y;
     const Cache8 &c = a.cache;
     const int begin = chunk * sp.chunk, step = kWaves * kKeys;
-    int key = begin + wave * kKeys - step;   // (the loop's first turn only requests)
-    // (no kernel writes the lengths while this one reads them: a scalar load)
-    typedef __attribute__((address_space(4))) const int32_t entry;
+    int key = begin + wave * kKeys;
+    // (everything that waits for nothing is requested first)
+    Tile tile(a, sp, b, lane, s_keys[wave], s_values[wave]);
+    tile.look_up(key);
     int64_t first;
-    const int len = ((entry *)a.lens)[b], n_new = rows_of(a, b, first);
+    const int n_new = rows_of(a, b, first);
     const int rows = (n_new < a.max_new ? n_new : a.max_new) * a.group;   // <= R
     if (rows <= 0) return;
+    // this lane's column: row (the last one's for the columns behind), and its digit of it
+    const int mine = col / 3, digit = col - 3 * mine, r = mine < rows ? mine : rows - 1, token = token_of(a, r);
+    QueryRow<T, D> row;
+    row.load(static_cast<const T *>(a.q) + (first + token) * a.q_stride +
+             ((int64_t)h * a.group + r - token * a.group) * D + g * 16);
     // keys that the last row sees, most of all
+    // (no kernel writes the lengths while this one reads them: a scalar load)
+    typedef __attribute__((address_space(4))) const int32_t entry;
+    const int len = ((entry *)a.lens)[b];
     const int n = sees(a, len, n_new, token_of(a, rows - 1));
     if (begin >= n && chunk > 0) return;
     const int end = n - begin < sp.chunk ? n : begin + sp.chunk;
-
-    Tile tile(a, sp, b, lane, end, s_keys[wave], s_values[wave]);
-    tile.look_up(key + step);
-    // this lane's column: row (the last one's for the columns behind), and its digit of it
-    const int mine = col / 3, digit = col - 3 * mine, r = mine < rows ? mine : rows - 1;
-    i32x4 q[kLoads];
-    float mul[R];
-    int seen[R];   // keys that each row sees
-    {
-        const int token = token_of(a, r);
-        i32x4 all[kLoads][3];
-        float m;
-        query_digits<T, D>(static_cast<const T *>(a.q) + (first + token) * a.q_stride +
-                               ((int64_t)h * a.group + r - token * a.group) * D + g * 16,
-                           a.scale, all, m);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int d0 = all[j][0][k], d1 = all[j][1][k], d2 = all[j][2][k];
-                q[j][k] = digit == 0 ? d0 : digit == 1 ? d1 : d2;
-            }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            mul[i] = as_float((uint32_t)__builtin_amdgcn_readlane((int)as_bits(m), 3 * i));
-            seen[i] = i < rows ? sees(a, len, n_new, token_of(a, i)) : 0;
-        }
-    }
-    asm volatile("" : "+v"(tile.id));   // (the entries are there: no wait for them in the loop's first turn)
+    tile.end = end;
 
     const int8_t *keys = c.k + h * c.head_stride, *values = c.v + h * c.head_stride;
     const float *key_scales = c.k_scale + h * c.scale_head, *value_scales = c.v_scale + h * c.scale_head;
@@ -120,13 +100,47 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
         m[i] = kLowest;
         l[i] = 0.0f;
     }
-    float ks = 0.0f, vs = 0.0f;
-    // (past the last tile loads of no bytes are requested: with a way around them the
-    // compiler counts none, and waits too long for those before)
-    do {
-        const bool real = key >= begin;   // (uniform)
+    // Requests a tile's keys (and the next one's table entries), its values.
+    float ks, vs;
+    uint32_t there;
+    auto request_keys = [&](int key0) {
+        tile.locate(key0);
+        ks = load_scale(key_scales);
+        tile.load_codes(keys, s_keys[wave]);
+        tile.look_up(key0 + step);
+        asm volatile("" ::: "memory");   // (in this order: the waits count them)
+    };
+    auto request_values = [&]() {
+        vs = load_scale(value_scales);
+        tile.load_codes(values, s_values[wave]);
+        there = tile.there;
+        asm volatile("" ::: "memory");
+    };
+    request_keys(key);
+    request_values();
+    i32x4 q[kLoads];
+    float mul[R];
+    int seen[R];   // keys that each row sees
+    {
+        i32x4 all[kLoads][3];
+        float m;
+        row.digits(a.scale, all, m);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int d0 = all[j][0][k], d1 = all[j][1][k], d2 = all[j][2][k];
+                q[j][k] = digit == 0 ? d0 : digit == 1 ? d1 : d2;
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            mul[i] = as_float((uint32_t)__builtin_amdgcn_readlane((int)as_bits(m), 3 * i));
+            seen[i] = i < rows ? sees(a, len, n_new, token_of(a, i)) : 0;
+        }
+    }
+    for (; key < end; key += step) {
         float x[R];
-        if (real) {
+        {
             // (this tile's key codes are in LDS when all but its values' loads have come back)
             i32x4 kk[kParts][kLoads];
             tile.template read_keys<kBehind>(kk);
@@ -150,13 +164,10 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
                 x[i] = sum * (ks * mul[i]);
             }
         }
-        const uint32_t there = tile.there;
-        tile.locate(key + step);
-        ks = load_scale(key_scales);
-        tile.load_codes(keys, s_keys[wave]);
-        tile.look_up(key + 2 * step);
-        asm volatile("" ::: "memory");   // (in this order: the waits count them)
-        if (real) {
+        // (past the last tile loads of no bytes are requested: with a way around them the
+        // compiler counts none, and waits too long for those before)
+        request_keys(key + step);
+        {
             const int at = there >> g & 1 ? key + lane : 0x7FFFFFFF;
             float up[R], down[R], keep[R];
             uint32_t w[R];
@@ -208,11 +219,8 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
                 }
             }
         }
-        vs = load_scale(value_scales);
-        tile.load_codes(values, s_values[wave]);
-        asm volatile("" ::: "memory");
-        key += step;
-    } while (key < end);
+        request_values();
+    }
 
     // (the tile past the end, no bytes, has arrived everywhere: its place is free)
     wait_loads<0>();
@@ -267,23 +275,27 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
     }
 }
 
-template <typename T, int D, bool STREAM, int R>
-__global__ __launch_bounds__(64 * kWaves, D == 128 ? 2 : 3) void attn8_few_kernel(Attn8Args a, Attn8Split sp) {
-    few_workgroup<T, D, STREAM, R>(a, sp);
+template <typename T, int D, bool STREAM, int R, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 1 : D == 128 ? 2 : 3) void attn8_few_kernel(Attn8Args a, Attn8Split sp) {
+    few_workgroup<T, D, STREAM, R, W>(a, sp);
 }
 
 namespace {
 
-template <typename T, int D, bool STREAM> void launch_rows(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
+template <typename T, int D, bool STREAM, int W> void launch_rows(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
     const dim3 grid(a.cache.heads, a.batch, (unsigned)sp.chunks);
-    if (sp.rows == 1) attn8_few_kernel<T, D, STREAM, 1><<<grid, 64 * kWaves, 0, st>>>(a, sp);
-    else if (sp.rows == 2) attn8_few_kernel<T, D, STREAM, 2><<<grid, 64 * kWaves, 0, st>>>(a, sp);
-    else attn8_few_kernel<T, D, STREAM, kMost><<<grid, 64 * kWaves, 0, st>>>(a, sp);
+    if (sp.rows == 1) attn8_few_kernel<T, D, STREAM, 1, W><<<grid, 64 * W, 0, st>>>(a, sp);
+    else if (sp.rows == 2) attn8_few_kernel<T, D, STREAM, 2, W><<<grid, 64 * W, 0, st>>>(a, sp);
+    else attn8_few_kernel<T, D, STREAM, kMost, W><<<grid, 64 * W, 0, st>>>(a, sp);
 }
 
 template <typename T, int D> void launch(const Attn8Args &a, const Attn8Split &sp, bool stream, hipStream_t st) {
-    if (stream) launch_rows<T, D, true>(a, sp, st);
-    else launch_rows<T, D, false>(a, sp, st);
+    // Eight waves where a workgroup has its CU alone, and more than two tiles for each of
+    // four: 16 x 5..1503 keys, 12 float32 heads of 64, 9.6 us, 11.0 with four (32 x 62..2001,
+    // 16 heads of 128 over 8, 17.5 and 17.9; but 1 x 452 8.9 and 8.6).
+    const bool eight = (int64_t)a.cache.heads * a.batch * sp.chunks <= 256 && sp.chunk > 512 && a.max_len > 512;
+    if (eight) stream ? launch_rows<T, D, true, 8>(a, sp, st) : launch_rows<T, D, false, 8>(a, sp, st);
+    else stream ? launch_rows<T, D, true, 4>(a, sp, st) : launch_rows<T, D, false, 4>(a, sp, st);
 }
 
 }  // namespace

@@ -53,59 +53,65 @@ __device__ __forceinline__ void digits_of(const uint32_t *w, uint32_t *digit) {
     digit[2] = b01 | b23;
 }
 
-// A query row in three digits: lane (any column, g = lane / 16) takes 16 dimensions of each
-// 64 from src on, which is the row's 16 g. digit[j][t]: digit t, least significant
-// first, of piece j's numbers n = x 2^(21 - e), |n| < 2^22, 2^e the largest element's
-// power of two. mul: of a sum of products with n, to a score without the key's scale;
-// NaN (and digits of zeros) for a row that is not finite.
-template <typename T, int D>
-__device__ __forceinline__ void query_digits(const T *src, float scale, i32x4 (*digit)[3], float &mul) {
-    constexpr int kLoads = D / 64;
-    float x[kLoads][16];
-    uint32_t top = 0;
+// A query row: lane (any column, g = lane / 16) takes 16 dimensions of each 64 from src on,
+// which is the row's 16 g.
+template <typename T, int D> struct QueryRow {
+    static constexpr int kLoads = D / 64, kEach = 16 / (int)sizeof(T);
+    u32x4 w[kLoads][sizeof(T)];
+
+    __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
+        for (int j = 0; j < kLoads; ++j)
 #pragma unroll
-        for (int p = 0; p < (int)sizeof(T); ++p) {
-            const u32x4 w = reinterpret_cast<const u32x4 *>(src + 64 * j)[p];
+            for (int p = 0; p < (int)sizeof(T); ++p) w[j][p] = reinterpret_cast<const u32x4 *>(src + 64 * j)[p];
+    }
+    __device__ __forceinline__ float at(int j, int i) const {
+        const u32x4 x = w[j][i / kEach];
+        if constexpr (sizeof(T) == 2) return (float)__builtin_bit_cast(h8, x)[i % kEach];
+        else return __builtin_bit_cast(f4, x)[i % kEach];
+    }
+    // In three digits: digit[j][t] is digit t, least significant first, of piece j's numbers
+    // n = x 2^(21 - e), |n| < 2^22, 2^e the largest element's power of two. mul: of a sum of
+    // products with n, to a score without the key's scale; NaN (and digits of zeros)
+    // for a row that is not finite.
+    __device__ __forceinline__ void digits(float scale, i32x4 (*digit)[3], float &mul) const {
+        uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
-                float v;
-                if constexpr (sizeof(T) == 2) v = (float)__builtin_bit_cast(h8, w)[i];
-                else v = __builtin_bit_cast(f4, w)[i];
-                x[j][p * (16 / (int)sizeof(T)) + i] = v;
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
                 // (as whole numbers: infinities and NaN are above every finite one)
-                const uint32_t bits = as_bits(v) & 0x7FFFFFFFu;
+                const uint32_t bits = as_bits(at(j, i)) & 0x7FFFFFFFu;
                 top = bits > top ? bits : top;
             }
-        }
-    top = column_max(top);
-    const bool finite = top < 0x7F800000u;
-    // (the smallest rows 2^64 times as large)
-    const bool small = top < (64u << 23);
-    const float lift = small ? 0x1p64f : 1.0f;
-    if (small) top = as_bits(as_float(top) * 0x1p64f);
-    const int e = top ? (int)(top >> 23) : 127;
-    const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
-    mul = finite ? __builtin_ldexpf(scale, e - 127 - 21 - (small ? 64 : 0)) : __builtin_nanf("");
+        top = column_max(top);
+        const bool finite = top < 0x7F800000u;
+        // (the smallest rows 2^64 times as large)
+        const bool small = top < (64u << 23);
+        const float lift = small ? 0x1p64f : 1.0f;
+        if (small) top = as_bits(as_float(top) * 0x1p64f);
+        const int e = top ? (int)(top >> 23) : 127;
+        const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
+        mul = finite ? __builtin_ldexpf(scale, e - 127 - 21 - (small ? 64 : 0)) : __builtin_nanf("");
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
+        for (int j = 0; j < kLoads; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t w[4], d[3];
+            for (int k = 0; k < 4; ++k) {
+                uint32_t n[4], d[3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // (one that would round to 2^22 stays one below; n as the bits of
-                // 2^23 + 2^22 + n less those of n = 0)
-                const float v = finite ? x[j][4 * k + i] * lift * up : 0.0f;
-                w[i] = as_bits(__builtin_amdgcn_fmed3f(v, -4194303.0f, 4194303.0f) + 12582912.0f) +
-                       (0x8080u - 0x4B400000u);
+                for (int i = 0; i < 4; ++i) {
+                    // (one that would round to 2^22 stays one below; n as the bits of
+                    // 2^23 + 2^22 + n less those of n = 0)
+                    const float v = finite ? at(j, 4 * k + i) * lift * up : 0.0f;
+                    n[i] = as_bits(__builtin_amdgcn_fmed3f(v, -4194303.0f, 4194303.0f) + 12582912.0f) +
+                           (0x8080u - 0x4B400000u);
+                }
+                digits_of(n, d);
+#pragma unroll
+                for (int t = 0; t < 3; ++t) digit[j][t][k] = (int)d[t];
             }
-            digits_of(w, d);
-#pragma unroll
-            for (int t = 0; t < 3; ++t) digit[j][t][k] = (int)d[t];
-        }
-}
+    }
+};
 
 // Weights times value scales as numbers below 2^22: times `up`, 2^(21 - exponent of the
 // largest) a touch less so that none rounds up to 2^22, plus 2^23 + 0x8080, whose bytes
@@ -129,7 +135,8 @@ template <int D, bool STREAM> struct CodeTile {
 
     const Cache8 &c;
     const int32_t *table;
-    const int table_width, lane, end;
+    const int table_width, lane;
+    int end;                 // of the keys that any row sees (set before the first tile is located)
     const uint32_t magic, stride;
     uint8_t *s_keys, *s_values;
     // Lanes 16 s on look after part s: its table entry, then where it is, as bytes to its
@@ -143,9 +150,9 @@ template <int D, bool STREAM> struct CodeTile {
     uint32_t bytes, there;   // (there: a bit for each part)
     uint32_t at[2][kLoads];  // of a load's pieces, in even and odd parts
 
-    __device__ __forceinline__ CodeTile(const Attn8Args &a, const Attn8Split &sp, int64_t b, int lane, int end,
+    __device__ __forceinline__ CodeTile(const Attn8Args &a, const Attn8Split &sp, int64_t b, int lane,
                                         uint8_t *s_keys, uint8_t *s_values)
-        : c(a.cache), table(a.table + b * a.table_width), table_width(a.table_width), lane(lane), end(end),
+        : c(a.cache), table(a.table + b * a.table_width), table_width(a.table_width), lane(lane), end(0),
           magic(sp.page_magic), stride((uint32_t)a.cache.token_stride), s_keys(s_keys), s_values(s_values), id(0),
           from(0), from_scales(0), bytes(0), there(0) {
         constexpr int kRows = 64 / kPieces;   // of a load: whole rows, 64 lanes on 1 KB after another
