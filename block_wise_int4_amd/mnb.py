@@ -784,19 +784,22 @@ def mnb_cross_attn(q, k, v, lens=None, scale=None, workspace=None, out=None):
     return out
 
 
-def _launch(fn, index, *args):
-    """Calls entry point `fn` on torch's current stream of device `index`, with
-    that device current (the null stream is the current device's)."""
+def _elsewhere(fn, index):
+    """Entry point `fn` with device `index` current while it runs (its launches go
+    there, and the null stream is the current device's)."""
+    def call(*args):
+        with torch.cuda.device(index):
+            return getattr(lib(), fn)(*args)
+    return call
+
+
+def _entry(fn, index):
+    """Entry point `fn` for tensors on device `index`, and torch's current stream
+    there."""
     if index < 0:
         raise ValueError("the tensors must be on the GPU")
-    call = getattr(lib(), fn)
-    if torch._C._cuda_getDevice() == index:
-        status = call(*args, _stream_handle(index))
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, _stream_handle(index))
-    if status:
-        _check(fn, status)
+    here = torch._C._cuda_getDevice() == index
+    return getattr(lib(), fn) if here else _elsewhere(fn, index), torch._C._cuda_getCurrentRawStream(index)
 
 
 def _head_rows(t, name, heads, dim, dtype, index, device):
@@ -894,9 +897,13 @@ def mnb_rope(q, k, positions, freqs, interleaved=False, gain=1.0, q_out=None, k_
     device, nothing = one.device, (None, (None, 0, None, 0, 0))
     q_out, of_q = nothing if q is None else _rope_rows(q, q_out, "q", T, dim, dtype, index, device)
     k_out, of_k = nothing if k is None else _rope_rows(k, k_out, "k", T, dim, dtype, index, device)
-    _launch("mnb_rope", index, *of_q, *of_k, _whole(positions, "positions", torch.int32, T, index, device),
-            _whole(freqs, "freqs", torch.float64, pairs, index, device), T, dim, 2 * pairs,
-            ROPE_INTERLEAVED if interleaved else ROPE_HALF, gain, code)
+    at, of = (_whole(positions, "positions", torch.int32, T, index, device),
+              _whole(freqs, "freqs", torch.float64, pairs, index, device))
+    call, stream = _entry("mnb_rope", index)
+    status = call(*of_q, *of_k, at, of, T, dim, 2 * pairs, ROPE_INTERLEAVED if interleaved else ROPE_HALF, gain, code,
+                  stream)
+    if status:
+        _check("mnb_rope", status)
     return q_out, k_out
 
 
@@ -945,8 +952,11 @@ def mnb_kv_append_i8(k, v, slots, cache):
     outside the cache are skipped)."""
     T, device, index = slots.numel(), cache.device, cache.index
     k_stride, v_stride = _tokens(k, "k", T, cache), _tokens(v, "v", T, cache)
-    _launch("mnb_kv_append_i8", index, k.data_ptr(), v.data_ptr(), k_stride, v_stride,
-            _whole(slots, "slots", torch.int64, T, index, device), T, cache.ref)
+    at = _whole(slots, "slots", torch.int64, T, index, device)
+    call, stream = _entry("mnb_kv_append_i8", index)
+    status = call(k.data_ptr(), v.data_ptr(), k_stride, v_stride, at, T, cache.ref, stream)
+    if status:
+        _check("mnb_kv_append_i8", status)
 
 
 def mnb_kv_read_i8(slots, cache, k=None, v=None):
@@ -959,8 +969,11 @@ def mnb_kv_read_i8(slots, cache, k=None, v=None):
     if v is None:
         v = torch.empty((T, *cache.token_shape), dtype=cache.dtype, device=device)
     k_stride, v_stride = _tokens(k, "k", T, cache), _tokens(v, "v", T, cache)
-    _launch("mnb_kv_read_i8", index, _whole(slots, "slots", torch.int64, T, index, device), T, cache.ref, k.data_ptr(),
-            v.data_ptr(), k_stride, v_stride)
+    at = _whole(slots, "slots", torch.int64, T, index, device)
+    call, stream = _entry("mnb_kv_read_i8", index)
+    status = call(at, T, cache.ref, k.data_ptr(), v.data_ptr(), k_stride, v_stride, stream)
+    if status:
+        _check("mnb_kv_read_i8", status)
     return k, v
 
 
@@ -988,7 +1001,7 @@ def mnb_paged_attn_i8(q, cache, block_table, lens, max_len, starts=None, max_new
     most max_new, are the last of request b's lens[b] positions, and each sees
     the positions up to its own. scale: 1 / sqrt(head_dim) unless given.
     Returns out [T, heads, head_dim]; rows of no request stay as they were."""
-    device, index, dtype = cache.device, cache.index, cache.dtype
+    device, index, dtype, i32 = cache.device, cache.index, cache.dtype, torch.int32
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError(f"q must be [T, heads, {cache.head_dim}] with contiguous heads")
     if block_table.dim() != 2:
@@ -996,16 +1009,22 @@ def mnb_paged_attn_i8(q, cache, block_table, lens, max_len, starts=None, max_new
     T, heads, dim = q.shape
     B, width = block_table.shape
     q_ptr, q_stride = _head_rows(q, "q", heads, cache.head_dim, dtype, index, device)
-    if starts is None and T != B:
+    first = None
+    if starts is not None:
+        first = _whole(starts, "starts", i32, B + 1, index, device)
+    elif T != B:
         raise ValueError(f"q has {T} tokens for {B} requests: starts says whose they are")
     if out is None:
         out = torch.empty((T, heads, dim), dtype=dtype, device=device)
     if workspace is None:
         workspace = paged_attn_i8_workspace(q, cache, block_table, max_len, max_new)
-    _launch("mnb_paged_attn_i8", index, q_ptr, q_stride, cache.ref,
-            _whole(block_table, "block_table", torch.int32, B * width, index, device),
-            _whole(lens, "lens", torch.int32, B, index, device),
-            None if starts is None else _whole(starts, "starts", torch.int32, B + 1, index, device), T, B, heads,
-            width, max_len, max_new, dim ** -0.5 if scale is None else scale, *_workspace(workspace, index, device),
-            _whole(out, "out", dtype, T * heads * dim, index, device))
+    table, length, to = (_whole(block_table, "block_table", i32, B * width, index, device),
+                         _whole(lens, "lens", i32, B, index, device),
+                         _whole(out, "out", dtype, T * heads * dim, index, device))
+    work, work_bytes = _workspace(workspace, index, device)
+    call, stream = _entry("mnb_paged_attn_i8", index)
+    status = call(q_ptr, q_stride, cache.ref, table, length, first, T, B, heads, width, max_len, max_new,
+                  dim ** -0.5 if scale is None else scale, work, work_bytes, to, stream)
+    if status:
+        _check("mnb_paged_attn_i8", status)
     return out
