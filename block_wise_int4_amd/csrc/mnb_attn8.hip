@@ -22,7 +22,14 @@
 // The next tile's key codes are requested as soon as this one's are in registers,
 // its value codes after the second product's reads.
 // The waves' sums are joined in LDS, and the chunks' by a second launch.
+//
+// Bound by the latency of a tile's steps (two products, their exchange and the softmax
+// between) where workgroups are few, by the vector unit and the codes' way through LDS where
+// they are many: 16 rows over 32 x 1000 keys of 8 heads of 128 16.8 us, 4.0 TB/s of codes
+// and scales, 8 rows over 32 x 8000 112 us, 4.8 TB/s (a stream of reads reaches 6.8).
 #include "mnb_attn8_tiles.h"
+
+#include <algorithm>
 
 namespace mnb {
 
@@ -314,13 +321,29 @@ struct Plan {
     bool many;
 };
 
-// Which kernel, and how a call is cut into workgroups over `chunk` keys. Few rows: a
-// row of up to kWholeBytes of codes is one workgroup, and the call one launch (up
-// to kFullBytes from kFullUnits rows on); then kMany workgroups of kLeast keys or
-// more, and at least kFew of them. Many rows: kManyWgs workgroups, of kManyKeys
-// keys or more.
-constexpr int64_t kWholeBytes = 512 << 10, kFullBytes = 1 << 20, kMany = 4096, kLeast = 512, kFew = 256,
-                  kFullUnits = 192, kManyWgs = 512, kManyKeys = 256, kManyRows = 33;
+// Which kernel, and how a call is cut into workgroups over `chunk` keys. Figures are us
+// a call, replayed from a graph; 8 heads of 128 are shared by 16, 8 of 64 by 32.
+//
+// Few rows: a row of up to kWholeBytes of codes is one workgroup, and the call one launch
+// (one request of 2000 keys and 8 x 64: 10.1; whole 15.7; 452 keys and 8 x 128 whole 8.6,
+// in pieces 10). From kFullUnits rows of tiles on, which fill the card by themselves, that
+// goes up to kFullBytes (float32, 16 x 1500 keys, 12 x 64: 9.5, in pieces 11.3; but with
+// 128 rows of tiles, 16 x 3000, 8 x 64, 15.9 in pieces and 20.9 whole; and past 1 MB, 24 x
+// 16000, 12 x 64, 77 in pieces and 98 whole). Longer rows: kMany workgroups (16 x 16000, 8 x
+// 128: 73, with 4096 80; with 1024 the same 0.1% over 372 calls, 20% worse at the worst) of
+// kLeast keys or more (512 1% slower over those calls, 16 x 3000 22.7 for 18.2; 1024 0.3%),
+// and at least kFew of them (1 x 6000 9.8, with 128 11.1; 1 x 16000 with 512 13.1 for 11.8).
+//
+// Many rows: from kManyRows on, three tiles of this file's kernel, which the other form
+// takes as one: 40 rows and 64 x 300 keys 22 and 34, 8 x 8000 53 and 61; below, 32 rows and
+// 32 x 1000 33 and 22. (Calls of few workgroups go on losing by it up to some 100 rows: 8 x
+// 500 keys, 64 rows, 15.6 and 12.6.) kManyWgs workgroups of kManyKeys keys or more (8 x
+// 8000 keys, 124 rows: 56, with 256 68), and where those are too few kFullWgs of
+// kLeastKeys or more (1 x 2000, 124 rows: 15.0, in pieces of 256 17.2; 1 x 410 new 14.6
+// and 16.8).
+constexpr int64_t kWholeBytes = 128 << 10, kFullBytes = 1 << 20, kMany = 2048, kLeast = 768, kFew = 256,
+                  kFullUnits = 192, kManyWgs = 512, kManyKeys = 256, kFullWgs = 256, kLeastKeys = 128,
+                  kManyRows = 33;
 Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.rows = max_new * group;
@@ -334,7 +357,7 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64
     const double all = (double)units * (double)keys;
     if (p.many) {
         if (all / kManyWgs < (double)keys) chunk = (int64_t)(all / kManyWgs);
-        if (chunk < kManyKeys) chunk = kManyKeys;
+        if (chunk < kManyKeys) chunk = std::max((int64_t)(all / kFullWgs), kLeastKeys);
     } else if (max_len > (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim)) {
         chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
         if (chunk < kLeast) chunk = kLeast;
@@ -356,7 +379,8 @@ template <typename T, int D> void launch_some(const Attn8Args &a, const Attn8Spl
 template <typename T, int D, bool LOG2> void launch_join(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
     const int64_t rows = (a.tokens < a.max_new ? a.tokens : a.max_new) * a.group;
     // a group of lanes per chunk of the row, as far as a workgroup goes and rows do not
-    // fill the card by themselves
+    // fill the card by themselves (a call over 1 x 32000 keys 16.3 us, by one group a row
+    // 22.6; 8 x 62 rows after up to 2000 keys 30.5, by a group per chunk 32.5)
     const int64_t lanes = (int64_t)a.batch * a.cache.heads * rows * (D / 4);
     int shift = 0;
     while ((1 << shift) < sp.chunks && (D / 4) << shift < kJoin && lanes << shift < kJoinLanes) ++shift;
@@ -373,7 +397,8 @@ template <typename T, int D> hipError_t launch(const Attn8Args &a, const Attn8Sp
             return hipGetLastError();
         }
     }
-    // Codes that the L2 (32 MB in all) cannot hold are read past it.
+    // Codes that the L2 (32 MB in all) cannot hold are read past it: 32 x 1000 keys, 66 MB,
+    // 12.5 us and 14.7 without, 1 GB 132 and 148 (33 MB 8.4 and 8.2).
     const bool stream = sp.q_tiles == 1 && 2.0 * a.batch * a.cache.heads * a.max_len * D > 32e6;
     if (sp.rows <= kFewRows) {
         if (hipError_t e = launch_attn8_few(a, sp, D, sizeof(T) == 2 ? 1 : 0, stream, st)) return e;
