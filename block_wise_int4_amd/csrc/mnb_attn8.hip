@@ -340,7 +340,7 @@ struct Plan {
 // 500 keys, 64 rows, 15.6 and 12.6.) kManyWgs workgroups of kManyKeys keys or more (8 x
 // 8000 keys, 124 rows: 56, with 256 68), and where those are too few kFullWgs of
 // kLeastKeys or more (1 x 2000, 124 rows: 15.0, in pieces of 256 17.2; 1 x 410 new 14.6
-// and 16.8).
+// and 16.8); up to kManyKeys keys are one piece (2 x 200 new 12.6, in two 13.3).
 constexpr int64_t kWholeBytes = 128 << 10, kFullBytes = 1 << 20, kMany = 2048, kLeast = 768, kFew = 256,
                   kFullUnits = 192, kManyWgs = 512, kManyKeys = 256, kFullWgs = 256, kLeastKeys = 128,
                   kManyRows = 33;
@@ -357,7 +357,7 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64
     const double all = (double)units * (double)keys;
     if (p.many) {
         if (all / kManyWgs < (double)keys) chunk = (int64_t)(all / kManyWgs);
-        if (chunk < kManyKeys) chunk = std::max((int64_t)(all / kFullWgs), kLeastKeys);
+        if (chunk < kManyKeys && keys > kManyKeys) chunk = std::max((int64_t)(all / kFullWgs), kLeastKeys);
     } else if (max_len > (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim)) {
         chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
         if (chunk < kLeast) chunk = kLeast;

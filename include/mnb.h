@@ -567,7 +567,8 @@ int mnb_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
  * bytes of a decoding step's attention. Each row (one token's keys, or
  * values, of one head: head_dim numbers) is stored as int8 codes c and one
  * float32 scale s, and stands for c * s:
- *   s = amax / 127, rounded to float32 (amax the row's largest |x|),
+ *   s = amax / 127, rounded to float32 (amax the row's largest |x|; at most
+ *       0x1.020406p+121, of which 127 times are still finite),
  *   c = x / s rounded to the nearest whole number (the exact quotient, ties to
  *       even), within -127 .. 127; 0 where s is 0.
  * A scale of its own for every token and head: what is stored does not depend
@@ -637,9 +638,16 @@ int mnb_kv_read_i8(const int64_t *slots, int64_t T, const mnb_kv_cache_i8 *cache
  * mnb_paged_attn's; the workspace's size is that of a call of exactly this B,
  * max_len and max_new.
  *
- * Scores, softmax statistics and sums over keys are float32. A query row that
- * holds an infinity or a NaN gives NaN (zeros if it sees nothing), and so does
- * a key or value row of scale NaN to every row that sees it.
+ * Scores, softmax statistics and sums over keys are float32. Queries count as
+ * 22-bit numbers against their row's largest, weights times value scales as
+ * 22-bit numbers against the largest of 64 keys. float16 calls of 33 query rows
+ * and more a key-value head (max_new * Hq / Hkv) round weights times value
+ * scales to float16 instead, 11 bits, as the output is; weights below 2^-32 of
+ * a row's largest may count as zeros there. float16: |scale| above 2^80 counts
+ * as 2^80, by where the softmax of float16 queries has one key left or equal
+ * ones. A query row that holds an infinity or a NaN gives NaN (zeros if it sees
+ * nothing), and so does a key or value row of scale NaN to every row that sees
+ * it.
  */
 size_t mnb_paged_attn_i8_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t max_len,
                                          int64_t max_new, int dtype);
