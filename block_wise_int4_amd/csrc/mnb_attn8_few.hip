@@ -9,6 +9,13 @@
 //   softmax        a key a lane; maxima over the wave by lane permutes
 //   O^T = CV^T P^T the weights' digits go through LDS to become the columns 3 r + t again,
 //                  whose sums stay apart until the end.
+//
+// Long rows are bound by memory: 2 rows, 32 x 500..16384 keys of 8 heads of 128, 571 MB in
+// 93..105 us, 5.4..6.1 TB/s (16 x 16 tiles of the other kernel took 116; a stream of reads
+// reaches 6.8). One request of 452 keys takes 7.7 us, of one key 6.6: a launch, the chain
+// of length, table, codes and scales, two products and the waves' join. Against that form
+// (us replayed from a graph): 1 row, 8 x 1500 keys, 11.3 and 18.1; 2 rows 12.3 and 18.1; 5
+// rows 16.1 and 18.2, 1 x 500 10.1 and 9.4, 32 x 12000 121 and 120.
 #include "mnb_attn8_tiles.h"
 
 namespace mnb {
