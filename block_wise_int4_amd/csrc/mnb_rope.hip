@@ -33,8 +33,8 @@ template <typename T> __device__ __forceinline__ T rounded(float x) {
 
 // A wave takes one token: its lanes work out the pairs' cosines and sines into
 // LDS, then turn the heads, a unit a lane, kAhead units under way (9999 float32 tokens of
-// 24 x 128, interleaved, 246 MB: 50 us, 4.9 TB/s, what a copy reaches; with one unit 60; 8
-// float16 tokens 3.6, a launch). VEC: 16-byte pieces
+// 24 x 128, interleaved, 246 MB: 50..55 us, 4.5..4.9 TB/s, what a copy reaches; as called 55,
+// with one unit 64; 8 float16 tokens 3.6, a launch). VEC: 16-byte pieces
 // (or, in the half layout, two of them, one from each half); otherwise a unit is one
 // pair, or one element behind them.
 template <typename T, bool INTERLEAVED, bool VEC>

@@ -88,8 +88,9 @@ class Decoder:
 
     def prompt(self, x, added):
         """Keys and values of prompts, x [sum(added), width]. Attention among a
-        prompt's rows is not among the operators: every layer is given the
-        embeddings x, where a model would give it the layer before's output."""
+        prompt's rows is not among the operators over this cache (it is over the
+        one in 8 bits, mnb_paged_attn_i8): every layer is given the embeddings x,
+        where a model would give it the layer before's output."""
         slots = self.place(added)
         for layer in self.layers:
             layer.append(x, slots)
