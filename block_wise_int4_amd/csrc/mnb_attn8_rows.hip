@@ -13,11 +13,15 @@
 //                 index is renumbered to the keys a lane holds, and CV^T comes out
 //                 of LDS through the transposing 8-byte reads.
 // Weights are held against a reference 2^7 below the running maximum, which moves
-// when a score passes that maximum by more than 2^8; times value scales against the
-// largest's power of two so far, they are rounded to float16 (11 bits: as the
-// output is). Their sum, the denominator, is float32.
+// when a score passes that maximum by more than 2^8; a score less its reference is one
+// multiply-add. That rounds, and equal scores of different steps do not round alike: below
+// kFar 2^-10 of a weight at most, about what float16 takes anyway. A wave whose scores may
+// be larger (by its queries' largest element and the step's key scales) goes on with
+// scores rounded first and the maximum itself taken off them, which is exact.
+// Weights times value scales, against the largest's power of two so far, are rounded to
+// float16 (11 bits: as the output is). Their sum, the denominator, is float32.
 //
-// 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 24 us: 4.4 GFLOP, 39 MB. Half of
+// 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 25 us: 4.4 GFLOP, 39 MB. Half of
 // that is the loop, bound by vector instructions (400 a wave and step, exponentials counted
 // as four, against 1024 cycles of matrix products), 13 steps in the fullest CU where the
 // mean is 6; a launch and a step take 8. 8 x 62 rows after up to 2000 keys take 22 and
@@ -34,6 +38,7 @@ namespace {
 
 constexpr int kKeys = 64;     // of a step: four 16-key parts
 constexpr float kLift = 7.0f, kSlack = 8.0f + kLift;
+constexpr float kFar = 16384.0f;
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -62,6 +67,23 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t *to) {
 __device__ __forceinline__ float halves_max(float x) {
     const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(x), as_bits(x), false, false));
     return fmaxf(as_float(r.x), as_float(r.y));
+}
+
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ us2 as_us2(uint32_t x) { return __builtin_bit_cast(us2, x); }
+
+// The largest of a wave's, whose halves have the same.
+template <int N> __device__ __forceinline__ float turned(float x) {   // by N of 16 lanes
+    const int b = __builtin_bit_cast(int, x);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, 0x120 + N, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_max(float x) {
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(as_bits(x), as_bits(x), false, false));
+    x = fmaxf(as_float(r.x), as_float(r.y));
+    x = fmaxf(x, turned<8>(x));
+    x = fmaxf(x, turned<4>(x));
+    x = fmaxf(x, turned<2>(x));
+    return fmaxf(x, turned<1>(x));
 }
 
 }  // namespace
@@ -207,28 +229,28 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     // The reference of this lane's row (once a key is seen), the sum of weights
     // exp2(score - ref), of this lane's keys; biased exponent of the value scales' unit.
     float ref = 0.0f, l = 0.0f;
-    bool started = false;
+    bool started = false, far = false;   // far, of the wave: ref is the running maximum itself
     int unit = 1;
     fetch(begin);
     look_up(begin + kKeys);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the compiler does not count loads to LDS)
-    uint32_t top = 0;
+    us2 tops = {0, 0};   // largest |q|, as whole numbers: infinities and NaN are above every finite one
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
         q[j] = *reinterpret_cast<const h8 *>(in_rows(col, 2 * j + half));
         const u32x4 x = __builtin_bit_cast(u32x4, q[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
-            top = lo > top ? lo : top;
-            top = hi > top ? hi : top;
-        }
+        for (int e = 0; e < 4; ++e) tops = __builtin_elementwise_max(tops, as_us2(x[e] & 0x7FFF7FFFu));
     }
+    uint32_t top = tops.x > tops.y ? tops.x : tops.y;
     const u32x2 both = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(top, top, false, false));
-    finite = both.x < 0x7C00u && both.y < 0x7C00u;
+    top = both.x > both.y ? both.x : both.y;
+    finite = top < 0x7C00u;
     if (!finite)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) q[j] = h8{};
+    // what no product of codes with one of the wave's queries passes
+    const float most_product = 128.0f * D * wave_max((float)as_h2(finite ? top : 0u).x);
     __syncthreads();   // (the tiles' place is free)
     put(0);
     valid = valid_next;
@@ -266,13 +288,18 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         // scores less the reference, plus the unit's power of two: its inverse, 2^(126 -
         // unit), then comes with the weights and leaves value scales below one
         float shift = (float)(126 - unit);
+        if (!far && __any(fabsf(s_ks[buf][lane]) * most_product >= kFar)) {
+            far = true;
+            if (started) ref += kLift;
+        }
+        const float from = far ? 0.0f : shift - ref;   // (a product plus zero is rounded alone)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f4 ks = *reinterpret_cast<const f4 *>(s_ks[buf] + 32 * t + 8 * j + 4 * half);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][4 * j + e] = __builtin_fmaf(s[t][4 * j + e], ks[e], shift - ref);
+                for (int e = 0; e < 4; ++e) s[t][4 * j + e] = __builtin_fmaf(s[t][4 * j + e], ks[e], from);
             }
         if (valid != ~0ull || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
 #pragma unroll
@@ -291,10 +318,11 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         float top = s[0][0];
 #pragma unroll
         for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
-        if (__any(top > (started ? shift + kSlack : -__builtin_inff())) || most > unit) {
+        if (far || __any(top > (started ? shift + kSlack : -__builtin_inff())) || most > unit) {
             top = halves_max(top);
             const bool some = top > -__builtin_inff();
-            float by = top - shift - kLift;   // how far the reference moves
+            // how far the reference moves
+            float by = far ? top - ref : top - shift - kLift;
             by = started ? fmaxf(by, 0.0f) : some ? by : 0.0f;
             const int raised = most > unit ? most : unit, less = unit - raised + 127;
             const float keep = started ? __builtin_amdgcn_exp2f(-by) : 1.0f;   // (nothing to keep at the start)
@@ -304,12 +332,13 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[d][e] *= keep_sums;
+            ref = !far ? ref + by : !some ? ref : started ? fmaxf(ref, top) : top;
             started |= some;
-            ref += by;
-            by += (float)(raised - unit);
+            const float less_by = far ? ref : by + (float)(raised - unit);
             unit = raised;
+            const float more = far ? (float)(126 - unit) + kLift : 0.0f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] -= by;
+            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] = (s[e / 16][e % 16] - less_by) + more;
         }
         u32x4 p[2][2];
         float sum[2] = {0.0f, 0.0f};
@@ -379,6 +408,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         return;
     }
     // a piece: the sums in two halves of D / 2 dimensions, 4 bytes each
+    const float lower = far ? 0x1p-7f : 1.0f, by = back * lower;   // (kLift: against ref itself)
     float *sums = sp.sums + (((b * c.heads + h) * sp.rows + row0 + wave * 32) * sp.chunks + chunk) * D;
 #pragma unroll
     for (int d0 = 0; d0 < D / 32; d0 += D / 64) {
@@ -387,7 +417,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
-                    f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
+                    f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * by;
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
@@ -399,7 +429,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     if (on && half == 0) {
         float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
         stats[0] = started ? ref : kLowest;
-        stats[1] = l;
+        stats[1] = l * lower;
     }
 }
 

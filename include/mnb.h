@@ -574,7 +574,8 @@ int mnb_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
  * A scale of its own for every token and head: what is stored does not depend
  * on how tokens are cut into calls, and no row is ever rounded twice. A row
  * that holds an infinity or a NaN is stored as codes 0 with the scale NaN: it
- * stands for NaN throughout.
+ * stands for NaN throughout. Scales that a caller writes itself are zero or
+ * positive.
  *
  * Pages, slots, tables and lengths are those of mnb_kv_cache (mnb_kv_tables
  * serves both). The codes of token `t % page_size` of head h in block `id`

@@ -304,6 +304,43 @@ def test_float16_scales_up_to_the_largest(new):
             assert ((rows - want).abs() <= want.abs() * (2.0 ** -10 + 2.0 ** -20) + 2.0 ** -25).all(), (scale, b)
 
 
+@pytest.mark.parametrize("size", [1e2, 3e3, 1e5, 1e7, 1e9, 3e10])
+@pytest.mark.parametrize("dt,new,keys", [("f16", None, 700), ("f16", [20, 20], 700), ("f16", [60, 40], 300),
+                                         ("f16", [60, 40], 5000), ("f32", None, 700), ("f32", [60, 40], 300)])
+def test_equal_scores_of_any_size_weigh_the_same(dt, new, keys, size):
+    # keys of one score (half of them written as half the codes with twice the scale): the mean of
+    # their values; a quarter of them far below, and none of it
+    dim, heads = 64, 2
+    for sign in (1, -1):
+        q, cache, table, ln, starts = _case(51, [keys, keys // 2], heads, 1, dim, 16, dt, new=new)
+        cache.k.fill_(64)
+        cache.k[:, :, 1::2] = 32
+        scale = torch.full_like(cache.k_scale, 1.0)
+        scale[:, :, 1::2] = 2.0
+        q.fill_(100.0)
+        low = torch.zeros_like(scale, dtype=torch.bool)
+        low[:, :, 3::4] = True
+        cache.k_scale.copy_(torch.where(low, scale * (0.5 if sign > 0 else 2.0), scale))
+        n = max(new) if new else 1
+        by = sign * size / (dim * 100.0 * 64)
+        got = _np(mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=n, scale=by))
+        vn, sn = _np(cache.v) * _np(cache.v_scale)[..., None], _np(cache.v_scale)
+        rows = oracle.visible(q.shape[0], ln.tolist(), None if starts is None else starts.tolist(), keys, n)
+        for b, t, m in rows:
+            ids = table[b].cpu().numpy()
+            v = oracle.paged_rows(vn, ids, m, 16)[:, 0]
+            vs = oracle.paged_rows(sn[..., None], ids, m, 16)[:, 0, 0]
+            keep = np.arange(m) % 4 != 3 if size > 50 else slice(None)
+            v, vs = v[keep], vs[keep]
+            want, a = v.mean(axis=0), np.abs(v).mean(axis=0)
+            # sums of n terms; whole numbers of 21 bits of weights times value scales; the exponents' reference,
+            # up to 2^12 a float32 number (2^-12 twice); float16: weights times value scales, and the output
+            tol = a * (m + 64) * 2.0 ** -23 + 2.0 ** -21 * vs.max() * (np.abs(v) / vs[:, None]).mean(axis=0) + 2.0 ** -25
+            tol += a * 2.0 ** -20 if dt == "f32" else a * (2.0 ** -11 + 2.0 ** -11) + np.abs(want) * 2.0 ** -11
+            for h in range(heads):
+                _near(got[t, h], want, tol, f"scores of {sign * size:g}, row {t} of {m} keys, head {h}")
+
+
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_the_same_slot_twice_and_requests_that_share_blocks(dt):
     cache = _cache(4, 2, 16, 64, dt, code=3, scale=0.5)
