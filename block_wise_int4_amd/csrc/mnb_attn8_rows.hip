@@ -12,14 +12,16 @@
 //   O^T = CV^T P^T takes P = w vs from those registers as it is: the contraction
 //                 index is renumbered to the keys a lane holds, and CV^T comes out
 //                 of LDS through the transposing 8-byte reads.
-// Weights are held against a reference 2^7 below the running maximum, which moves
-// when a score passes that maximum by more than 2^8; a score less its reference is one
-// multiply-add. That rounds, and equal scores of different steps do not round alike: below
-// kFar 2^-10 of a weight at most, about what float16 takes anyway. A wave whose scores may
-// be larger (by its queries' largest element and the step's key scales) goes on with
-// scores rounded first and the maximum itself taken off them, which is exact.
-// Weights times value scales, against the largest's power of two so far, are rounded to
-// float16 (11 bits: as the output is). Their sum, the denominator, is float32.
+// Weights are held against a reference, the running maximum or up to 2^8 below it; a
+// score less its reference is one multiply-add. That rounds, and equal scores of different
+// steps do not round alike: below kFar 2^-10 of a weight at most, about what float16 takes
+// anyway. A wave whose scores may be larger (by its queries' largest element and the
+// step's key scales) goes on with scores rounded first and the maximum itself taken off
+// them, which is exact.
+// Weights times value scales are the second product's terms, rounded to float16 once (11
+// bits: as the output is). A power of two of the row's own, `up`, keeps its largest so far
+// at 2^7 .. 2^15, whatever the scales of keys that it does not see or that have no weight;
+// it comes with the exponentials. The weights' sum, the denominator, is float32.
 //
 // 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 25 us: 4.4 GFLOP, 39 MB. Half of
 // that is the loop, bound by vector instructions (400 a wave and step, exponentials counted
@@ -37,8 +39,9 @@ namespace mnb {
 namespace {
 
 constexpr int kKeys = 64;     // of a step: four 16-key parts
-constexpr float kLift = 7.0f, kSlack = 8.0f + kLift;
-constexpr float kFar = 16384.0f;
+constexpr float kSlack = 8.0f, kFar = 16384.0f;
+constexpr float kMostUp = 60.0f, kMostTerm = 32768.0f;
+constexpr int kTerm = 7;      // a row's largest term is taken to 2^7 .. 2^8
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -227,10 +230,9 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     // The reference of this lane's row (once a key is seen), the sum of weights
-    // exp2(score - ref), of this lane's keys; biased exponent of the value scales' unit.
-    float ref = 0.0f, l = 0.0f;
+    // exp2(score - ref), of this lane's keys, and the logarithm of its terms' factor.
+    float ref = 0.0f, l = 0.0f, up = kMostUp;
     bool started = false, far = false;   // far, of the wave: ref is the running maximum itself
-    int unit = 1;
     fetch(begin);
     look_up(begin + kKeys);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the compiler does not count loads to LDS)
@@ -271,28 +273,10 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[t] = mma32(*reinterpret_cast<const h8 *>(from + 32 * t * D), q[j], s[t]);
         }
-        // element e of half t is key 32 t + e % 4 + 8 (e / 4) + 4 half. The largest value
-        // scale that is a number; from 2^125 on float16 outputs overflow in any case
+        if (!far && __any(fabsf(s_ks[buf][lane]) * most_product >= kFar)) far = true;
+        const float from = far ? 0.0f : up - ref;   // (a product plus zero is rounded alone)
+        // element e of half t is key 32 t + e % 4 + 8 (e / 4) + 4 half
         f4 vs[2][4];
-        float scales = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                vs[t][j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 32 * t + 8 * j + 4 * half);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) scales = fmaxf(scales, vs[t][j][e]);
-            }
-        int most = __builtin_amdgcn_readfirstlane((int)as_bits(halves_max(scales))) >> 23;
-        most = most < 252 ? most : 252;
-        // scores less the reference, plus the unit's power of two: its inverse, 2^(126 -
-        // unit), then comes with the weights and leaves value scales below one
-        float shift = (float)(126 - unit);
-        if (!far && __any(fabsf(s_ks[buf][lane]) * most_product >= kFar)) {
-            far = true;
-            if (started) ref += kLift;
-        }
-        const float from = far ? 0.0f : shift - ref;   // (a product plus zero is rounded alone)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -300,6 +284,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 const f4 ks = *reinterpret_cast<const f4 *>(s_ks[buf] + 32 * t + 8 * j + 4 * half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[t][4 * j + e] = __builtin_fmaf(s[t][4 * j + e], ks[e], from);
+                vs[t][j] = *reinterpret_cast<const f4 *>(s_vs[buf] + 32 * t + 8 * j + 4 * half);
             }
         if (valid != ~0ull || key0 + kKeys > least) {   // uniform: the end of a row, or a missing block
 #pragma unroll
@@ -318,15 +303,15 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         float top = s[0][0];
 #pragma unroll
         for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e / 16][e % 16]);
-        if (far || __any(top > (started ? shift + kSlack : -__builtin_inff())) || most > unit) {
+        if (far || __any(top > (started ? up + kSlack : -__builtin_inff()))) {
             top = halves_max(top);
             const bool some = top > -__builtin_inff();
-            // how far the reference moves
-            float by = far ? top - ref : top - shift - kLift;
+            float by = far ? top - ref : top - up;   // how far the reference moves
             by = started ? fmaxf(by, 0.0f) : some ? by : 0.0f;
-            const int raised = most > unit ? most : unit, less = unit - raised + 127;
+            // (sums so far shrink by that; the factor takes up what it can of it)
+            const float more = started ? fminf(up + floorf(by), kMostUp) - up : 0.0f;
             const float keep = started ? __builtin_amdgcn_exp2f(-by) : 1.0f;   // (nothing to keep at the start)
-            const float keep_sums = keep * as_float((uint32_t)(less > 0 ? less : 0) << 23);
+            const float keep_sums = started ? __builtin_amdgcn_exp2f(more - by) : 1.0f;
             l *= keep;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
@@ -334,25 +319,39 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 for (int e = 0; e < 16; ++e) o[d][e] *= keep_sums;
             ref = !far ? ref + by : !some ? ref : started ? fmaxf(ref, top) : top;
             started |= some;
-            const float less_by = far ? ref : by + (float)(raised - unit);
-            unit = raised;
-            const float more = far ? (float)(126 - unit) + kLift : 0.0f;
+            up += more;
+            const float less = far ? ref : by, plus = far ? up : more;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] = (s[e / 16][e % 16] - less_by) + more;
+            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] = (s[e / 16][e % 16] - less) + plus;
+        }
+        float sum[2] = {0.0f, 0.0f}, terms[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float w = __builtin_amdgcn_exp2f(s[e / 16][e % 16]);
+            sum[e % 2] += w;
+            s[e / 16][e % 16] = w * vs[e / 16][e % 16 / 4][e % 4];
+            terms[e / 16] = fmaxf(terms[e / 16], s[e / 16][e % 16]);
+        }
+        float term = fmaxf(terms[0], terms[1]);
+        l += __builtin_amdgcn_ldexpf(sum[0] + sum[1], -(int)up);
+        if (__any(term > kMostTerm)) {
+            term = halves_max(term);
+            const int down = term > kMostTerm ? (int)(as_bits(term) >> 23) - 127 - kTerm : 0;   // 8 .. 121
+            const float factor = as_float((uint32_t)(127 - down) << 23);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] *= factor;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] *= factor;
+            up -= (float)down;
         }
         u32x4 p[2][2];
-        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const float w0 = __builtin_amdgcn_exp2f(s[t][e]), w1 = __builtin_amdgcn_exp2f(s[t][e + 1]);
-                sum[0] += w0;
-                sum[1] += w1;
-                const h2 w = {(_Float16)(w0 * vs[t][e / 4][e % 4]), (_Float16)(w1 * vs[t][e / 4][e % 4 + 1])};
-                p[t][e / 8][e % 8 / 2] = as_u32(w);
-            }
-        l = __builtin_fmaf(sum[0] + sum[1], as_float((uint32_t)(unit + 1) << 23), l);   // 2^(unit - 126)
+        for (int e = 0; e < 32; e += 2) {
+            const h2 w = {(_Float16)s[e / 16][e % 16], (_Float16)s[e / 16][e % 16 + 1]};
+            p[e / 16][e % 16 / 8][e % 8 / 2] = as_u32(w);
+        }
         // p[t][k] element j of lane half h is key 32 t + 16 k + 8 (j / 4) + 4 h + j % 4
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -383,7 +382,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     const u32x2 ls = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(as_bits(l), as_bits(l), false, false));
     l = as_float(ls.x) + as_float(ls.y);
     if (!finite && l != 0.0f) l = __builtin_nanf("");   // (its products were taken with zeros)
-    const float back = as_float((uint32_t)(unit + 1) << 23);   // 2^(unit - 126)
+    const float back = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
     __syncthreads();   // (the tiles' last reads are over)
     if (n <= sp.chunk) {
         const float by = l == 0.0f ? 0.0f : back / l;   // (sums are zeros where no key has weight)
@@ -408,7 +407,6 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         return;
     }
     // a piece: the sums in two halves of D / 2 dimensions, 4 bytes each
-    const float lower = far ? 0x1p-7f : 1.0f, by = back * lower;   // (kLift: against ref itself)
     float *sums = sp.sums + (((b * c.heads + h) * sp.rows + row0 + wave * 32) * sp.chunks + chunk) * D;
 #pragma unroll
     for (int d0 = 0; d0 < D / 32; d0 += D / 64) {
@@ -417,7 +415,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
-                    f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * by;
+                    f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
@@ -429,7 +427,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     if (on && half == 0) {
         float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
         stats[0] = started ? ref : kLowest;
-        stats[1] = l * lower;
+        stats[1] = l;
     }
 }
 

@@ -643,8 +643,8 @@ int mnb_kv_read_i8(const int64_t *slots, int64_t T, const mnb_kv_cache_i8 *cache
  * 22-bit numbers against their row's largest, weights times value scales as
  * 22-bit numbers against the largest of 64 keys. float16 calls of 33 query rows
  * and more a key-value head (max_new * Hq / Hkv) round weights times value
- * scales to float16 instead, 11 bits, as the output is; weights below 2^-32 of
- * a row's largest may count as zeros there. float16: |scale| above 2^80 counts
+ * scales to float16 instead, 11 bits, as the output is; what is below 2^-31 of
+ * a row's largest may count as zero there. float16: |scale| above 2^80 counts
  * as 2^80 (products of queries with rows that were appended are zero or above
  * 2^-55, so there is nothing left to tell apart). A query row that holds an
  * infinity or a NaN gives NaN (zeros if it sees nothing), and so does a key or

@@ -342,6 +342,49 @@ def test_equal_scores_of_any_size_weigh_the_same(dt, new, keys, size):
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("new,keys", [(None, 300), ([20, 20], 300), ([60, 40], 300), ([60, 40], 2000)])
+def test_values_of_zeros(dt, new, keys):
+    q, cache, table, ln, starts = _case(52, [keys, 70], 2, 1, 64, 16, dt, new=new)
+    cache.v_scale.zero_()
+    got = mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=max(new) if new else 1)
+    assert not got.any()
+    cache.v_scale.fill_(1.0)
+    cache.v.zero_()
+    cache.v_scale.view(-1)[::3] = 0.0
+    assert not mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=max(new) if new else 1).any()
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("new,keys", [(None, 300), ([20, 20], 300), ([60, 60], 300), ([60, 60], 2000)])
+def test_large_values_of_little_or_no_weight(dt, new, keys):
+    # values of 0.001 beside one of 60000 that a row does not see, or whose key lies far below the
+    # others, before or behind them; and keys that rise, from large values to small ones
+    n = max(new) if new else 1
+    for at in ("last", 3, 100, keys - 70, "rising"):
+        q, cache, table, ln, starts = _case(53, [keys, 250], 2, 1, 64, 16, dt, new=new)
+        cache.v_scale.copy_(torch.where(torch.isfinite(cache.v_scale), cache.v_scale * 1e-3, cache.v_scale))
+        q.copy_(q * 0.1 + 1.0)
+        for b, held in enumerate((keys, 250)):
+            def place(t):
+                return int(table[b, t // 16]), 0, t % 16
+            if at == "rising":      # values fall by 2^25 over the keys, scores rise by 2^40
+                for t in range(held):
+                    part = t / (held - 1)
+                    cache.v_scale[place(t)] = 400.0 * 2.0 ** (-25 * part)
+                    cache.k[place(t)] = 64
+                    cache.k_scale[place(t)] = 40 * 0.6931 * part / 64 / 8
+                continue
+            t = held - 1 if at == "last" else at if at < held else 7
+            cache.v[place(t)] = 127
+            cache.v_scale[place(t)] = 60000.0 / 127
+            if at != "last":
+                cache.k[place(t)] = -127
+                cache.k_scale[place(t)] = 60.0 / 127 / 8
+        got = mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=n)
+        _check(got, q, cache, table, ln, starts, keys, n, dt, what=f"value at {at}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_the_same_slot_twice_and_requests_that_share_blocks(dt):
     cache = _cache(4, 2, 16, 64, dt, code=3, scale=0.5)
     g = torch.Generator(DEV).manual_seed(5)
