@@ -242,9 +242,84 @@ def test_many_requests_most_of_them_empty(dt):
         _check(got, q, cache, table, ln, starts, 70, 50 if n else 1, dt)
 
 
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("new", [None, 2])
+def test_as_many_requests_as_a_call_takes(new, dt):
+    # 65536 requests over 40 blocks that they share, a block each; against plain products in float64
+    B, heads, kv_heads, dim = 65536, 2, 1, 64
+    g = torch.Generator(DEV).manual_seed(6)
+    cache = _cache(40, kv_heads, 16, dim, dt)
+    rows = [torch.randn((640, kv_heads, dim), device=DEV, generator=g).to(TD[dt]) for _ in range(2)]
+    mnb.mnb_kv_append_i8(*rows, torch.arange(640, device=DEV), cache)
+    ids = torch.randint(0, 40, (B, 1), device=DEV, generator=g).int()
+    lens = torch.randint(0, 17, (B,), device=DEV, generator=g).int()
+    tokens = B * (new or 1)
+    q = torch.randn((tokens, heads, dim), device=DEV, generator=g).to(TD[dt])
+    starts = None if new is None else torch.arange(0, tokens + 1, new, **I32)
+    got = mnb.mnb_paged_attn_i8(q, cache, ids, lens, 16, starts=starts, max_new=new or 1)
+    k, v = ((c.double() * s.double()[..., None])[:, 0] for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    at = ids[:, 0].long().repeat_interleave(new or 1)
+    sees = lens.long() if new is None else (lens.long()[:, None] + torch.tensor([-1, 0], device=DEV)).clamp(min=0).flatten()
+    score = (q.double()[:, :, None, :] * k[at][:, None]).sum(dim=-1) * dim ** -0.5
+    hidden = torch.arange(16, device=DEV)[None, None, :] >= sees[:, None, None]
+    w = torch.where(hidden, 0.0, torch.exp(score - score.amax(dim=-1, keepdim=True)))
+    total = w.sum(dim=-1, keepdim=True)
+    p = torch.where(total > 0, w / total, 0.0)
+    want = (p[..., None] * v[at][:, None]).sum(dim=2)
+    a = (p[..., None] * v[at][:, None].abs()).sum(dim=2)
+    # the bound of one row, with |q|, |k| and |v| at their largest here
+    u, s_abs = 2.0 ** -24, float((q.double().abs().amax() * k.abs().sum(dim=-1).amax()) * dim ** -0.5)
+    rel = 2 * (2 * ((dim + 8) * u * s_abs + 4 * u * s_abs) + 2.0 ** -21 + 80 * u)
+    tol = a * rel + 16 * 2.0 ** -21 * float(v.abs().amax()) + want.abs() * u + 1e-30
+    if dt == "f16":
+        tol += a * 2.0 ** -10 + 16 * 2.0 ** -25 * float(v.abs().amax()) + want.abs() * 2.0 ** -11 + 2.0 ** -25
+    assert ((got.double() - want).abs() <= tol).all()
+    assert not got[sees == 0].any()
+
+
+def test_more_tokens_than_a_launch_has_workgroups_for():
+    # 64 tokens a workgroup, 65536 workgroups: the rest in a second turn
+    T = (1 << 22) + 12345
+    g = torch.Generator(DEV).manual_seed(7)
+    cache = _cache(-(-T // 16), 1, 16, 64, "f16")
+    x = torch.randn((T, 1, 64), dtype=torch.float16, device=DEV, generator=g)
+    slots = torch.randperm(T, device=DEV)
+    mnb.mnb_kv_append_i8(x, x.neg(), slots, cache)
+    back = mnb.mnb_kv_read_i8(slots, cache)
+    for got, rows in zip(back, (x, -x)):
+        # half a code's step, amax / 254, and half a step of float16 in what is read back, 2^-11 of at most
+        # amax (1 + 1 / 254); the scale's rounding, 2^-24 of amax, with it: below 1 / 254 + 2^-11 + 2^-18
+        most = rows.float().abs().amax(dim=-1, keepdim=True) * (1 / 254 + 2.0 ** -11 + 2.0 ** -18)
+        assert ((got.float() - rows.float()).abs() <= most).all()
+    some = torch.cat([torch.arange(5, device=DEV), torch.arange(T - 5, T, device=DEV),
+                      torch.randint(0, T, (200,), device=DEV)])
+    codes, scales = oracle.quantize_rows(_np(x[some]))
+    at = slots[some]
+    assert np.array_equal(cache.k[at // 16, :, at % 16].cpu().numpy(), codes)
+    assert np.array_equal(cache.k_scale[at // 16, :, at % 16].cpu().numpy(), scales)
+
+
 # ---------------------------------------------------------------------------
 # far places, far scales, repeated slots
 # ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,dim", [("f16", 64), ("f16", 128), ("f32", 64), ("f32", 128)])
+def test_rows_of_all_exponents(dt, dim):
+    rng = np.random.default_rng(dim)
+    low, high, most = (-149, 127, 3.4028234e38) if dt == "f32" else (-24, 15, 65504.0)
+    x = rng.uniform(-1.9, 1.9, (600, 2, dim)) * 2.0 ** rng.uniform(low, high, (600, 2, 1))
+    grid = 2.0 ** np.floor(rng.uniform(max(low, -120), high - 8, (86, 2, 1)))
+    x[::7] = np.round(rng.uniform(-127.5, 127.5, (86, 2, dim)) * 2) / 2 * grid      # halves between codes
+    rows = torch.from_numpy(np.clip(x, -most, most)).to(TD[dt]).to(DEV)
+    cache, slots = _cache(38, 2, 16, dim, dt), torch.arange(600, device=DEV)
+    mnb.mnb_kv_append_i8(rows, rows, slots, cache)
+    codes, scales = oracle.quantize_rows(_np(rows))
+    assert np.array_equal(cache.v.transpose(1, 2).reshape(-1, 2, dim)[:600].cpu().numpy(), codes)
+    assert np.array_equal(cache.v_scale.transpose(1, 2).reshape(-1, 2)[:600].cpu().numpy(), scales)
+    exact = codes.astype(np.float64) * scales.astype(np.float64)[..., None]
+    assert np.array_equal(mnb.mnb_kv_read_i8(slots, cache)[0].cpu().numpy(),
+                          exact.astype(np.float16 if dt == "f16" else np.float32))
+
 
 @pytest.mark.parametrize("new", [None, [9, 4], [40, 50]])
 def test_offsets_past_32_bits(new):
