@@ -26,7 +26,7 @@
 // 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 25 us: 4.4 GFLOP, 39 MB. Half of
 // that is the loop, bound by vector instructions (400 a wave and step, exponentials counted
 // as four, against 1024 cycles of matrix products), 13 steps in the fullest CU where the
-// mean is 6; a launch and a step take 8. 8 x 62 rows after up to 2000 keys take 22 and
+// mean is 6; a launch and a step take 8. 8 x 62 rows after up to 2000 keys take 23 and
 // the join 6: some 200 workgroups of five steps, 2 us each where a CU has one (4800 cycles,
 // of which 1024 are matrix and 1600 vector instructions: latency). 64 keys a step: with 32
 // these took 34 and 35 us. Two teams of four waves on alternate steps, joined in LDS, were
