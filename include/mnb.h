@@ -641,14 +641,15 @@ int mnb_kv_read_i8(const int64_t *slots, int64_t T, const mnb_kv_cache_i8 *cache
  *
  * Scores, softmax statistics and sums over keys are float32. Queries count as
  * 22-bit numbers against their row's largest, weights times value scales as
- * 22-bit numbers against the largest of 64 keys. float16 calls of 33 query rows
- * and more a key-value head (max_new * Hq / Hkv) round weights times value
- * scales to float16 instead, 11 bits, as the output is; what is below 2^-31 of
- * a row's largest may count as zero there. float16: |scale| above 2^80 counts
- * as 2^80 (products of queries with rows that were appended are zero or above
- * 2^-55, so there is nothing left to tell apart). A query row that holds an
- * infinity or a NaN gives NaN (zeros if it sees nothing), and so does a key or
- * value row of scale NaN to every row that sees it.
+ * 22-bit numbers against the largest of 64 keys (or 2^-103, where that is
+ * less). float16 calls of 33 query rows and more a key-value head (max_new * Hq
+ * / Hkv) round weights times value scales to float16 instead, 11 bits, as the
+ * output is; what is below 2^-31 of a row's largest may count as zero there.
+ * float16: |scale| above 2^80 counts as 2^80 (products of queries with rows
+ * that were appended are zero or above 2^-55, so there is nothing left to tell
+ * apart). A query row that holds an infinity or a NaN gives NaN (zeros if it
+ * sees nothing), and so does a key or value row of scale NaN to every row that
+ * sees it.
  */
 size_t mnb_paged_attn_i8_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t head_dim, int64_t max_len,
                                          int64_t max_new, int dtype);
