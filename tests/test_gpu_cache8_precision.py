@@ -1,0 +1,77 @@
+"""GPU: how finely the attention over the 8-bit cache holds weights times value
+scales, in rows whose terms nearly cancel: an output is then far smaller than its
+terms, and neither its own rounding nor a bound relative to it hides theirs.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from block_wise_int4_amd import mnb
+from test_gpu_cache8 import DEV, TD, _bound, _cache, _case, _near, _np
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("new", [None, [5], [20], [60], [130]], ids=str)
+@pytest.mark.parametrize("keys,dim", [(300, 64), (300, 128), (3000, 128)])
+def test_terms_that_cancel(keys, dim, new, dt):
+    # keys of one score; values 100 of scale 1 + 0.51 2^-10 and -100 of scale 1 + 0.49 2^-10, in turn: either
+    # scale is half a float16 step from the number that float16 makes of it, to opposite sides, and the
+    # result is 50 * 0.02 * 2^-10 instead of 50 * 2^-10
+    q, cache, table, ln, starts = _case(61, [keys], 2, 1, dim, 16, dt, new=new)
+    cache.k.zero_()
+    cache.k_scale.fill_(1.0)
+    cache.v.fill_(100)
+    cache.v[:, :, 1::2] = -100
+    cache.v_scale.fill_(1.0 + 0.51 * 2.0 ** -10)
+    cache.v_scale[:, :, 1::2] = 1.0 + 0.49 * 2.0 ** -10
+    got = _np(mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=new[0] if new else 1))
+    scales = cache.v_scale[0, 0, :2].tolist()
+    tokens = got.shape[0]
+    for t in range(tokens):
+        n = keys - tokens + t + 1
+        want = 100 * (scales[0] * ((n + 1) // 2) - scales[1] * (n // 2)) / n
+        # weights of 1 exactly; 22-bit numbers (half a step of 2^-21 each) times codes of 100; sums of n
+        # terms of 100.05, in pieces joined by factors of 1; the division, the output
+        tol = 100.05 * (2.0 ** -21 + (n + 64) * 2.0 ** -24) + abs(want) * (2.0 ** -11 if dt == "f16" else 2.0 ** -22)
+        tol += 2.0 ** -25
+        assert np.abs(got[t] - want).max() <= tol, (t, n, np.abs(got[t] - want).max() / tol)
+
+
+@pytest.mark.parametrize("heads", [4, 12, 40, 130])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_two_keys_that_cancel(dim, heads):
+    # float16, weights of every size: values of opposite sign whose products with the weights are a few
+    # thousandths apart, for each of many query heads. The bound of a float32 call (weights within 2^-21 of the
+    # tile's largest), the exponents' rounding beside a power of two up to 2^60 (four times half a step of
+    # numbers below 128, 2^-18, of which a weight is moved by ln 2 times as much, in both sums), the output
+    B = 8
+    g = torch.Generator(DEV).manual_seed(dim + heads)
+    cache = _cache(B, 1, 16, dim, "f16", code=0, scale=0.0)
+    q = torch.randn((B, heads, dim), device=DEV, generator=g).half()
+    cache.k[:, 0, :2] = torch.randint(-127, 128, (B, 2, dim), device=DEV, generator=g).to(torch.int8)
+    cache.k_scale[:, 0, :2] = 0.02
+    table = torch.arange(B, **I32)[:, None].contiguous()
+    lens = torch.full((B,), 2, **I32)
+    for head in range(min(heads, 4)):      # cancels for one head at a time
+        k = _np(cache.k[:, 0, :2]) * float(cache.k_scale[0, 0, 0])
+        score = (k * _np(q[:, head])[:, None]).sum(axis=2) * dim ** -0.5
+        ratio = np.exp(score[:, 0] - score[:, 1])     # of the weights
+        cache.v[:, 0, 0], cache.v[:, 0, 1] = 100, -100
+        cache.v_scale[:, 0, 0] = 0.37
+        cache.v_scale[:, 0, 1] = torch.from_numpy(0.37 * ratio * (1 + 2.0 ** -9)).to(DEV).float()
+        got = _np(mnb.mnb_paged_attn_i8(q, cache, table, lens, 2))
+        vn, sn = _np(cache.v) * _np(cache.v_scale)[..., None], _np(cache.v_scale)
+        for b in range(B):
+            v, vs = vn[b, 0, :2], sn[b, 0, :2]
+            ref = oracle.attend(_np(q[b, head]), k[b], v, dim ** -0.5)
+            p = np.exp(score[b] - score[b].max())
+            a = (p[:, None] * np.abs(v)).sum(axis=0) / p.sum()
+            tol = _bound(_np(q[b, head]), k[b], v, vs, dim ** -0.5, "f32") + a * 2 * 4 * 2.0 ** -18 * np.log(2)
+            assert np.all(np.abs(ref) < a * 2.0 ** -8)
+            _near(got[b, head], ref, tol + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25, f"request {b}, head {head} of {heads}")
