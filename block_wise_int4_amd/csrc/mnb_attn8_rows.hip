@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kKeys = 64;     // of a step: four 16-key parts
 constexpr float kSlack = 8.0f, kFar = 16384.0f;
-constexpr float kMostUp = 60.0f, kMostTerm = 32768.0f;
+constexpr float kMostUp = 60.0f, kMostTerm = 32768.0f, kMostFloat = 3.402823466e38f;
 constexpr int kTerm = 7;      // a row's largest term is taken to 2^7 .. 2^8
 
 typedef float f16v __attribute__((ext_vector_type(16)));
@@ -338,11 +338,16 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         float term = fmaxf(terms[0], terms[1]);
         l += __builtin_amdgcn_ldexpf(sum[0] + sum[1], -(int)up);
         if (__any(term > kMostTerm)) {
-            term = halves_max(term);
-            const int down = term > kMostTerm ? (int)(as_bits(term) >> 23) - 127 - kTerm : 0;   // 8 .. 121
+            // (terms past float32's range, of value scales from 2^59 on, stand for its largest, 2^68 or more of
+            // the reference's weight: infinite in float16 but with codes of zero, which infinity makes NaN)
+            term = fminf(halves_max(term), kMostFloat);
+            const int down = term > kMostTerm ? (int)(as_bits(term) >> 23) - 127 - kTerm : 0;   // 8 .. 120
             const float factor = as_float((uint32_t)(127 - down) << 23);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e / 16][e % 16] *= factor;
+            for (int e = 0; e < 32; ++e) {
+                const float x = s[e / 16][e % 16];
+                s[e / 16][e % 16] = (x > kMostFloat ? kMostFloat : x) * factor;   // (NaN stays)
+            }
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -433,6 +438,8 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         }
     }
     if (on && half == 0) {
+        // (the lane counted again: kept over the loop, it is the register too many)
+        const int r = row0 + wave * 32 + (int)__builtin_amdgcn_mbcnt_lo(~0u, 0u);
         float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
         stats[0] = started ? ref : kLowest;
         stats[1] = l;
