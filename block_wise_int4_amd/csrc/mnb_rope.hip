@@ -111,16 +111,27 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(RopeArgs a, float per
 
 namespace {
 
-template <typename T, bool INTERLEAVED> hipError_t launch(const RopeArgs &a, hipStream_t st) {
-    const unsigned grid = (unsigned)((a.tokens + kWaves - 1) / kWaves);
+// Tokens of a launch, whose threads (64 a token) are counted in 32 bits. (A loop over
+// tokens in the kernel takes a register too many: four waves a SIMD for five.)
+constexpr int64_t kMostTokens = 1 << 25;
+
+template <typename T, bool INTERLEAVED> hipError_t launch(RopeArgs a, hipStream_t st) {
     constexpr int piece = 16 / (int)sizeof(T);
     const bool vec = INTERLEAVED ? a.rot_dim % piece == 0 : a.rot_dim / 2 % piece == 0;
     const int turning = !vec ? a.rot_dim / 2 : INTERLEAVED ? a.rot_dim / piece : a.rot_dim / 2 / piece;
     const float per_units = 1.0f / (float)(turning + (a.head_dim - a.rot_dim) / (vec ? piece : 1));
-    // (head_dim is a whole number of pieces)
-    if (vec) rope_kernel<T, INTERLEAVED, true><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
-    else rope_kernel<T, INTERLEAVED, false><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
-    return hipGetLastError();
+    for (int64_t left = a.tokens;;) {
+        a.tokens = left < kMostTokens ? left : kMostTokens;
+        const unsigned grid = (unsigned)((a.tokens + kWaves - 1) / kWaves);
+        // (head_dim is a whole number of pieces)
+        if (vec) rope_kernel<T, INTERLEAVED, true><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
+        else rope_kernel<T, INTERLEAVED, false><<<grid, 64 * kWaves, 0, st>>>(a, per_units);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || (left -= a.tokens) == 0) return e;
+        if (a.q_heads) a.q += a.tokens * a.q_stride, a.q_out += a.tokens * a.q_out_stride;
+        if (a.k_heads) a.k += a.tokens * a.k_stride, a.k_out += a.tokens * a.k_out_stride;
+        a.positions += a.tokens;
+    }
 }
 
 }  // namespace
