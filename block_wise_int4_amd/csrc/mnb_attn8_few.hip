@@ -163,6 +163,7 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
 #pragma unroll
                 for (int s = 0; s < kParts; ++s)
                     *reinterpret_cast<i32x4 *>(s_products + col * kScoreStride + 16 * s + 4 * g) = p[s];
+            wave_fence();
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int32_t *p = s_products + 3 * i * kScoreStride + lane;
@@ -170,6 +171,7 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
                     __builtin_fmaf((float)p[2 * kScoreStride], 256.0f, (float)p[kScoreStride]), 256.0f, (float)p[0]);
                 x[i] = sum * (ks * mul[i]);
             }
+            wave_fence();   // (the digits take the products' place)
         }
         // (past the last tile loads of no bytes are requested: with a way around them the
         // compiler counts none, and waits too long for those before)
@@ -197,9 +199,11 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
             for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int t = 0; t < 3; ++t) s_digits[(3 * i + t) * kDigitStride + lane] = (uint8_t)(w[i] >> (8 * t));
+            wave_fence();
             // this lane's column: its digits of keys 16 g on; what a step of its sums is
             // worth, and what its sums so far are
             const i32x4 p = *reinterpret_cast<const i32x4 *>(s_digits + (col < kColumns ? col : 0) * kDigitStride + 16 * g);
+            wave_fence();   // (the next tile's products take the digits')
             float worth = down[0], kept = keep[0];
 #pragma unroll
             for (int i = 1; i < R; ++i) {

@@ -407,6 +407,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                                  as_u32(h2{(_Float16)(o[d][e + 2] * by), (_Float16)(o[d][e + 3] * by)})};
                 *reinterpret_cast<u32x2 *>(in_rows(col, 4 * d + e / 4) + 4 * half) = w;
             }
+        wave_fence();
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
@@ -429,6 +430,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
                     f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
+        wave_fence();
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
             const int row = k * kRowsAtOnce + carried;
@@ -436,6 +438,7 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 *reinterpret_cast<f4 *>(sums + (int64_t)row * sp.chunks * D + 32 * d0 + carried_piece * 4) =
                     *reinterpret_cast<const f4 *>(in_rows(row, carried_piece));
         }
+        wave_fence();   // (the second half takes the first's place)
     }
     if (on && half == 0) {
         // (the lane counted again: kept over the loop, it is the register too many)

@@ -132,6 +132,13 @@ __device__ __forceinline__ float mul_round_odd(float q, float s) {
     return __builtin_bit_cast(float, u);
 }
 
+// Between LDS accesses of some lanes of a wave and accesses of others to the same place. The
+// hardware keeps a wave's LDS operations in order; the compiler keeps those of one lane.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <typename T> struct Io;
 template <> struct Io<float> {
     static constexpr int kScaleBytes = 4;

@@ -76,8 +76,7 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(RopeArgs a, float per
         }
         if (!ready) {   // (behind the first loads)
             for (int i = lane; i < pairs; i += 64) s_turn[wave][i] = turn_of(position, a.freqs[i], a.gain);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            wave_fence();
             ready = true;
         }
 #pragma unroll
