@@ -75,3 +75,44 @@ def test_two_keys_that_cancel(dim, heads):
             tol = _bound(_np(q[b, head]), k[b], v, vs, dim ** -0.5, "f32") + a * 2 * 4 * 2.0 ** -18 * np.log(2)
             assert np.all(np.abs(ref) < a * 2.0 ** -8)
             _near(got[b, head], ref, tol + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25, f"request {b}, head {head} of {heads}")
+
+
+@pytest.mark.parametrize("size", [50, 3e3, 8e3, 1.1e4, 1.126e4, 1.128e4, 1.2e4, 1.6e4, 3e4])
+@pytest.mark.parametrize("rise", [0, 12])
+@pytest.mark.parametrize("new", [None, [10], [20], [60]], ids=str)
+def test_equal_scores_of_different_steps_cancel(new, rise, size):
+    # keys of one score, 64 with a value of 100, 64 with -100, in turn; with `rise` the first 128 are that much
+    # lower, 64 of them twice. Calls of many float16 rows take a score less its reference as one multiply-add
+    # while 128 times the codes' and the query's largest sum stays below 2^14 by log2(e): codes of 127 reach
+    # scores of 11267 there. The reference and its difference from the factor's exponent are then float32
+    # numbers up to 2^14, each off by 2^-11, which moves a step's weights by ln 2 times 2^-10 at most, in the
+    # sum and in the total. Beyond that, and in the other calls, equal scores weigh the same.
+    dim, keys = 64, 640
+    one_fma = new is not None and 2 * new[0] >= 33 and size < 11267      # (two heads share the keys)
+    for sign in (1, -1):
+        q, cache, table, ln, starts = _case(62, [keys], 2, 1, dim, 16, "f16", new=new)
+        q.fill_(100.0)
+        cache.k.fill_(127)
+        cache.k_scale.fill_(1.0)
+        cache.v_scale.fill_(1.0)
+        for t in range(keys):
+            where = int(table[0, t // 16]), 0, t % 16
+            cache.v[where] = 100 if t // 64 % 2 == 0 else -100
+            if t < 128:
+                cache.k_scale[where] = 1.0 - sign * rise * (2 - t // 64) / size
+        by = sign * size / (dim * 100.0 * 127)
+        got = _np(mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=new[0] if new else 1, scale=by))
+        ids, kn, vn = table[0].cpu().numpy(), _np(cache.k) * _np(cache.k_scale)[..., None], _np(cache.v)
+        tokens = got.shape[0]
+        for t in range(tokens):
+            n = keys - tokens + t + 1
+            k, v = (oracle.paged_rows(x, ids, n, 16)[:, 0] for x in (kn, vn))
+            ref = oracle.attend(_np(q)[t, 0], k, v, by)
+            # terms of 100 as 22-bit numbers, sums of n of them; the lower keys' weights, below e^-12 in all
+            # but off by any part of themselves where scores are large; the output
+            tol = 100 * (2.0 ** -20 + (n + 64) * 2.0 ** -24 + (2 * 2.0 ** -10 if one_fma else 0.0))
+            tol += np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
+            if rise:
+                tol += 100 * 64 * 2 * np.exp(-12.0) / (n - 128) * (size * 2.0 ** -22 if size > 100 else 2.0 ** -16)
+            worst = (np.abs(got[t] - ref) / tol).max()
+            assert worst <= 1.0, (sign, t, worst)
