@@ -113,7 +113,8 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
     request_values();
     i32x4 q[kLoads][3];   // in digits: lane (query col, pieces 4 j + g)
     float mul;
-    row.digits(a.scale, q, mul);
+    int exponent;
+    row.digits(a.scale, q, mul, exponent);
     for (; key < end; key += step) {
         float x[kParts][4];
         {
@@ -132,9 +133,9 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                 hi = hi << 8;
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) hi = mma64(kk[s][j], q[j][1], hi);
-                const f4 by = ks[s] * mul;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * by[i];
+                for (int i = 0; i < 4; ++i)
+                    x[s][i] = __builtin_fmaf((float)hi[i], 256.0f, (float)lo[i]) * score_step(ks[s][i], mul, exponent);
             }
         }
         // (past the last tile loads of no bytes are requested: with a way around them the

@@ -127,11 +127,13 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
     request_values();
     i32x4 q[kLoads];
     float mul[R];
+    int exponent[R];
     int seen[R];   // keys that each row sees
     {
         i32x4 all[kLoads][3];
         float m;
-        row.digits(a.scale, all, m);
+        int e;
+        row.digits(a.scale, all, m, e);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
 #pragma unroll
@@ -142,6 +144,7 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             mul[i] = as_float((uint32_t)__builtin_amdgcn_readlane((int)as_bits(m), 3 * i));
+            exponent[i] = __builtin_amdgcn_readlane(e, 3 * i);
             seen[i] = i < rows ? sees(a, len, n_new, token_of(a, i)) : 0;
         }
     }
@@ -169,7 +172,7 @@ __device__ __forceinline__ void few_workgroup(const Attn8Args &a, const Attn8Spl
                 const int32_t *p = s_products + 3 * i * kScoreStride + lane;
                 const float sum = __builtin_fmaf(
                     __builtin_fmaf((float)p[2 * kScoreStride], 256.0f, (float)p[kScoreStride]), 256.0f, (float)p[0]);
-                x[i] = sum * (ks * mul[i]);
+                x[i] = sum * score_step(ks, mul[i], exponent[i]);
             }
             wave_fence();   // (the digits take the products' place)
         }

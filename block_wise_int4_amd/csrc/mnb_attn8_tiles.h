@@ -71,10 +71,11 @@ template <typename T, int D> struct QueryRow {
         else return __builtin_bit_cast(f4, x)[i % kEach];
     }
     // In three digits: digit[j][t] is digit t, least significant first, of piece j's numbers
-    // n = x 2^(21 - e), |n| < 2^22, 2^e the largest element's power of two. mul: of a sum of
-    // products with n, to a score without the key's scale; NaN (and digits of zeros)
-    // for a row that is not finite.
-    __device__ __forceinline__ void digits(float scale, i32x4 (*digit)[3], float &mul) const {
+    // n = x 2^(21 - e), |n| < 2^22, 2^e the largest element's power of two. mul 2^exponent: of a
+    // sum of products with n, to a score without the key's scale (apart, as it may lie far
+    // past float32's range and the score not); NaN (and digits of zeros) for a row that is
+    // not finite.
+    __device__ __forceinline__ void digits(float scale, i32x4 (*digit)[3], float &mul, int &exponent) const {
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
@@ -92,7 +93,8 @@ template <typename T, int D> struct QueryRow {
         if (small) top = as_bits(as_float(top) * 0x1p64f);
         const int e = top ? (int)(top >> 23) : 127;
         const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
-        mul = finite ? __builtin_ldexpf(scale, e - 127 - 21 - (small ? 64 : 0)) : __builtin_nanf("");
+        mul = finite ? __builtin_amdgcn_frexp_mantf(scale) : __builtin_nanf("");
+        exponent = __builtin_amdgcn_frexp_expf(scale) + e - 127 - 21 - (small ? 64 : 0);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
 #pragma unroll
@@ -112,6 +114,13 @@ template <typename T, int D> struct QueryRow {
             }
     }
 };
+
+// What a sum of products with a query's numbers is worth as a score: mul 2^exponent times
+// the key's scale. (The power of two first: exact unless the whole is below 2^-126, the
+// score below 2^-85, or past float32's range.)
+__device__ __forceinline__ float score_step(float key_scale, float mul, int exponent) {
+    return __builtin_amdgcn_ldexpf(key_scale, exponent) * mul;
+}
 
 // Weights times value scales as numbers below 2^22: times `up`, 2^(21 - exponent of the
 // largest) a touch less so that none rounds up to 2^22, plus 2^23 + 0x8080, whose bytes

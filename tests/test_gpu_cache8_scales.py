@@ -54,3 +54,21 @@ def test_large_value_scales_of_little_weight(exponent, new):
             cache.v_scale[where] = 2.0 ** exponent
             got = mnb.mnb_paged_attn_i8(q, cache, table, ln, keys, starts=starts, max_new=n)
             _check(got, q, cache, table, ln, starts, keys, n, "f16", what=f"key {at}, 2^{left}")
+
+
+@pytest.mark.parametrize("new", [None, [3], [40]], ids=str)
+@pytest.mark.parametrize("size,keys_size,scale", [
+    (2e-38, 1e38, 0.5), (1e-36, 1e34, 3.0), (3e-34, 1e36, 1 / 300), (3e-39, 1e38, 3.0), (1e38, 1e-41, 1 / 300),
+    (1e-30, 1e-10, 1e38), (1e-42, 1e4, 3e38), (3e37, 1e-10, 1e-27)])
+def test_float32_products_of_far_sizes(size, keys_size, scale, new):
+    # queries and keys whose products are ordinary numbers
+    q, cache, table, ln, starts = _case(73, [90], 2, 1, 64, 16, "f32", new=new)
+    n = new[0] if new else 1
+    q = (q / q.abs().amax()).double().mul(size).float()
+    ok = torch.isfinite(cache.k_scale)
+    most = float((cache.k.abs().amax(dim=-1) * cache.k_scale.where(ok, torch.zeros_like(cache.k_scale))).amax())
+    cache.k_scale.copy_(torch.where(ok, (cache.k_scale.double() / most * keys_size).float(), cache.k_scale))
+    where = _at(table, 16, 0, 7)
+    cache.k_scale[where], cache.k[where] = 0.0, 0      # a key of zeros among them
+    got = mnb.mnb_paged_attn_i8(q, cache, table, ln, 90, starts=starts, max_new=n, scale=scale)
+    _check(got, q, cache, table, ln, starts, 90, n, "f32", scale, f"{size} x {keys_size}")
