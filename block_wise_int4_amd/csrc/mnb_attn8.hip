@@ -325,15 +325,24 @@ struct Plan {
 // Which kernel, and how a call is cut into workgroups over `chunk` keys. Figures are us
 // a call, replayed from a graph; 8 heads of 128 are shared by 16, 8 of 64 by 32.
 //
-// Few rows: a row of up to kWholeBytes of codes is one workgroup, and the call one launch
-// (one request of 2000 keys and 8 x 64: 10.1; whole 15.7; 452 keys and 8 x 128 whole 8.6,
-// in pieces 10). From kFullUnits rows of tiles on, which fill the card by themselves, that
-// goes up to kFullBytes (float32, 16 x 1500 keys, 12 x 64: 9.5, in pieces 11.3; but with
-// 128 rows of tiles, 16 x 3000, 8 x 64, 15.9 in pieces and 20.9 whole; and past 1 MB, 24 x
-// 16000, 12 x 64, 77 in pieces and 98 whole). Longer rows: kMany workgroups (16 x 16000, 8 x
-// 128: 73, with 4096 80; with 1024 the same 0.1% over 372 calls, 20% worse at the worst) of
-// kLeast keys or more (512 1% slower over those calls, 16 x 3000 22.7 for 18.2; 1024 0.3%),
-// and at least kFew of them (1 x 6000 9.8, with 128 11.1; 1 x 16000 with 512 13.1 for 11.8).
+// Few rows: a row whole is one workgroup, and the call one launch. Whole it takes as long
+// as its longest row; cut, as long as the CUs' share of all rows, and the join. So it
+// stays whole while what the longest row has over a CU's share, for rows of max_len each,
+// is no more than the join costs: kJoinBytes of codes for up to kFewRows rows (64
+// dimensions, 12 float32 heads: 4 requests of 1500 keys 9.1 us, cut 9.1, of 3000 12.7 and
+// 9.9; 8 of 1500 9.4 and 9.9, of 3000 13.7 and 12.1; 16 of 3000 15.5 and 16.5; one of 3000
+// and 2 heads 12.2 and 8.8), kTileJoinBytes for tiles of 16, whose workgroups need longer a
+// byte (8 heads of 128 shared by 64: 12 requests of 700 keys 12.0 and 11.9, of 1100 16.6 and
+// 13.7, 24 of 1100 17.3 and 18.2). 96 and 160 KB for the first are 0.3% and 0.1% slower in
+// the mean of 2004 calls of 1..128 requests of up to 520..8000 keys, 32 and 64 KB for the
+// second the same and 0.3% of 750; the better side of each call would be 0.8% and 1.1% faster
+// (longest rows among short ones, which the call does not know, are the worst: 320 rows of
+// tiles of 5..8000 keys 62 whole and 44 cut). Past kFullBytes rows are cut (24 x 16000, 12 x
+// 64, 77 cut and 98 whole).
+// Longer rows: kMany workgroups (16 x 16000, 8 x 128: 73, with 4096 80; with 1024 the same
+// 0.1% over 372 calls, 20% worse at the worst) of kLeast keys or more (512 1% slower over
+// those calls, 16 x 3000 22.7 for 18.2; 1024 0.3%), and at least kCus of them (1 x 6000 9.8,
+// with 128 11.1; 1 x 16000 with 512 13.1 for 11.8).
 //
 // Many rows: from kManyRows on, three tiles of this file's kernel, which the other form
 // takes as one: 40 rows and 64 x 300 keys 22 and 34, 8 x 8000 53 and 61; below, 32 rows and
@@ -342,9 +351,15 @@ struct Plan {
 // 8000 keys, 124 rows: 56, with 256 68), and where those are too few kFullWgs of
 // kLeastKeys or more (1 x 2000, 124 rows: 15.0, in pieces of 256 17.2; 1 x 410 new 14.6
 // and 16.8); up to kManyKeys keys are one piece (2 x 200 new 12.6, in two 13.3).
-constexpr int64_t kWholeBytes = 128 << 10, kFullBytes = 1 << 20, kMany = 2048, kLeast = 768, kFew = 256,
-                  kFullUnits = 192, kManyWgs = 512, kManyKeys = 256, kFullWgs = 256, kLeastKeys = 128,
-                  kManyRows = 33;
+constexpr int64_t kCus = 256, kJoinBytes = 128 << 10, kTileJoinBytes = 48 << 10, kFullBytes = 1 << 20, kMany = 2048,
+                  kLeast = 768, kManyWgs = 512, kManyKeys = 256, kFullWgs = 256, kLeastKeys = 128, kManyRows = 33;
+
+// Whether rows of max_len keys of few query rows stay whole, `units` of them.
+bool whole_rows(int64_t rows, int64_t units, int64_t max_len, int head_dim) {
+    const int64_t bytes = 2 * max_len * head_dim, join = rows <= kFewRows ? kJoinBytes : kTileJoinBytes;
+    return bytes <= kFullBytes && bytes * (kCus - std::min(units, kCus)) <= join * kCus;
+}
+
 Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64_t max_len, int head_dim, int dtype) {
     Plan p;
     p.rows = max_new * group;
@@ -359,10 +374,10 @@ Plan plan(int64_t batch, int64_t kv_heads, int64_t group, int64_t max_new, int64
     if (p.many) {
         if (all / kManyWgs < (double)keys) chunk = (int64_t)(all / kManyWgs);
         if (chunk < kManyKeys && keys > kManyKeys) chunk = std::max((int64_t)(all / kFullWgs), kLeastKeys);
-    } else if (max_len > (units < kFullUnits ? kWholeBytes : kFullBytes) / (2 * head_dim)) {
+    } else if (!whole_rows(p.rows, units, max_len, head_dim)) {
         chunk = all / kMany < (double)keys ? (int64_t)(all / kMany) : keys;
         if (chunk < kLeast) chunk = kLeast;
-        if (units * ((keys + chunk - 1) / chunk) < kFew) chunk = (int64_t)(all / kFew);
+        if (units * ((keys + chunk - 1) / chunk) < kCus) chunk = (int64_t)(all / kCus);
     }
     if (chunk < step) chunk = step;
     chunk = (chunk + step - 1) / step * step;
