@@ -19,8 +19,8 @@
 // step's key scales) goes on with scores rounded first and the maximum itself taken off
 // them, which is exact.
 // Weights times value scales are the second product's terms, two float16 numbers each, 22
-// bits: one number (11 bits) took 2.3 us of 31.6 off 8 x 62 rows after up to 2000 keys,
-// nothing off 16 prompts of 62..410 rows, and put outputs off by 2.9e-4 of their size where
+// bits: one number (11 bits) took 1.9 us of 26.1 off 16 prompts of 62..410 rows and 1.6 of
+// 31.0 off 8 x 62 rows after up to 2000 keys, and put outputs off by 2.9e-4 of their size where
 // their own rounding is 2.1e-4. A power of two of the row's own, `up`, keeps its largest so
 // far at 2^7 .. 2^15, whatever the scales of keys that it does not see or that have no
 // weight; it comes with the exponentials, whose arguments it makes up to 2^6 larger (2^-18 of
@@ -259,6 +259,8 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     __syncthreads();   // (the tiles' place is free)
     put(0);
     valid = valid_next;
+    float minus = -1.0f;
+    asm("" : "+s"(minus));   // (known, it makes the multiply-adds below subtractions)
     int buf = 0;
     for (int key0 = begin; key0 < end; key0 += kKeys, buf ^= 1) {
         __syncthreads();
@@ -354,14 +356,15 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
                 for (int e = 0; e < 16; ++e) o[d][e] *= factor;
             up -= (float)down;
         }
-        // (each term as two float16 numbers: what the first leaves is exact, and the second's)
+        // (each term as two float16 numbers: what the first leaves is exact, and the second's;
+        // written as multiply-adds, which take and give float16 by themselves)
         u32x4 p[2][2], rest[2][2];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             const float x = s[e / 16][e % 16], y = s[e / 16][e % 16 + 1];
-            const h2 w = {(_Float16)x, (_Float16)y};
+            const h2 w = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(x, y));
+            const h2 r = {(_Float16)__builtin_fmaf((float)w.x, minus, x), (_Float16)__builtin_fmaf((float)w.y, minus, y)};
             p[e / 16][e % 16 / 8][e % 8 / 2] = as_u32(w);
-            const h2 r = {(_Float16)(x - (float)w.x), (_Float16)(y - (float)w.y)};
             rest[e / 16][e % 16 / 8][e % 8 / 2] = as_u32(r);
         }
         // p[t][k] element j of lane half h is key 32 t + 16 k + 8 (j / 4) + 4 h + j % 4
@@ -397,6 +400,11 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
     if (!finite && l != 0.0f) l = __builtin_nanf("");   // (its products were taken with zeros)
     const float back = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
     __syncthreads();   // (the tiles' last reads are over)
+    // (the lane counted again, for its places in LDS and memory: kept over the loop these are
+    // the registers too many)
+    const int lane_now = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    const int col_now = lane_now & 31, half_now = lane_now >> 5;
+    const int carried_now = lane_now / kRowPieces, piece_now = lane_now % kRowPieces;
     if (n <= sp.chunk) {
         const float by = l == 0.0f ? 0.0f : back / l;   // (sums are zeros where no key has weight)
 #pragma unroll
@@ -405,18 +413,18 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
             for (int e = 0; e < 16; e += 4) {
                 const u32x2 w = {as_u32(h2{(_Float16)(o[d][e] * by), (_Float16)(o[d][e + 1] * by)}),
                                  as_u32(h2{(_Float16)(o[d][e + 2] * by), (_Float16)(o[d][e + 3] * by)})};
-                *reinterpret_cast<u32x2 *>(in_rows(col, 4 * d + e / 4) + 4 * half) = w;
+                *reinterpret_cast<u32x2 *>(in_rows(col_now, 4 * d + e / 4) + 4 * half_now) = w;
             }
         wave_fence();
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
-            const int row = k * kRowsAtOnce + carried;
+            const int row = k * kRowsAtOnce + carried_now;
             int64_t of, head;
             token_head(row, of, head);
             if (wave * 32 + row < rows)
                 *reinterpret_cast<u32x4 *>(static_cast<_Float16 *>(a.out) +
-                                           (of * ((int64_t)c.heads * a.group) + head) * D + carried_piece * 8) =
-                    *reinterpret_cast<const u32x4 *>(in_rows(row, carried_piece));
+                                           (of * ((int64_t)c.heads * a.group) + head) * D + piece_now * 8) =
+                    *reinterpret_cast<const u32x4 *>(in_rows(row, piece_now));
         }
         return;
     }
@@ -428,21 +436,20 @@ template <int D> __device__ __forceinline__ void rows_workgroup(const Attn8Args 
         for (int d = 0; d < D / 64; ++d)
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<f4 *>(in_rows(col, 8 * d + e / 2 + half)) =
+                *reinterpret_cast<f4 *>(in_rows(col_now, 8 * d + e / 2 + half_now)) =
                     f4{o[d0 + d][e], o[d0 + d][e + 1], o[d0 + d][e + 2], o[d0 + d][e + 3]} * back;
         wave_fence();
 #pragma unroll 1
         for (int k = 0; k < kCarries; ++k) {
-            const int row = k * kRowsAtOnce + carried;
+            const int row = k * kRowsAtOnce + carried_now;
             if (wave * 32 + row < rows)
-                *reinterpret_cast<f4 *>(sums + (int64_t)row * sp.chunks * D + 32 * d0 + carried_piece * 4) =
-                    *reinterpret_cast<const f4 *>(in_rows(row, carried_piece));
+                *reinterpret_cast<f4 *>(sums + (int64_t)row * sp.chunks * D + 32 * d0 + piece_now * 4) =
+                    *reinterpret_cast<const f4 *>(in_rows(row, piece_now));
         }
         wave_fence();   // (the second half takes the first's place)
     }
-    if (on && half == 0) {
-        // (the lane counted again: kept over the loop, it is the register too many)
-        const int r = row0 + wave * 32 + (int)__builtin_amdgcn_mbcnt_lo(~0u, 0u);
+    if (wave * 32 + col_now < rows && half_now == 0) {
+        const int r = row0 + wave * 32 + col_now;
         float *stats = sp.stats + 2 * (((b * c.heads + h) * sp.rows + r) * sp.chunks + chunk);
         stats[0] = started ? ref : kLowest;
         stats[1] = l;

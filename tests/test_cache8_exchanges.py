@@ -29,8 +29,8 @@ FENCE = "wave_fence();"
                            "s_digits[(3 * i + t) * kDigitStride + lane] =", FENCE,
                            "(s_digits + (col < kColumns ? col : 0)", FENCE, "request_values();\n    }"]),
     # whole rows of results; pieces in two halves through one place
-    ("mnb_attn8_rows.hip", ["<u32x2 *>(in_rows(col, 4 * d", FENCE, "<const u32x4 *>(in_rows(row, carried_piece))",
-                            "<f4 *>(in_rows(col, 8 * d", FENCE, "<const f4 *>(in_rows(row, carried_piece))", FENCE]),
+    ("mnb_attn8_rows.hip", ["<u32x2 *>(in_rows(col_now, 4 * d", FENCE, "<const u32x4 *>(in_rows(row, piece_now))",
+                            "<f4 *>(in_rows(col_now, 8 * d", FENCE, "<const f4 *>(in_rows(row, piece_now))", FENCE]),
     # a token's cosines and sines
     ("mnb_rope.hip", ["s_turn[wave][i] = turn_of", FENCE, "s_turn[wave][unit[i]"]),
 ])
