@@ -3,8 +3,8 @@
 // m the running maximum.
 //
 // Both products are whole numbers. A query row is held as its largest element's
-// power of two times 22-bit numbers and a sign, these as three digits of 8 bits;
-// a tile's weights w_t vs_t as the power of two of the tile's largest times 22-bit
+// power of two times whole numbers below 2^23, these as three digits of 8 bits;
+// a tile's weights w_t vs_t as the power of two of the tile's largest times such
 // numbers, in three digits as well. So codes enter the matrix unit as they are
 // stored, nothing is rounded between the digits and the 32-bit sums, and float16
 // and float32 calls differ in their first loads and last stores alone.
@@ -129,7 +129,7 @@ __device__ __forceinline__ void attn8_workgroup(const Attn8Args &a, const Attn8S
                     lo = mma64(kk[s][j], q[j][0], lo);
                     hi = mma64(kk[s][j], q[j][2], hi);
                 }
-                // (below 2^21 * 2^8: the two upper digits in one number)
+                // (up to 2^21 * 2^8: the two upper digits in one number)
                 hi = hi << 8;
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) hi = mma64(kk[s][j], q[j][1], hi);

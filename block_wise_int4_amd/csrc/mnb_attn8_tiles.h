@@ -53,6 +53,12 @@ __device__ __forceinline__ void digits_of(const uint32_t *w, uint32_t *digit) {
     digit[2] = b01 | b23;
 }
 
+// The biased exponent under which a positive number is no more than 1.985 times a power of
+// two: three balanced digits hold whole numbers up to 127 (2^16 + 2^8 + 1), 1.992 2^22.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+    return (int)(as_bits(as_float(bits) * (1.0f + 0x1p-7f)) >> 23);
+}
+
 // A query row: lane (any column, g = lane / 16) takes 16 dimensions of each 64 from src on,
 // which is the row's 16 g.
 template <typename T, int D> struct QueryRow {
@@ -71,7 +77,8 @@ template <typename T, int D> struct QueryRow {
         else return __builtin_bit_cast(f4, x)[i % kEach];
     }
     // In three digits: digit[j][t] is digit t, least significant first, of piece j's numbers
-    // n = x 2^(21 - e), |n| < 2^22, 2^e the largest element's power of two. mul 2^exponent: of a
+    // n = x 2^(22 - e), 2^e the largest element's power of two (the next one where three
+    // digits would not hold the largest): |n| < 2^23. mul 2^exponent: of a
     // sum of products with n, to a score without the key's scale (apart, as it may lie far
     // past float32's range and the score not); NaN (and digits of zeros) for a row that is
     // not finite.
@@ -91,10 +98,10 @@ template <typename T, int D> struct QueryRow {
         const bool small = top < (64u << 23);
         const float lift = small ? 0x1p64f : 1.0f;
         if (small) top = as_bits(as_float(top) * 0x1p64f);
-        const int e = top ? (int)(top >> 23) : 127;
-        const float up = as_float((uint32_t)(127 + 21 + 127 - e) << 23);
+        const int e = top ? exponent_of(top) : 127;
+        const float up = as_float((uint32_t)(127 + 22 + 127 - e) << 23);
         mul = finite ? __builtin_amdgcn_frexp_mantf(scale) : __builtin_nanf("");
-        exponent = __builtin_amdgcn_frexp_expf(scale) + e - 127 - 21 - (small ? 64 : 0);
+        exponent = __builtin_amdgcn_frexp_expf(scale) + e - 127 - 22 - (small ? 64 : 0);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
 #pragma unroll
@@ -102,11 +109,8 @@ template <typename T, int D> struct QueryRow {
                 uint32_t n[4], d[3];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // (one that would round to 2^22 stays one below; n as the bits of
-                    // 2^23 + 2^22 + n less those of n = 0)
                     const float v = finite ? at(j, 4 * k + i) * lift * up : 0.0f;
-                    n[i] = as_bits(__builtin_amdgcn_fmed3f(v, -4194303.0f, 4194303.0f) + 12582912.0f) +
-                           (0x8080u - 0x4B400000u);
+                    n[i] = (uint32_t)(int)__builtin_rintf(v) + 0x8080u;
                 }
                 digits_of(n, d);
 #pragma unroll
@@ -122,16 +126,17 @@ __device__ __forceinline__ float score_step(float key_scale, float mul, int expo
     return __builtin_amdgcn_ldexpf(key_scale, exponent) * mul;
 }
 
-// Weights times value scales as numbers below 2^22: times `up`, 2^(21 - exponent of the
-// largest) a touch less so that none rounds up to 2^22, plus 2^23 + 0x8080, whose bytes
-// are the digits; `down` takes their sums back (NaN where one was not finite).
+// Weights times value scales as whole numbers below 2^23: times `up`, 2^22 over the largest's
+// power of two, plus 2^23 + 0x8080, whose bytes are the digits; `down` takes their sums back
+// (NaN where one was not finite). (Of 22 bits, and queries as well, float32 outputs were off
+// by 4.9e-7 of their size, where the float32 formula is by 2.8e-7.)
 constexpr float kDigits = 8388608.0f + 32896.0f;
 __device__ __forceinline__ void weight_steps(uint32_t most, float &up, float &down) {
     const bool finite = most < 0x7F800000u;
-    int e = (int)(most >> 23);
+    int e = exponent_of(most);
     e = e < 24 ? 24 : e;
-    up = as_float((uint32_t)(127 + 21 + 127 - e) << 23) * (1.0f - 0x1p-21f);
-    down = finite ? as_float((uint32_t)(e - 21) << 23) * (1.0f + 0x1p-21f) : __builtin_nanf("");
+    up = as_float((uint32_t)(127 + 22 + 127 - e) << 23);
+    down = finite ? as_float((uint32_t)(e - 22) << 23) : __builtin_nanf("");
 }
 
 // A wave's tile. s_keys, s_values: its places in LDS, kKeys rows of D codes, 16-byte

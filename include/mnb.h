@@ -640,13 +640,13 @@ int mnb_kv_read_i8(const int64_t *slots, int64_t T, const mnb_kv_cache_i8 *cache
  * max_len and max_new.
  *
  * Scores, softmax statistics and sums over keys are float32. Queries count as
- * 22-bit numbers against their row's largest, weights times value scales as
- * 22-bit numbers against the largest of 64 keys (or 2^-103, where that is
- * less). float16 calls of 33 query rows and more a key-value head (max_new * Hq
- * / Hkv) hold them against the row's own largest so far instead, as two float16
- * numbers, 22 bits, of weights that may be off by 2^-16 of themselves, or by
- * half a float32 step of their scores; what is below 2^-31 of a row's largest
- * may count as zero there.
+ * whole numbers below 2^23 against their row's largest, weights times value
+ * scales as such numbers against the largest of 64 keys (or 2^-103, where that
+ * is less). float16 calls of 33 query rows and more a key-value head (max_new *
+ * Hq / Hkv) hold these against the row's own largest so far instead, as two
+ * float16 numbers, 22 bits, of weights that may be off by 2^-16 of themselves,
+ * or by half a float32 step of their scores; what is below 2^-31 of a row's
+ * largest may count as zero there.
  * float16: |scale| above 2^80 counts as 2^80 (products of queries with rows
  * that were appended are zero or above 2^-55, so there is nothing left to tell
  * apart). A query row that holds an infinity or a NaN gives NaN (zeros if it

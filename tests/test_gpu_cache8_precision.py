@@ -116,3 +116,60 @@ def test_equal_scores_of_different_steps_cancel(new, rise, size):
                 tol += 100 * 64 * 2 * np.exp(-12.0) / (n - 128) * (size * 2.0 ** -22 if size > 100 else 2.0 ** -16)
             worst = (np.abs(got[t] - ref) / tol).max()
             assert worst <= 1.0, (sign, t, worst)
+
+
+# Half a step of the whole numbers that stand for a row's queries, and for a tile's weights times value scales, to
+# the largest of them: numbers below 2^23 (the largest at 0.99 2^22 or more).
+HALF_STEP = 2.0 ** -23 / 0.99
+
+
+@pytest.mark.parametrize("heads", [1, 4, 8, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_float32_weights_times_value_scales(dim, heads):
+    # two keys of one score and nearly one value scale, codes of 100 and -100: the result is the difference of the
+    # scales; each product may be off by half a step of the larger one's, the sum, its factor and the
+    # division by a few roundings of the small result
+    B = 2048
+    g = torch.Generator(DEV).manual_seed(dim + heads)
+    cache = _cache(B, 1, 16, dim, "f32", code=0, scale=0.0)
+    cache.v[:, 0, 0], cache.v[:, 0, 1] = 100, -100
+    first = 2.0 ** (20 * torch.rand((B,), device=DEV, generator=g).double() - 10)
+    second = first * (1 - 2.0 ** -12 * torch.rand((B,), device=DEV, generator=g).double())
+    cache.v_scale[:, 0, 0], cache.v_scale[:, 0, 1] = first.float(), second.float()
+    q = torch.randn((B, heads, dim), device=DEV, generator=g)
+    got = mnb.mnb_paged_attn_i8(q, cache, torch.arange(B, **I32)[:, None].contiguous(), torch.full((B,), 2, **I32), 2)
+    first, second = cache.v_scale[:, 0, 0].double(), cache.v_scale[:, 0, 1].double()
+    want = 50 * (first - second)
+    tol = 100 * first * HALF_STEP + want.abs() * 2.0 ** -20
+    worst = ((got.double() - want[:, None, None]).abs() / tol[:, None, None]).max()
+    assert worst <= 1, float(worst)
+
+
+@pytest.mark.parametrize("heads", [1, 4, 8, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_float32_queries(dim, heads):
+    # rows of one large element, which meets codes of zero, and of small equal ones, which all are off alike:
+    # a key of score about one and one of score zero, of values 100 and -100
+    B = 2048
+    u = 2.0 ** -24
+    g = torch.Generator(DEV).manual_seed(dim + heads)
+    cache = _cache(B, 1, 16, dim, "f32", code=0, scale=0.0)
+    cache.k[:, 0, 0, 1:] = 127
+    cache.k_scale[:, 0, :2] = 1.0
+    cache.v[:, 0, 0], cache.v[:, 0, 1] = 100, -100
+    cache.v_scale[:, 0, :2] = 1.0
+    top = 1 + torch.rand((B, heads), device=DEV, generator=g)
+    small = (2.0 ** -7 * (1 + torch.rand((B, heads), device=DEV, generator=g)))
+    q = small[..., None].repeat(1, 1, dim)
+    q[..., 0] = top
+    scale = float(np.float32(2.0 ** 6 / (127 * dim)))
+    got = mnb.mnb_paged_attn_i8(q, cache, torch.arange(B, **I32)[:, None].contiguous(), torch.full((B,), 2, **I32), 2,
+                                scale=scale)
+    s = small.double() * (dim - 1) * 127 * scale
+    want = 100 * torch.tanh(s / 2)
+    # the score moves the result by 50 times as much at most; off by the queries' half steps and float32's
+    # roundings; the weights (2^-21 for the exponential, half a step) in numerator and denominator
+    off = (dim - 1) * 127 * scale * top.double() * HALF_STEP + (dim + 8) * u * s
+    tol = 50 * off + 200 * (2.0 ** -21 + HALF_STEP) + want * 8 * u
+    worst = ((got.double() - want[..., None]).abs() / tol[..., None]).max()
+    assert worst <= 1, float(worst)

@@ -59,7 +59,8 @@ def test_large_value_scales_of_little_weight(exponent, new):
 @pytest.mark.parametrize("new", [None, [3], [40]], ids=str)
 @pytest.mark.parametrize("size,keys_size,scale", [
     (2e-38, 1e38, 0.5), (1e-36, 1e34, 3.0), (3e-34, 1e36, 1 / 300), (3e-39, 1e38, 3.0), (1e38, 1e-41, 1 / 300),
-    (1e-30, 1e-10, 1e38), (1e-42, 1e4, 3e38), (3e37, 1e-10, 1e-27)])
+    (1e-30, 1e-10, 1e38), (1e-42, 1e4, 3e38), (3e37, 1e-10, 1e-27),
+    (3.4e38, 3e-38, 1 / 30), (3.4e38, 1e-10, 1e-28)])
 def test_float32_products_of_far_sizes(size, keys_size, scale, new):
     # queries and keys whose products are ordinary numbers
     q, cache, table, ln, starts = _case(73, [90], 2, 1, 64, 16, "f32", new=new)
