@@ -12,13 +12,16 @@ constexpr int kMostPairs = 512;
 constexpr int kAhead = 4;
 
 // gain * (cos, sin) of position * freq radians. The fraction of a turn is taken in
-// float64: of a float32 angle of 10^5 turns nothing would be left below 2^-7.
+// float64: of a float32 angle of 10^5 turns nothing would be left below 2^-7. Its first
+// 24 bits give the cosine and sine, which are turned on by the rest (up to 2 pi 2^-26
+// radians, as much as the rounding of a number near one).
 __device__ __forceinline__ float2 turn_of(int position, double freq, float gain) {
     const double turns = (double)position * freq * 0.15915494309189535;
-    const float part = (float)(turns - __builtin_rint(turns));   // -0.5 .. 0.5
+    const double fraction = turns - __builtin_rint(turns);   // -0.5 .. 0.5
+    const float part = (float)fraction, rest = 6.2831853f * (float)(fraction - (double)part);
     float s, c;
     sincospif(2.0f * part, &s, &c);
-    return float2{gain * c, gain * s};
+    return float2{gain * __builtin_fmaf(-s, rest, c), gain * __builtin_fmaf(c, rest, s)};
 }
 
 // A float32 result rounded to T. (Hidden from the compiler, which would fold some of the
