@@ -75,10 +75,6 @@ struct Attn8Split {
     float *sums, *stats;
 };
 
-// Joins the chunks' pieces. LOG2: their maxima are of scores times log2(e).
-hipError_t launch_attn8_join(const Attn8Args &a, const Attn8Split &sp, int head_dim, int dtype, bool log2,
-                             hipStream_t st);
-
 // The same sums for up to kFewRows query rows of a (request, key-value head)
 // (mnb_attn8_few.hip).
 constexpr int kFewRows = 5;

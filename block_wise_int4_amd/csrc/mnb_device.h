@@ -121,17 +121,6 @@ __host__ __device__ __forceinline__ uint16_t f64_to_f16_bits(double d) {
     return sign | (uint16_t)bits;
 }
 
-// float32 product q * s rounded to odd: of an int8 q, the float16 conversion that
-// follows then rounds the exact product once.
-__device__ __forceinline__ float mul_round_odd(float q, float s) {
-    const float p = q * s;
-    if (p == 0.0f || __builtin_isinf(p)) return p;  // (a float16 zero or infinity either way)
-    const float e = __builtin_fmaf(q, s, -p);  // q * s - p, exact
-    uint32_t u = __builtin_bit_cast(uint32_t, p);
-    if (e != 0.0f && (u & 1u) == 0u) u += ((e > 0.0f) == (p > 0.0f)) ? 1u : 0xFFFFFFFFu;
-    return __builtin_bit_cast(float, u);
-}
-
 // Between LDS accesses of some lanes of a wave and accesses of others to the same place. The
 // hardware keeps a wave's LDS operations in order; the compiler keeps those of one lane.
 __device__ __forceinline__ void wave_fence() {

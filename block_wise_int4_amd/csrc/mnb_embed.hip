@@ -23,6 +23,16 @@ namespace mnb {
 
 constexpr int kEmbedWaves = 4;
 
+// float32 product q * s rounded to odd.
+__device__ __forceinline__ float mul_round_odd(float q, float s) {
+    const float p = q * s;
+    if (p == 0.0f || __builtin_isinf(p)) return p;  // (a float16 zero or infinity either way)
+    const float e = __builtin_fmaf(q, s, -p);  // q * s - p, exact
+    uint32_t u = __builtin_bit_cast(uint32_t, p);
+    if (e != 0.0f && (u & 1u) == 0u) u += ((e > 0.0f) == (p > 0.0f)) ? 1u : 0xFFFFFFFFu;
+    return __builtin_bit_cast(float, u);
+}
+
 // 16 consecutive entries of one row: table bytes raw (zeros for an invalid
 // id) times the row's scale s, written to dst[0, 16).
 template <typename T>
