@@ -77,7 +77,7 @@ struct Attn8Split {
 
 // The same sums for up to kFewRows query rows of a (request, key-value head)
 // (mnb_attn8_few.hip).
-constexpr int kFewRows = 5;
+constexpr int kFewRows = 2;
 hipError_t launch_attn8_few(const Attn8Args &a, const Attn8Split &sp, int head_dim, int dtype, bool stream,
                             hipStream_t st);
 

@@ -1,6 +1,6 @@
-// Attention of up to five query rows of a (request, key-value head) over the 8-bit
-// cache: the single tokens of a decoding step whose heads share keys in groups of up
-// to five. The same whole numbers as in mnb_attn8.hip, but for the digits' place: here
+// Attention of one or two query rows of a (request, key-value head) over the 8-bit
+// cache: the single tokens of a decoding step whose heads share keys by no more than
+// two. The same whole numbers as in mnb_attn8.hip, but for the digits' place: here
 // a row's three digits are three columns of one product, so that a tile takes a third
 // of the products, and a score belongs to one lane, so that a tile takes a quarter of
 // the vector instructions:
@@ -12,17 +12,18 @@
 //
 // Long rows are bound by memory: 2 rows, 32 x 500..16384 keys of 8 heads of 128, 571 MB in
 // 93..105 us, 5.4..6.1 TB/s (16 x 16 tiles of the other kernel took 116; a stream of reads
-// reaches 6.8). One request of 452 keys takes 7.7 us, of one key 6.6: a launch, the chain
+// reaches 6.8). One request of 452 keys takes 7.7 us, of one key 6.0: a launch, the chain
 // of length, table, codes and scales, two products and the waves' join. Against that form
-// (us replayed from a graph): 1 row, 8 x 1500 keys, 11.3 and 18.1; 2 rows 12.3 and 18.1; 5
-// rows 16.1 and 18.2, 1 x 500 10.1 and 9.4, 32 x 12000 121 and 120.
+// (us replayed from a graph): 1 row, 8 x 1500 keys, 10.5 and 12.5; 2 rows 11.1 and 12.4,
+// 32 x 16000 169 and 175; over 380 calls each 17% and 12% faster in the mean. (Of three to five
+// rows it was 5% to 6% slower: 3 rows, 8 x 2000 keys, 13.7 and 12.8, 5 rows 13.8 and 13.2.)
 #include "mnb_attn8_tiles.h"
 
 namespace mnb {
 
 namespace {
 
-constexpr int kMost = 5;                     // rows
+constexpr int kMost = 2;                     // rows
 constexpr int kColumns = 3 * kMost;
 constexpr int kScoreStride = kKeys + 4;      // of a column of products, in words: columns turned in the banks
 constexpr int kDigitStride = kKeys + 16;     // of a column of digits, in bytes
@@ -299,7 +300,6 @@ namespace {
 template <typename T, int D, bool STREAM, int W> void launch_rows(const Attn8Args &a, const Attn8Split &sp, hipStream_t st) {
     const dim3 grid(a.cache.heads, a.batch, (unsigned)sp.chunks);
     if (sp.rows == 1) attn8_few_kernel<T, D, STREAM, 1, W><<<grid, 64 * W, 0, st>>>(a, sp);
-    else if (sp.rows == 2) attn8_few_kernel<T, D, STREAM, 2, W><<<grid, 64 * W, 0, st>>>(a, sp);
     else attn8_few_kernel<T, D, STREAM, kMost, W><<<grid, 64 * W, 0, st>>>(a, sp);
 }
 

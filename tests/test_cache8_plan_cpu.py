@@ -18,7 +18,7 @@ def _longest(B, heads, kv_heads, dim):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("group", [1, 5, 8, 16])
+@pytest.mark.parametrize("group", [1, 2, 3, 8, 16])
 def test_the_longest_whole_row_grows_with_the_requests(group, dim):
     longest = [_longest(B, group, 1, dim) for B in range(1, 400)]
     assert all(a <= b for a, b in zip(longest, longest[1:]))

@@ -80,7 +80,7 @@ def _check(name, lines):
         assert loads(since) + loads(loop[:second]) >= later, f"{name}: values"
 
 
-@pytest.mark.parametrize("source,kernels", [("mnb_attn8.hip", 8), ("mnb_attn8_few.hip", 48)])
+@pytest.mark.parametrize("source,kernels", [("mnb_attn8.hip", 8), ("mnb_attn8_few.hip", 32)])
 def test_waits_are_for_loads_that_came_before(source, kernels, tmp_path):
     found = list(_kernels(source, tmp_path))
     assert len(found) == kernels
