@@ -25,8 +25,10 @@
 //
 // Bound by the latency of a tile's steps (two products, their exchange and the softmax
 // between) where workgroups are few, by the vector unit and the codes' way through LDS where
-// they are many: 16 rows over 32 x 1000 keys of 8 heads of 128 16.8 us, 4.0 TB/s of codes
-// and scales, 8 rows over 32 x 8000 112 us, 4.8 TB/s (a stream of reads reaches 6.8).
+// they are many: 16 rows over 32 x 1000 keys of 8 heads of 128 16.4 us, 4.1 TB/s of codes
+// and scales, 8 rows over 32 x 8000 111 us, 4.9 TB/s (a stream of reads reaches 6.8). Many
+// float32 rows are taken 16 at a time as well, each tile with codes of its own: 16 prompts of
+// 410 rows, 16 heads of 128 over 8, 119 us, 8 x 62 rows after up to 2000 keys 36.
 #include "mnb_attn8_tiles.h"
 
 #include <algorithm>
@@ -345,12 +347,16 @@ struct Plan {
 // with 128 11.1; 1 x 16000 with 512 13.1 for 11.8).
 //
 // Many rows: from kManyRows on, three tiles of this file's kernel, which the other form
-// takes as one: 40 rows and 64 x 300 keys 22 and 34, 8 x 8000 53 and 61; below, 32 rows and
-// 32 x 1000 33 and 22. (Calls of few workgroups go on losing by it up to some 100 rows: 8 x
-// 500 keys, 64 rows, 15.6 and 12.6.) kManyWgs workgroups of kManyKeys keys or more (8 x
-// 8000 keys, 124 rows: 56, with 256 68), and where those are too few kFullWgs of
-// kLeastKeys or more (1 x 2000, 124 rows: 15.0, in pieces of 256 17.2; 1 x 410 new 14.6
-// and 16.8); up to kManyKeys keys are one piece (2 x 200 new 12.6, in two 13.3).
+// takes as one: 64 requests of 40 rows after 300 keys 26 and 37, of 64 rows 30 and 49; 32
+// rows 25 and 28, but 32 of those after 1000 keys 39 and 25. (The border moves with the work:
+// calls of few workgroups go on losing by the other form up to some 100 rows, 8 x 500 keys
+// 64 rows 17.7 and 12.9. By the tiles of 16 rows, all requests and heads together, times
+// max_len head_dim / 128 + 500, above half a million, 5814 calls of 20..410 rows would be
+// 2% behind the better form in the mean, by the constant they are 11%.) kManyWgs workgroups
+// of kManyKeys keys or more (8 x 8000 keys, 124 rows: 74, with 256 85, with 1024 76), and
+// where those are too few kFullWgs of kLeastKeys or more (1 x 2000, 124 rows: 15.6, in
+// pieces of 256 18.9; 1 x 410 new 15.7 and 18.7); up to kManyKeys keys are one piece (2 x 200
+// new 14.0, in two 14.6).
 constexpr int64_t kCus = 256, kJoinBytes = 128 << 10, kTileJoinBytes = 48 << 10, kFullBytes = 1 << 20, kMany = 2048,
                   kLeast = 768, kManyWgs = 512, kManyKeys = 256, kFullWgs = 256, kLeastKeys = 128, kManyRows = 33;
 

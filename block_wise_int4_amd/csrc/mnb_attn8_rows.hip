@@ -26,15 +26,15 @@
 // weight; it comes with the exponentials, whose arguments it makes up to 2^6 larger (2^-18 of
 // a weight). The weights' sum, the denominator, is float32.
 //
-// 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 25 us: 4.4 GFLOP, 39 MB. Half of
-// that is the loop, bound by vector instructions (400 a wave and step, exponentials counted
-// as four, against 1024 cycles of matrix products), 13 steps in the fullest CU where the
-// mean is 6; a launch and a step take 8. 8 x 62 rows after up to 2000 keys take 23 and
-// the join 6: some 200 workgroups of five steps, 2 us each where a CU has one (4800 cycles,
-// of which 1024 are matrix and 1600 vector instructions: latency). 64 keys a step: with 32
-// these took 34 and 35 us. Two teams of four waves on alternate steps, joined in LDS, were
-// 1 to 2.5 us slower in calls of few workgroups and 15% faster in those that fill every CU
-// once with whole rows.
+// 16 prompts of 62..410 rows, 16 heads of 128 over 8, take 27 us: 4.4 GFLOP, 39 MB. Half of
+// that is the loop, bound by vector instructions (470 a wave and step, exponentials counted
+// as four, against 1536 cycles of matrix products), 13 steps in the fullest CU where the
+// mean is 6; a launch and a step take 8. 8 x 62 rows after up to 2000 keys take 25 and
+// the join 6: some 200 workgroups of five steps, over 2 us each where a CU has one (5500
+// cycles, of which 1536 are matrix and 1900 vector instructions: latency). With 32 keys a step,
+// terms of 11 bits, these took 34 and 35 us (24 and 23 with 64). Two teams of four waves on
+// alternate steps, joined in LDS, were 1 to 2.5 us slower in calls of few workgroups and 15%
+// faster in those that fill every CU once with whole rows.
 #include "mnb_attn8.h"
 
 namespace mnb {

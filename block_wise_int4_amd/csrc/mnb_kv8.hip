@@ -1,9 +1,11 @@
 // The 8-bit key-value cache: tokens quantized as they are written, and slots
 // read back as the numbers they stand for. 26240 float16 tokens of 8 x 128 (164 MB
-// either way) are appended in 40 us, 4.1 TB/s, near what the vector instructions take (850
-// a wave for 16 rows of 128: half of them a row's place and scale, the rest conversions
-// and exact quotients), and read back in 28, 5.9 TB/s, codes mostly from the last-level
-// cache; 8 tokens take 3.1 and 2.6, a launch.
+// either way), appended and read back, three sets of tensors in turn: 44..46 us on the
+// device, 3.6 TB/s, and 28, 5.9 TB/s, codes mostly from the last-level cache. Appends
+// alone take 41, of the same tokens again and again, which that cache holds, 37: about what
+// the vector instructions take (850 a wave for 16 rows of 128, half of them a row's place
+// and scale, the rest conversions and exact quotients: 88 thousand cycles a SIMD). 13120
+// float32 tokens (135 MB) alone: 33 and, read back, 32. 8 tokens take 3.1 and 2.6, a launch.
 #include "mnb_cache8.h"
 #include "mnb_device.h"
 
@@ -242,9 +244,9 @@ __global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Args a, int per, 
 namespace {
 
 // Tokens per workgroup: rows for its lanes, kAhead times where 1024 workgroups are left
-// by that. Float16 tokens of 8 x 128, with and without, us replayed from a graph: 4096
-// appended 9.6 and 10.1, read back 7.5 and 8.6, 26240 35.4 and 41.4, 27.1 and 34.4; but
-// 1024 6.3 and 4.7, 4.4 and 4.4.
+// by that. The same float16 tokens of 8 x 128 again, with and without, us replayed from a
+// graph: 4096 appended 9.6 and 10.1, read back 7.5 and 8.6, 26240 35.4..36.6 and 41.4, 27.1
+// and 34.4; but 1024 6.3 and 4.7, 4.4 and 4.4.
 template <typename T, int D, bool APPEND> hipError_t launch(const Kv8Args &a, hipStream_t st) {
     constexpr int lanes = APPEND ? D / kPart : D * (int)sizeof(T) / 16, rows = kThreads / lanes;
     const int64_t each = 2 * (int64_t)a.cache.heads;
